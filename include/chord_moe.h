@@ -53,6 +53,9 @@ enum chord_status {
   CHORD_ERR_ROUTING_INVALID = -7    /* an expert id out of range (device status) */
 };
 
+/* Element types of the row operators and of MXFP4 quantisation. */
+enum chord_dtype { CHORD_DTYPE_BF16 = 0, CHORD_DTYPE_FP16 = 1, CHORD_DTYPE_FP32 = 2 };
+
 /* GEMM epilogues. */
 enum chord_epilogue {
   CHORD_EPI_STORE = 0,        /* C[r, n] = bf16(acc[r, n]) */
@@ -393,6 +396,103 @@ int chord_moe_layer(const chord_bf16* x, const float* logits, const float* bias,
                     int E_total, int expert_begin, int E_local, int topk, chord_bf16* out,
                     float* topk_weights_out, int32_t* topk_ids_out, void* workspace,
                     size_t ws_bytes, const chord_tuning* tuning, int* dev_status, void* stream);
+
+/* ------------------------------------- token rows in expert order, and back
+ * The rows of the aligned order that chord_moe_align writes, for callers that
+ * run the experts themselves, with the gradients that training needs.  With
+ * p(t, j) = sorted_positions[t*topk + j] (a row below `capacity`, or negative
+ * when the expert of assignment (t, j) is not local):
+ *   permute             out[p(t,j)] = x[t]; padding rows become zeros
+ *   permute_backward    dx[t] = sum_j dout[p(t,j)]
+ *   unpermute           out[t] = sum_j topk_weights[t,j] * y[p(t,j)]
+ *   unpermute_backward  dy[p(t,j)] = topk_weights[t,j] * dout[t], padding rows
+ *                       become zeros; dweights[t,j] = <dout[t], y[p(t,j)]>
+ * A token without a local expert gets zeros (dweights too).  Rows at or past
+ * num_tokens_post_padded are not written, and no padding row is read, so
+ * what padding rows of dout and y hold (also NaN) reaches no result.
+ *   dtype     chord_dtype of all row matrices of the call; sums are FP32 in
+ *             increasing j (dweights: FP32), rounded once
+ *   *_stride  row strides in elements; rows that are read may overlap
+ *             (stride 0: one row for all), rows that are written may not
+ *   H         any length; 16-byte accesses where bases, strides and H allow
+ *   sorted_token_ids, num_tokens_post_padded, sorted_positions
+ *             as chord_moe_align writes them for this M, topk and capacity
+ * topk <= 32.  Results are the same from call to call (no atomics).
+ */
+int chord_moe_permute(const void* x, int dtype, int64_t x_stride, const int32_t* sorted_positions,
+                      const int32_t* sorted_token_ids, const int32_t* num_tokens_post_padded, int M, int topk,
+                      int H, size_t capacity, void* out, int64_t out_stride, void* stream);
+int chord_moe_permute_backward(const void* dout, int dtype, int64_t dout_stride, const int32_t* sorted_positions,
+                               int M, int topk, int H, size_t capacity, void* dx, int64_t dx_stride, void* stream);
+int chord_moe_unpermute(const void* y, int dtype, int64_t y_stride, const float* topk_weights,
+                        const int32_t* sorted_positions, int M, int topk, int H, size_t capacity, void* out,
+                        int64_t out_stride, void* stream);
+int chord_moe_unpermute_backward(const void* dout, const void* y, int dtype, int64_t dout_stride, int64_t y_stride,
+                                 const float* topk_weights, const int32_t* sorted_positions,
+                                 const int32_t* sorted_token_ids, const int32_t* num_tokens_post_padded, int M,
+                                 int topk, int H, size_t capacity, void* dy, int64_t dy_stride, float* dweights,
+                                 void* stream);
+
+/* ------------------------------------------------------------------- MXFP4
+ * Microscaled 4-bit floating point (OCP Microscaling Formats v1.0, MXFP4):
+ * 32 consecutive values of a row share a scale 2^(s - 127) (E8M0, one byte),
+ * each value is an E2M1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), two to
+ * a byte, low nibble = even k.
+ *   quantize    s = floor(log2(amax)) - 2 + 127, at least 0; code =
+ *               x / scale rounded to the nearest E2M1 value, ties to the even
+ *               code, magnitudes above 6 become 6.  A block that holds an
+ *               infinity or a NaN gets s = 255 and codes 0, and reads as NaN.
+ *               x [rows, K] of `dtype`, codes [rows, K/2], scales [rows, K/32]
+ *   dequantize  the inverse: out [rows, K] of `dtype`, rounded once
+ * K % 32 == 0; codes 16-byte aligned.
+ */
+int chord_mxfp4_quantize(const void* x, int dtype, int64_t x_stride, int64_t rows, int K, uint8_t* codes,
+                         uint8_t* scales, void* stream);
+int chord_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, void* out, int dtype,
+                           int64_t out_stride, void* stream);
+
+/* The experts' product with both operands in MXFP4 (tcgen05 block-scaled
+ * MMA): for every expert e and each of its expert_counts[e] rows r from
+ * expert_offsets[e] on (the aligned order of chord_moe_align)
+ *   acc[n]  = sum_k A[r, k] * W[e, n, k]     (FP32 accumulate)
+ *   C[r, n] = bf16(acc[n])                                CHORD_EPI_STORE
+ *   C[r, i] = bf16(silu(acc[i]) * acc[N/2 + i])           CHORD_EPI_SILU_MUL
+ * Padding rows of C are not written.
+ *   prepack        codes [E, N, K/2] and scales [E, N, K/32] as `quantize`
+ *                  writes them -> the kernel's layout, with a 256-byte header
+ *                  that the product checks on the device; done once.
+ *                  gate_up as for chord_w4a16_prepack (rows 0..N/2-1 gate,
+ *                  N/2..N-1 up).  K % 32 == 0, N % 8 == 0 (gate_up: N % 16);
+ *                  N is padded to 128 and K to 256 with zeros.
+ *   quantize_rows  token rows x [M, K] quantised straight into the product's
+ *                  row operand: token t to its rows sorted_positions[t, :]
+ *                  (each token is quantised once), or, with sorted_positions
+ *                  NULL, row r of x to row r for r < num_tokens_post_padded
+ *                  (a previous product's C).  `rows` holds
+ *                  chord_mxfp4_rows_bytes(capacity, K) bytes, 16-byte aligned;
+ *                  num_tokens_post_padded may be NULL with positions.
+ *   workspace      chord_mxfp4_moe_gemm_workspace_bytes() bytes, 16-byte
+ *                  aligned, zeroed once when allocated; every call leaves its
+ *                  counters zero.  Calls that may overlap need their own.
+ *                  After a call that recorded CHORD_ERR_TIMEOUT zero it again.
+ *   dev_status     device int for errors found on the device (may be NULL):
+ *                  a weights header that does not match the call, counts and
+ *                  offsets that are no aligned order of `capacity` rows (such
+ *                  an expert is skipped), a bounded wait that ran out
+ * Counts are read on the device, so the call never waits for the host.
+ * Results are the same from call to call.  E_local <= 1024.
+ */
+size_t chord_mxfp4_rows_bytes(size_t capacity, int K);
+int chord_mxfp4_quantize_rows(const void* x, int dtype, int64_t x_stride, int M, int K,
+                              const int32_t* sorted_positions, int topk, const int32_t* num_tokens_post_padded,
+                              size_t capacity, void* rows, size_t rows_bytes, void* stream);
+size_t chord_mxfp4_prepack_bytes(int E, int N, int K);
+int chord_mxfp4_prepack(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, int gate_up, void* packed,
+                        size_t packed_bytes, void* stream);
+size_t chord_mxfp4_moe_gemm_workspace_bytes(void);
+int chord_mxfp4_moe_gemm(const void* rows, size_t rows_bytes, const void* packed_w, int E_local, int N, int K,
+                         const int32_t* expert_counts, const int32_t* expert_offsets, size_t capacity, int epilogue,
+                         chord_bf16* C, void* workspace, size_t ws_bytes, int* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -28,6 +28,8 @@ CHORD_EPI_STORE = 0
 CHORD_EPI_SILU_MUL = 1
 CHORD_EPI_WEIGHTED_ADD = 2
 
+CHORD_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
 CHORD_PATH_AUTO = 0
 CHORD_PATH_SMALL_M = 1
 CHORD_PATH_LARGE_M = 2
@@ -47,6 +49,7 @@ class chord_tuning(ctypes.Structure):
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
+_L = ctypes.c_int64
 _SIGS = {
     "chord_last_error_string": (ctypes.c_char_p, []),
     "chord_version": (_I, []),
@@ -74,6 +77,18 @@ _SIGS = {
     "chord_moe_layer_plan": (_I, [_I, _I, _I, _P]),
     "chord_moe_layer": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z,
                              _P, _P, _P]),
+    "chord_moe_permute": (_I, [_P, _I, _L, _P, _P, _P, _I, _I, _I, _Z, _P, _L, _P]),
+    "chord_moe_permute_backward": (_I, [_P, _I, _L, _P, _I, _I, _I, _Z, _P, _L, _P]),
+    "chord_moe_unpermute": (_I, [_P, _I, _L, _P, _P, _I, _I, _I, _Z, _P, _L, _P]),
+    "chord_moe_unpermute_backward": (_I, [_P, _P, _I, _L, _L, _P, _P, _P, _P, _I, _I, _I, _Z, _P, _L, _P, _P]),
+    "chord_mxfp4_quantize": (_I, [_P, _I, _L, _L, _I, _P, _P, _P]),
+    "chord_mxfp4_dequantize": (_I, [_P, _P, _L, _I, _P, _I, _L, _P]),
+    "chord_mxfp4_rows_bytes": (_Z, [_Z, _I]),
+    "chord_mxfp4_quantize_rows": (_I, [_P, _I, _L, _I, _I, _P, _I, _P, _Z, _P, _Z, _P]),
+    "chord_mxfp4_prepack_bytes": (_Z, [_I, _I, _I]),
+    "chord_mxfp4_prepack": (_I, [_P, _P, _I, _I, _I, _I, _P, _Z, _P]),
+    "chord_mxfp4_moe_gemm_workspace_bytes": (_Z, []),
+    "chord_mxfp4_moe_gemm": (_I, [_P, _Z, _P, _I, _I, _I, _P, _P, _Z, _I, _P, _P, _Z, _P, _P]),
 }
 
 _lib = None
@@ -351,4 +366,148 @@ def chord_moe_layer(x, logits, bias, w13_packed, w2_packed, H: int, I: int, E_to
         _ptr(topk_weights_out, torch.float32, "topk_weights_out"),
         _ptr(topk_ids_out, torch.int32, "topk_ids_out"), _ptr(workspace, torch.uint8, "workspace"),
         workspace.numel(), tun[0] if tun else None, _ptr(dev_status, torch.int32, "dev_status"),
+        _stream(stream)))
+
+
+# ------------------------------------------- rows in expert order, and MXFP4
+def _rows(t, name, cols=None, rows=None, dtype=None):
+    """A 2-D CUDA tensor of rows with unit column stride: (pointer, dtype code, row stride).
+    A row length (cols) or row count (rows) that does not match is an error."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in CHORD_DTYPE or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix of rows with unit column stride")
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError(f"{name}'s rows hold {t.shape[1]} values, need {cols}")
+    if rows is not None and t.shape[0] != rows:
+        raise ValueError(f"{name} has {t.shape[0]} rows, need {rows}")
+    # a single row's stride is arbitrary in torch
+    return t.data_ptr(), CHORD_DTYPE[t.dtype], t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _count(t, n, name, dtype=torch.int32):
+    """A contiguous CUDA tensor of n values of `dtype`."""
+    p = _ptr(t, dtype, name)
+    if p is None or t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values")
+    return p
+
+
+def chord_moe_permute(x, sorted_positions, sorted_token_ids, num_tokens_post_padded, topk: int, out, stream=None):
+    """out[p(t, j)] = x[t] for every local assignment; padding rows become zeros.
+    x [M, H], out [capacity, H] of one type (BF16, FP16, FP32), any row strides."""
+    px, dt, lx = _rows(x, "x")
+    M, H = x.shape
+    po, _, lo = _rows(out, "out", H, None, x.dtype)
+    _check(lib().chord_moe_permute(px, dt, lx, _count(sorted_positions, M * topk, "sorted_positions"),
+                                   _count(sorted_token_ids, out.shape[0], "sorted_token_ids"),
+                                   _count(num_tokens_post_padded, 1, "num_tokens_post_padded"), M, topk, H,
+                                   out.shape[0], po, lo, _stream(stream)))
+
+
+def chord_moe_permute_backward(dout, sorted_positions, topk: int, dx, stream=None):
+    """dx[t] = sum over the local assignments of dout[p(t, j)].  dout [capacity, H], dx [M, H]."""
+    pd, dt, ld = _rows(dout, "dout")
+    M, H = dx.shape
+    px, _, lx = _rows(dx, "dx", dout.shape[1], None, dout.dtype)
+    _check(lib().chord_moe_permute_backward(pd, dt, ld, _count(sorted_positions, M * topk, "sorted_positions"), M,
+                                            topk, H, dout.shape[0], px, lx, _stream(stream)))
+
+
+def chord_moe_unpermute(y, topk_weights, sorted_positions, out, stream=None):
+    """out[t] = sum over the local assignments of topk_weights[t, j] * y[p(t, j)].
+    y [capacity, H], topk_weights FP32 [M, topk], out [M, H]."""
+    py, dt, ly = _rows(y, "y")
+    M, k = topk_weights.shape
+    po, _, lo = _rows(out, "out", y.shape[1], M, y.dtype)
+    _check(lib().chord_moe_unpermute(py, dt, ly, _ptr(topk_weights, torch.float32, "topk_weights"),
+                                     _count(sorted_positions, M * k, "sorted_positions"), M, k, y.shape[1],
+                                     y.shape[0], po, lo, _stream(stream)))
+
+
+def chord_moe_unpermute_backward(dout, y, topk_weights, sorted_positions, sorted_token_ids, num_tokens_post_padded,
+                                 dy, dweights, stream=None):
+    """dy[p(t, j)] = topk_weights[t, j] * dout[t], padding rows zeros; dweights[t, j] = <dout[t], y[p(t, j)]>."""
+    M, k = topk_weights.shape
+    pd, dt, ld = _rows(dout, "dout", None, M)
+    H = dout.shape[1]
+    py, _, ly = _rows(y, "y", H, None, dout.dtype)
+    cap = y.shape[0]
+    po, _, lo = _rows(dy, "dy", H, cap, dout.dtype)
+    _check(lib().chord_moe_unpermute_backward(
+        pd, py, dt, ld, ly, _ptr(topk_weights, torch.float32, "topk_weights"),
+        _count(sorted_positions, M * k, "sorted_positions"), _count(sorted_token_ids, cap, "sorted_token_ids"),
+        _count(num_tokens_post_padded, 1, "num_tokens_post_padded"), M, k, H, cap, po, lo,
+        _count(dweights, M * k, "dweights", torch.float32), _stream(stream)))
+
+
+def chord_mxfp4_quantize(x, codes, scales, stream=None):
+    """x [rows, K] (BF16, FP16, FP32) -> codes uint8 [rows, K/2], scales uint8 [rows, K/32]."""
+    px, dt, lx = _rows(x, "x")
+    rows, K = x.shape
+    _check(lib().chord_mxfp4_quantize(px, dt, lx, rows, K, _count(codes, rows * K // 2, "codes", torch.uint8),
+                                      _count(scales, rows * K // 32, "scales", torch.uint8), _stream(stream)))
+
+
+def chord_mxfp4_dequantize(codes, scales, out, stream=None):
+    """The values of codes and scales, out [rows, K] (BF16, FP16, FP32)."""
+    po, dt, lo = _rows(out, "out")
+    rows, K = out.shape
+    _check(lib().chord_mxfp4_dequantize(_count(codes, rows * K // 2, "codes", torch.uint8),
+                                        _count(scales, rows * K // 32, "scales", torch.uint8), rows, K, po, dt, lo,
+                                        _stream(stream)))
+
+
+def chord_mxfp4_rows_bytes(capacity: int, K: int) -> int:
+    return lib().chord_mxfp4_rows_bytes(capacity, K)
+
+
+def chord_mxfp4_quantize_rows(x, sorted_positions, topk: int, num_tokens_post_padded, capacity: int, rows,
+                              stream=None):
+    """Token rows x [M, K] quantised into the product's row operand `rows` (uint8,
+    chord_mxfp4_rows_bytes(capacity, K)): token t to its rows sorted_positions[t, :]; with
+    sorted_positions None, row r of x to row r below num_tokens_post_padded (topk unused)."""
+    px, dt, lx = _rows(x, "x")
+    M, K = x.shape
+    pos = None if sorted_positions is None else _count(sorted_positions, M * topk, "sorted_positions")
+    nt = None if num_tokens_post_padded is None else _count(num_tokens_post_padded, 1, "num_tokens_post_padded")
+    _check(lib().chord_mxfp4_quantize_rows(px, dt, lx, M, K, pos, topk, nt, capacity,
+                                           _ptr(rows, torch.uint8, "rows"), rows.numel(), _stream(stream)))
+
+
+def chord_mxfp4_prepack_bytes(E: int, N: int, K: int) -> int:
+    return lib().chord_mxfp4_prepack_bytes(E, N, K)
+
+
+def chord_mxfp4_prepack(codes, scales, gate_up: bool, packed, stream=None):
+    """codes uint8 [E, N, K/2] and scales uint8 [E, N, K/32] -> the product's weight operand."""
+    E, N, K2 = codes.shape
+    _check(lib().chord_mxfp4_prepack(_ptr(codes, torch.uint8, "codes"),
+                                     _count(scales, E * N * K2 // 16, "scales", torch.uint8), E, N, 2 * K2,
+                                     int(gate_up), _ptr(packed, torch.uint8, "packed"), packed.numel(),
+                                     _stream(stream)))
+
+
+def chord_mxfp4_moe_gemm_workspace_bytes() -> int:
+    return lib().chord_mxfp4_moe_gemm_workspace_bytes()
+
+
+def chord_mxfp4_moe_gemm(rows, packed_w, E_local: int, N: int, K: int, expert_counts, expert_offsets, capacity: int,
+                         epilogue: int, C, workspace, dev_status=None, stream=None):
+    """C [capacity, N or N/2] BF16 = the experts' product of the quantised rows; workspace: uint8 tensor of
+    chord_mxfp4_moe_gemm_workspace_bytes() bytes, zeroed once when allocated."""
+    cols = N // 2 if epilogue == CHORD_EPI_SILU_MUL else N
+    if not isinstance(C, torch.Tensor) or C.dtype != torch.bfloat16 or tuple(C.shape) != (capacity, cols):
+        raise ValueError(f"chord_mxfp4_moe_gemm: C must be bfloat16 [{capacity}, {cols}]")
+    if not isinstance(packed_w, torch.Tensor) or packed_w.numel() < chord_mxfp4_prepack_bytes(E_local, N, K):
+        raise ValueError("chord_mxfp4_moe_gemm: packed_w is smaller than E_local, N and K need")
+    _check(lib().chord_mxfp4_moe_gemm(
+        _ptr(rows, torch.uint8, "rows"), rows.numel(), _ptr(packed_w, torch.uint8, "packed_w"), E_local, N, K,
+        _count(expert_counts, E_local, "expert_counts"),
+        _count(expert_offsets, E_local + 1, "expert_offsets"), capacity, epilogue, _ptr(C, None, "C"),
+        _ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"),
         _stream(stream)))

@@ -5,16 +5,14 @@
 #include <cstdio>
 #include <cstring>
 
+#include "api_util.h"
 #include "chord_moe.h"
 #include "common.cuh"
 #include "kernels.h"
 
-namespace {
+namespace chord {
 
-thread_local char g_err[512] = "";
-// Test hook (chord_debug_force_timeout): later small-M GEMM launches
-// withhold their work items from the consumer warps.
-std::atomic<int> g_force_timeout{0};
+static thread_local char g_err[512] = "";
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -28,11 +26,20 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(CHORD_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace chord
+
+using chord::aligned16;
+using chord::cuda_fail;
+using chord::fail;
+using chord::valid_block_m;
+
+namespace {
+
+// Test hook (chord_debug_force_timeout): later small-M GEMM launches
+// withhold their work items from the consumer warps.
+std::atomic<int> g_force_timeout{0};
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-bool valid_block_m(int bm) { return bm == 8 || bm == 16 || bm == 32 || bm == 64 || bm == 128; }
 
 int check_tuning(const chord_tuning* t) {
   if (!t) return CHORD_OK;
@@ -164,7 +171,7 @@ int check_gemm_shapes(int N, int K, int epilogue) {
 
 extern "C" {
 
-const char* chord_last_error_string(void) { return g_err; }
+const char* chord_last_error_string(void) { return chord::g_err; }
 
 int chord_debug_force_timeout(int enable) {
   g_force_timeout.store(enable ? 1 : 0, std::memory_order_relaxed);

@@ -88,4 +88,35 @@ cudaError_t moe_sum_launch(const uint16_t* y, const float* w, const int32_t* pos
                            int H, uint16_t* out, cudaStream_t st, bool pdl = false,
                            int y_rows = 0x7fffffff);
 
+// Token rows into the aligned expert order and back, and their gradients
+// (dtype: chord_dtype; ld*: row strides in elements; rows: rows of the
+// expert order, positions at or past it count as not local).
+cudaError_t moe_permute_launch(const void* x, int dtype, long long ldx, const int32_t* pos, const int32_t* sorted,
+                               const int32_t* ntpp, int M, int topk, int H, int rows, void* out, long long ldo,
+                               cudaStream_t st);
+// w NULL: the plain sum (the permutation's gradient).
+cudaError_t moe_combine_launch(const void* y, int dtype, long long ldy, const float* w, const int32_t* pos, int M,
+                               int topk, int H, int rows, void* out, long long ldo, cudaStream_t st);
+cudaError_t moe_unpermute_backward_launch(const void* dout, const void* y, int dtype, long long ldd, long long ldy,
+                                          const float* w, const int32_t* pos, const int32_t* sorted,
+                                          const int32_t* ntpp, int M, int topk, int H, int rows, void* dy,
+                                          long long ldo, float* dw, cudaStream_t st);
+
+// MXFP4: row-major codes and scales; the product's rows (pos NULL: row r of
+// x is row r of the order); the product's weights; the product.
+cudaError_t mxfp4_quantize_launch(const void* x, int dtype, long long ldx, long long rows, int K, uint8_t* codes,
+                                  uint8_t* scales, cudaStream_t st);
+cudaError_t mxfp4_dequantize_launch(const uint8_t* codes, const uint8_t* scales, long long rows, int K, void* out,
+                                    int dtype, long long ldo, cudaStream_t st);
+size_t mxfp4_rows_bytes(size_t rows, int K);
+cudaError_t mxfp4_quantize_rows_launch(const void* x, int dtype, long long ldx, int M, int K, const int32_t* pos,
+                                       int topk, const int32_t* ntpp, int rows, uint8_t* out, cudaStream_t st);
+size_t mxfp4_prepack_bytes(int E, int N, int K);
+cudaError_t mxfp4_prepack_launch(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, bool gate_up,
+                                 uint8_t* out, cudaStream_t st);
+size_t mxfp4_gemm_workspace_bytes();
+cudaError_t mxfp4_gemm_launch(const uint8_t* rows, const uint8_t* w, int E, int N, int K, const int32_t* counts,
+                              const int32_t* offsets, int capacity, bool gate_up, uint16_t* C, void* ws, int* status,
+                              cudaStream_t st);
+
 }  // namespace chord

@@ -54,6 +54,25 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, MXFP4 inputs (E2M1, K = 64, one
+// E8M0 scale per 32 of K, read from TMEM), FP32 accumulate, one CTA.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+// 512 bytes of shared memory (32 rows of 16 B) -> four TMEM columns, the 32
+// lanes repeated in all four lane quarters: the layout of 128 rows' scales
+// (byte k of column c, lane i = scale k of row 32 c + i).  Executes in order
+// with the tcgen05.mma of the same thread.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
 // Arrive on `bar` once every tcgen05.mma issued so far by this thread completes.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -115,6 +134,21 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr) {
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Descriptor of a scale block for tc_cp_scales: no swizzle, rows of 16 B,
+// 8-row groups 128 B apart.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
+  return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128u >> 4) << 32) |
+         (static_cast<uint64_t>(1u) << 46);
+}
+// Instruction descriptor, kind::mxf4: A and B E2M1 (1 at [7,10) and [10,12)),
+// both K-major, N>>3 at [17,23), scales E8M0 (bit 23), M>>7 at [27,29); the
+// byte pair of a TMEM cell that holds this K = 64 step's scales (0 or 2) at
+// [4,6) for B and [29,31) for A; dense K = 64 (bit 31 zero).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int N, uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (1u << 27) |
+         (sf_id << 29);
 }
 
 // ------------------------------------------------------------ TMA tensor
