@@ -150,8 +150,15 @@ def _check_operands(A, C, K: int, N: int, epilogue: int, a_rows: int, c_rows: in
         raise ValueError(f"{what}: C holds {C.numel()} values, needs {c_rows} rows of {ncols}")
 
 
+# The current stream's handle without building a torch.cuda.Stream object, which
+# takes longer on the host (2.9 us) than the rest of a small call's checks.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -377,24 +384,30 @@ def _rows(t, name, cols=None, rows=None, dtype=None):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in CHORD_DTYPE or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    kind, shape, stride = t.dtype, t.shape, t.stride()
+    code = CHORD_DTYPE.get(kind)
+    if code is None or (dtype is not None and kind != dtype):
+        raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {kind}")
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be a matrix of rows with unit column stride")
-    if cols is not None and t.shape[1] != cols:
-        raise ValueError(f"{name}'s rows hold {t.shape[1]} values, need {cols}")
-    if rows is not None and t.shape[0] != rows:
-        raise ValueError(f"{name} has {t.shape[0]} rows, need {rows}")
-    # a single row's stride is arbitrary in torch
-    return t.data_ptr(), CHORD_DTYPE[t.dtype], t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    n, h = shape
+    if cols is not None and h != cols:
+        raise ValueError(f"{name}'s rows hold {h} values, need {cols}")
+    if rows is not None and n != rows:
+        raise ValueError(f"{name} has {n} rows, need {rows}")
+    # the row stride of a single row means nothing
+    return t.data_ptr(), code, stride[0] if n > 1 else max(stride[0], h)
 
 
 def _count(t, n, name, dtype=torch.int32):
     """A contiguous CUDA tensor of n values of `dtype`."""
-    p = _ptr(t, dtype, name)
-    if p is None or t.numel() != n:
-        raise ValueError(f"{name} must hold {n} values")
-    return p
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} values")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
 
 
 def chord_moe_permute(x, sorted_positions, sorted_token_ids, num_tokens_post_padded, topk: int, out, stream=None):

@@ -35,12 +35,12 @@ inline size_t dtype_bytes(int dtype) {
   return dtype == CHORD_DTYPE_FP32 ? 4 : dtype == CHORD_DTYPE_BF16 || dtype == CHORD_DTYPE_FP16 ? 2 : 0;
 }
 
-// Largest power-of-two access (in bytes, at most 16) to which every row of a
+// Largest power-of-two access (in bytes, at most `most`) to which every row of a
 // [rows, H] matrix with the given row stride (in elements) is aligned and by
 // which its row length divides.
-inline int row_access_bytes(const void* p, long long stride, long long H, size_t elem) {
+inline int row_access_bytes(const void* p, long long stride, long long H, size_t elem, unsigned most = 16) {
   const uintptr_t all = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride * static_cast<long long>(elem)) |
-                        static_cast<uintptr_t>(H * static_cast<long long>(elem)) | 16u;
+                        static_cast<uintptr_t>(H * static_cast<long long>(elem)) | most;
   return static_cast<int>(all & (~all + 1));
 }
 

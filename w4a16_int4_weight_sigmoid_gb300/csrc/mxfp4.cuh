@@ -30,7 +30,7 @@ constexpr int kMxTileBytes = kMxTileRows * kMxRowBytes;       // 16384
 constexpr int kMxTileScaleBytes = kMxTileRows * kMxRowScales; // 1024
 constexpr int kMxUnitBytes = kMxTileBytes + kMxTileScaleBytes;
 // Largest grid of the product (one CTA per SM): sizes its split workspace.
-constexpr int kMxMaxCtas = 192;
+constexpr int kMxMaxCtas = 160;
 constexpr uint32_t kMxMagic = 0x4D344843u;                    // "CH4M"
 constexpr uint32_t kMxVersion = 1u;
 
@@ -57,7 +57,7 @@ __device__ __forceinline__ float mx_inverse_scale(uint32_t code) {
   return __uint_as_float(min(254u, 254u - code) << 23);
 }
 // Eight values as eight E2M1 codes (nearest, ties to even, at most 6).
-__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
   uint32_t r;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -68,6 +68,17 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
       : "=r"(r)
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
+}
+// The inverse: eight codes as FP16 pairs (exact).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t q, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(q));
 }
 
 }  // namespace chord

@@ -2,11 +2,12 @@
 // into the experts' product's operand (with the permutation into expert
 // order), and the weights' repacking.
 //
-// A thread holds 8 consecutive values (one 16-byte load for 16-bit types);
-// four threads hold a block of 32, whose largest magnitude takes two
-// shuffles.  The maximum is taken on the bit patterns of |x| (ordered like
-// the values, infinities and NaNs above all finite ones), and the scale is a
-// power of two, so x / scale and its rounding to E2M1 are exact operations.
+// A thread holds 16 consecutive values (one 32-byte load for 16-bit types);
+// two threads hold a block of 32, whose largest magnitude takes one shuffle.
+// The maximum is taken on the bit patterns of |x| (ordered like the values,
+// infinities and NaNs above all finite ones; 16-bit types two to a register),
+// and the scale is a power of two, so x / scale and its rounding to E2M1 are
+// exact operations.
 #include <algorithm>
 
 #include "common.cuh"
@@ -17,78 +18,121 @@
 namespace chord {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kRun = 16;   // values per thread
 
-// Eight consecutive values as FP32; V elements per access (V divides 8).
-template <typename T, int V>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+// 32 bytes in one access, kept in program order (a programmatic launch reads
+// nothing before its wait).
+__device__ __forceinline__ void ld_32(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// kRun consecutive values as 32-bit words; kWide: 32-byte aligned.
+template <typename T>
+struct Run {
+  static constexpr int kWords = kRun * sizeof(T) / 4;
+  union {
+    uint32_t w[kWords];
+    T e[kRun];
+  };
+};
+template <bool kWide, typename T>
+__device__ __forceinline__ void load_run(const T* p, Run<T>& r) {
+  if (kWide) {
 #pragma unroll
-  for (int i = 0; i < 8 / V; ++i) {
-    const Vec<T, V> x = reinterpret_cast<const Vec<T, V>*>(p)[i];
+    for (int i = 0; i < Run<T>::kWords; i += 8) ld_32(reinterpret_cast<const uint32_t*>(p) + i, r.w + i);
+  } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[i * V + e] = to_f32(x.e[e]);
+    for (int i = 0; i < kRun; ++i) r.e[i] = p[i];
   }
 }
 
-// This thread's 8 codes and the scale code of the block that it shares with
-// the other lanes of its group of four.  All lanes of the warp call it.
-__device__ __forceinline__ uint32_t quantize8(float (&v)[8], uint32_t& scale) {
+// Bits of the largest |x| as FP32.
+__device__ __forceinline__ uint32_t run_max(const Run<float>& r) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  scale = mx_scale_code(m);
-  const float inv = mx_inverse_scale(scale);
+  for (int i = 0; i < kRun; ++i) m = max(m, r.w[i] & 0x7FFFFFFFu);
+  return m;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t run_max(const Run<T>& r) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = scale == 255u ? 0.f : v[i] * inv;
-  return e2m1x8(v);
+  for (int i = 0; i < Run<T>::kWords; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
+  T t;
+  t.v = static_cast<uint16_t>(max(m & 0xFFFFu, m >> 16));
+  return __float_as_uint(to_f32(t));
+}
+
+// This thread's 16 codes and the scale code of the block that it shares with
+// its neighbour lane.  All lanes of the warp call it.
+template <typename T>
+__device__ __forceinline__ uint2 quantize_run(const Run<T>& r, uint32_t& scale) {
+  uint32_t m = run_max(r);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  scale = mx_scale_code(m);
+  const float inv = scale == 255u ? 0.f : mx_inverse_scale(scale);
+  float v[kRun];
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) v[i] = to_f32(r.e[i]) * inv;
+  uint2 q = make_uint2(e2m1x8(v), e2m1x8(v + 8));
+  if (scale == 255u) q = make_uint2(0, 0);   // an infinity or a NaN in the block
+  return q;
 }
 
 // ---------------------------------------------------------------- row-major
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const T* __restrict__ x, long long ldx, long long rows,
-                                                            int K, uint8_t* __restrict__ codes,
+// CTA column: a run of each thread; rows blockIdx.y, + gridDim.y, ...
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const T* x, long long ldx, long long rows, int K,
+                                                            uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
-  const int g = blockIdx.x * kThreads + threadIdx.x;   // group of 8 values of the row
-  const bool in = g < K / 8;
+  const int g = blockIdx.x * kThreads + threadIdx.x;
+  const bool in = g < K / kRun;
   for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
-    float v[8] = {};
-    if (in) load8<T, V>(x + r * ldx + 8 * g, v);
+    Run<T> v = {};
+    if (in) load_run<kWide>(x + r * ldx + kRun * g, v);
     uint32_t scale;
-    const uint32_t q = quantize8(v, scale);
+    const uint2 q = quantize_run(v, scale);
     if (in) {
-      reinterpret_cast<uint32_t*>(codes + r * (K / 2))[g] = q;
-      if ((g & 3) == 0) scales[r * (K / kMxBlock) + g / 4] = static_cast<uint8_t>(scale);
+      reinterpret_cast<uint2*>(codes + r * (K / 2))[g] = q;
+      if ((g & 1) == 0) scales[r * (K / kMxBlock) + g / 2] = static_cast<uint8_t>(scale);
     }
   }
 }
 
-// E2M1 code -> value: an FP32 number whose exponent and mantissa come
-// straight from the three magnitude bits, times 2^126 (subnormal 0.5
-// included), then the block's scale.
-template <typename T, int V>
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __restrict__ codes,
                                                               const uint8_t* __restrict__ scales, long long rows,
                                                               int K, T* __restrict__ out, long long ldo) {
   const int g = blockIdx.x * kThreads + threadIdx.x;
-  if (g >= K / 8) return;
+  if (g >= K / kRun) return;
   for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
-    const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(codes + r * (K / 2)) + g);
-    const uint32_t code = __ldg(scales + r * (K / kMxBlock) + g / 4);
-    const float scale = code == 255u ? __uint_as_float(0x7FC00000u)
-                                     : code == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(code << 23);
-    T* dst = out + r * ldo + 8 * g;
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(codes + r * (K / 2)) + g);
+    const uint32_t code = __ldg(scales + r * (K / kMxBlock) + g / 2);
+    // 2^(code - 127): code 0 is subnormal, 255 is NaN
+    const float scale = __uint_as_float(code == 255u ? 0x7FC00000u : code == 0u ? 0x00400000u : code << 23);
+    uint32_t h[8];
+    e2m1x8_to_f16(q.x, *reinterpret_cast<uint32_t(*)[4]>(h));
+    e2m1x8_to_f16(q.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+    Run<T> o;
 #pragma unroll
-    for (int i = 0; i < 8 / V; ++i) {
-      Vec<T, V> o;
+    for (int i = 0; i < kRun; ++i)
+      from_f32(o.e[i], __half2float(__ushort_as_half(static_cast<uint16_t>(h[i / 2] >> (16 * (i & 1))))) * scale);
+    T* dst = out + r * ldo + kRun * g;
+    if (kWide) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const uint32_t n = (q >> (4 * (i * V + e))) & 15u;
-        const float mag = __uint_as_float((n & 7u) << 22) * __uint_as_float(253u << 23);
-        from_f32(o.e[e], (n & 8u ? -mag : mag) * scale);
-      }
-      reinterpret_cast<Vec<T, V>*>(dst)[i] = o;
+      for (int i = 0; i < Run<T>::kWords; i += 8) st_32(reinterpret_cast<uint32_t*>(dst) + i, o.w + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) dst[i] = o.e[i];
     }
   }
 }
@@ -96,39 +140,45 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __r
 // ------------------------------------------------------- the product's rows
 // Token rows into the operand layout: token t to its rows pos[t, :] (pos
 // given), or row r to row r below the padded total (pos NULL).  Each token
-// is read and quantised once, whatever the number of its experts.  Padding
-// rows are not written: the product computes each row from itself alone and
-// stores no padding row.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* __restrict__ x, long long ldx, int M, int K,
-                                                                 const int32_t* __restrict__ pos, int topk,
-                                                                 const int32_t* __restrict__ ntpp, int rows,
-                                                                 uint8_t* __restrict__ out) {
+// is read and quantised once, whatever the number of its experts; the next
+// token's positions are fetched meanwhile.  Padding rows are not written: the
+// product computes each row from itself alone and stores no padding row.
+// A programmatic launch: the product that follows starts while this ends.
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, long long ldx, int M, int K,
+                                                                 const int32_t* pos, int topk, const int32_t* ntpp,
+                                                                 int rows, uint8_t* __restrict__ out) {
   const int g = blockIdx.x * kThreads + threadIdx.x, lane = threadIdx.x & 31;
   const size_t padded = mx_rows_padded(rows);
   uint8_t* out_scales = out + static_cast<size_t>(mx_units(K)) * padded * kMxRowBytes;
-  const bool in_unit = g < mx_units(K) * (kMxUnitK / 8), in = g < K / 8;
-  const int unit = g / (kMxUnitK / 8), chunk = (g / 4) % kMxRowScales;
-  const int n = pos ? M : min(min(__ldg(ntpp), rows), M);
-  for (int t = blockIdx.y; t < n; t += gridDim.y) {
+  const bool in_unit = g < mx_units(K) * (kMxUnitK / kRun), in = g < K / kRun;
+  const int unit = g / (kMxUnitK / kRun), chunk = (g / 2) % kMxRowScales;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int n = pos ? M : min(min(ld_ca(ntpp), rows), M);
+  auto position = [&](int t) {
     int p = -1;
-    if (pos) {
-      if (lane < topk) p = __ldg(pos + static_cast<long long>(t) * topk + lane);
-      if (p >= rows) p = -1;
-    } else if (lane == 0) {
-      p = t;
+    if (t < n) {
+      if (!pos) p = lane == 0 ? t : -1;
+      else if (lane < topk) p = ld_ca(pos + static_cast<long long>(t) * topk + lane);
     }
+    return p < rows ? p : -1;
+  };
+  int p_next = position(blockIdx.y);
+  for (int t = blockIdx.y; t < n; t += gridDim.y) {
+    const int p = p_next;
     uint32_t left = __ballot_sync(0xffffffffu, p >= 0);
+    Run<T> v = {};
+    if (left && in) load_run<kWide>(x + t * ldx + kRun * g, v);
+    p_next = position(t + gridDim.y);
     if (!left) continue;
-    float v[8] = {};
-    if (in) load8<T, V>(x + t * ldx + 8 * g, v);
     uint32_t scale;
-    const uint32_t q = quantize8(v, scale);
+    const uint2 q = quantize_run(v, scale);
     for (; left; left &= left - 1) {
       const size_t r = __shfl_sync(0xffffffffu, p, __ffs(left) - 1);
       if (in_unit) {
-        reinterpret_cast<uint32_t*>(out + mx_chunk_offset(unit, padded, r, chunk))[g & 3] = q;
-        if ((g & 3) == 0) out_scales[(unit * padded + r) * kMxRowScales + chunk] = static_cast<uint8_t>(scale);
+        reinterpret_cast<uint2*>(out + mx_chunk_offset(unit, padded, r, chunk))[g & 1] = q;
+        if ((g & 1) == 0) out_scales[(unit * padded + r) * kMxRowScales + chunk] = static_cast<uint8_t>(scale);
       }
     }
   }
@@ -170,42 +220,48 @@ __global__ void mx_prepack_kernel(const uint8_t* __restrict__ codes, const uint8
   dst[kMxTileBytes + (c / 4) * 512 + (r % 32) * 16 + (r / 32) * 4 + c % 4] = s;
 }
 
+// Rows that the grid's y dimension covers at once: about 16 CTAs per SM,
+// each walking on to its next row.
+unsigned grid_rows(long long rows, int columns) {
+  const long long most = std::max(1LL, 16LL * 152 / columns);
+  return static_cast<unsigned>(std::min(rows, most));
+}
+
 template <typename T>
 cudaError_t quantize_t(const void* x, long long ldx, long long rows, int K, uint8_t* codes, uint8_t* scales,
                        cudaStream_t st) {
-  const dim3 grid((K / 8 + kThreads - 1) / kThreads, static_cast<unsigned>(std::min<long long>(rows, 65535)));
-  constexpr int kV = 16 / sizeof(T);
-  if (row_access_bytes(x, ldx, K, sizeof(T)) == 16)
-    quantize_kernel<T, kV><<<grid, kThreads, 0, st>>>(static_cast<const T*>(x), ldx, rows, K, codes, scales);
+  const int columns = (K / kRun + kThreads - 1) / kThreads;
+  const dim3 grid(columns, grid_rows(rows, columns));
+  if (row_access_bytes(x, ldx, K, sizeof(T), 32) == 32)
+    quantize_kernel<T, true><<<grid, kThreads, 0, st>>>(static_cast<const T*>(x), ldx, rows, K, codes, scales);
   else
-    quantize_kernel<T, 1><<<grid, kThreads, 0, st>>>(static_cast<const T*>(x), ldx, rows, K, codes, scales);
+    quantize_kernel<T, false><<<grid, kThreads, 0, st>>>(static_cast<const T*>(x), ldx, rows, K, codes, scales);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, long long rows, int K, void* out, long long ldo,
                          cudaStream_t st) {
-  const dim3 grid((K / 8 + kThreads - 1) / kThreads, static_cast<unsigned>(std::min<long long>(rows, 65535)));
-  constexpr int kV = 16 / sizeof(T);
-  if (row_access_bytes(out, ldo, K, sizeof(T)) == 16)
-    dequantize_kernel<T, kV><<<grid, kThreads, 0, st>>>(codes, scales, rows, K, static_cast<T*>(out), ldo);
+  const int columns = (K / kRun + kThreads - 1) / kThreads;
+  const dim3 grid(columns, grid_rows(rows, columns));
+  if (row_access_bytes(out, ldo, K, sizeof(T), 32) == 32)
+    dequantize_kernel<T, true><<<grid, kThreads, 0, st>>>(codes, scales, rows, K, static_cast<T*>(out), ldo);
   else
-    dequantize_kernel<T, 1><<<grid, kThreads, 0, st>>>(codes, scales, rows, K, static_cast<T*>(out), ldo);
+    dequantize_kernel<T, false><<<grid, kThreads, 0, st>>>(codes, scales, rows, K, static_cast<T*>(out), ldo);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t quantize_rows_t(const void* x, long long ldx, int M, int K, const int32_t* pos, int topk,
                             const int32_t* ntpp, int rows, uint8_t* out, cudaStream_t st) {
-  const dim3 grid((mx_units(K) * (kMxUnitK / 8) + kThreads - 1) / kThreads, std::min(M, 65535));
-  constexpr int kV = 16 / sizeof(T);
-  if (row_access_bytes(x, ldx, K, sizeof(T)) == 16)
-    quantize_rows_kernel<T, kV><<<grid, kThreads, 0, st>>>(static_cast<const T*>(x), ldx, M, K, pos, topk, ntpp, rows,
-                                                           out);
-  else
-    quantize_rows_kernel<T, 1><<<grid, kThreads, 0, st>>>(static_cast<const T*>(x), ldx, M, K, pos, topk, ntpp, rows,
-                                                          out);
-  return cudaGetLastError();
+  const int columns = (mx_units(K) * (kMxUnitK / kRun) + kThreads - 1) / kThreads;
+  const dim3 grid(columns, grid_rows(M, columns));
+  const T* xt = static_cast<const T*>(x);
+  if (row_access_bytes(x, ldx, K, sizeof(T), 32) == 32)
+    return launch_kernel(quantize_rows_kernel<T, true>, grid, dim3(kThreads), 0, st, true, xt, ldx, M, K, pos, topk,
+                         ntpp, rows, out);
+  return launch_kernel(quantize_rows_kernel<T, false>, grid, dim3(kThreads), 0, st, true, xt, ldx, M, K, pos, topk,
+                       ntpp, rows, out);
 }
 
 }  // namespace
