@@ -4,13 +4,17 @@
 //
 // Operand layouts of the experts' product.  K is padded to units of 256 (128
 // bytes of values, one row of the tensor core's 128-byte swizzle) with zeros.
-//   weights  [256-byte header][expert][tile of 128 weight rows][unit] of
-//            kMxUnitBytes: 128 rows x 128 B, then the unit's scales as two
-//            512-byte blocks (128 of K each).  One bulk copy moves a unit.
+//   weights  [256-byte header][expert][pair of tiles][unit][tile of the pair]
+//            of kMxUnitBytes: 128 weight rows x 128 B, then the unit's scales
+//            as two 512-byte blocks (128 of K each).  One bulk copy moves a
+//            pair's unit.  The last pair of an odd number of tiles has one.
 //            Gate/up weights: 32 rows of a tile hold 16 gate rows and the 16
 //            up rows of the same indices, so one warp of the epilogue has both.
-//   rows     [unit][row] of 128 B, then [unit][row] of 8 scale bytes, for
-//            mx_rows_padded(capacity) rows: the rows of a tile are contiguous.
+//   rows     [slab of 256 rows][unit][row] of 128 B, then the same of 8 scale
+//            bytes, for mx_rows_padded(capacity) rows: a tile's rows of a unit
+//            are one or two contiguous runs, and its units lie 32 KB apart
+//            whatever the capacity (units a whole capacity apart missed the
+//            TLB: 0.3 us more per unit at 71,632 rows).
 // In both, the 16-byte chunk c of row r sits at chunk c ^ (r % 8) of its 128
 // bytes (the 128-byte swizzle; tiles start at multiples of 8 rows), and a
 // chunk is exactly one block of 32 values.
@@ -36,12 +40,14 @@ constexpr uint32_t kMxVersion = 1u;
 
 __host__ __device__ inline int mx_units(int K) { return (K + kMxUnitK - 1) / kMxUnitK; }
 __host__ __device__ inline int mx_tiles(int N) { return (N + kMxTileRows - 1) / kMxTileRows; }
+constexpr int kMxSlabRows = 256;
 // A tile of rows starts at a multiple of 8 and is read in whole runs of 16.
-__host__ __device__ inline size_t mx_rows_padded(size_t rows) { return (rows + 15) / 16 * 16 + 16; }
-// Byte offset of a block of 32 values (16 B) of row r, and of its scale,
-// relative to the start of the values and of the scales.
-__host__ __device__ inline size_t mx_chunk_offset(int unit, size_t rows_padded, size_t r, int c) {
-  return (static_cast<size_t>(unit) * rows_padded + r) * kMxRowBytes + 16 * (static_cast<size_t>(c) ^ (r & 7));
+__host__ __device__ inline size_t mx_rows_padded(size_t rows) {
+  return (rows + 15 + kMxSlabRows - 1) / kMxSlabRows * kMxSlabRows;
+}
+// Place of row r's part of a unit, in rows of 128 B (values) or 8 B (scales).
+__host__ __device__ inline size_t mx_row_place(int unit, int units, size_t r) {
+  return (r / kMxSlabRows * units + unit) * kMxSlabRows + r % kMxSlabRows;
 }
 
 // Scale code of a block: floor(log2(amax)) - 2 (so that amax / scale lies in

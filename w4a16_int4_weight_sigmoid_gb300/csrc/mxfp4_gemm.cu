@@ -10,18 +10,29 @@
 //     decoding and prefill.  Every SM draws its operands from L2 at about
 //     60 GB/s, which bounds all sizes above a few dozen rows per expert: a
 //     second weight tile on the same rows brings 66 KB for what took 100;
-//   * the work is the list of items times their K units of 256, cut into one
-//     contiguous range per CTA of equal length to within a unit.  Every SM
-//     streams the same number of bytes whatever the number of items, and one
-//     token's few items spread over all SMs.  An item that a range boundary
-//     cuts is summed by the CTA that finishes last, from FP32 partials in
-//     workspace, in K order, so results do not depend on timing;
-//   * per unit and weight tile one bulk copy brings 128 weight rows with their
-//     scales (17 KB, contiguous, already swizzled), one more the rows and one
-//     the rows' scales;
-//   * the rows' scales arrive in row order; warp 2 rearranges them into the
-//     block layout in shared memory; tcgen05.cp moves both operands' scales
-//     to TMEM ahead of the MMAs of the unit, in order with them;
+//   * most items are dealt whole and in turn, so that CTAs at work at one time
+//     share weights and rows in L2 (a contiguous run of items per CTA spread
+//     the live weights over more than L2: many rows per expert 346 us).  Those
+//     that do not divide evenly among the CTAs come first, with one whole
+//     round more: their K units of 256 are cut into one range per CTA of equal
+//     length to within a unit.  One token's few items spread over all SMs in
+//     the same way.  An item that a range boundary cuts is summed by the CTA
+//     that finishes last, from FP32 partials in workspace, in K order, so
+//     results do not depend on timing.  The extra round keeps the parts of an
+//     item at two or three (8 items left over in 19 parts each: 245 us);
+//   * per unit one bulk copy brings the pair's weight rows with their scales
+//     (34 KB, contiguous, already swizzled), one or two the rows;
+//   * the rows' scales lie in row order in memory, and a row tile may start at
+//     any multiple of 8, so warp 3 copies them four bytes at a time into the
+//     block layout of a ring of their own, four units ahead (cp.async);
+//   * issuing a tcgen05 instruction takes about 45 cycles, and a unit has 14 to
+//     18 of them, so each weight tile has a warp of its own that issues its
+//     scale copies (tcgen05.cp, to TMEM columns of its own, in order with the
+//     MMAs) and MMAs;
+//   * the epilogue reads accumulators in the 16-lane layout, where one thread
+//     has a weight row's values of two adjacent tokens (and gate and up of
+//     the same index), packs them and turns them with stmatrix.trans, so that
+//     C is written 16 bytes per lane;
 //   * stages and accumulators are laid out for the launch's largest row tile,
 //     which every CTA finds from the counts: decoding has five stages and four
 //     accumulators, a full tile three stages and one accumulator.
@@ -36,27 +47,33 @@
 namespace chord {
 namespace {
 
-constexpr int kMaxTok = 240;
+constexpr int kMaxTok = 224;
 constexpr int kPair = 2;               // weight tiles per item
 constexpr int kMaxStages = 5, kMaxAcc = 4;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 4 * kPair, kEpiThreads = 32 * kEpiWarps;
 constexpr int kThreads = 32 * kEpiWarp0 + kEpiThreads;
 constexpr int kMaxExperts = 1024;
-// stage: weight tiles with their scales | rows | row scales as they arrive |
-// row scales in block layout (two K halves of up to 256 rows)
+// stage: weight tiles with their scales | rows
 constexpr int kBOff = kPair * kMxUnitBytes;
-constexpr int kSfbHalf = 1024;
-__host__ __device__ constexpr int stage_bytes(int tok) {
-  return (kBOff + tok * (kMxRowBytes + kMxRowScales) + 2 * kSfbHalf + 1023) / 1024 * 1024;
-}
+__host__ __device__ constexpr int stage_bytes(int tok) { return kBOff + tok * kMxRowBytes; }
 constexpr int kStageBudget = 3 * stage_bytes(kMaxTok);
-constexpr int kSmemBytes = kStageBudget + 1024;
-constexpr int kSfCol = 480;            // SFA of tile t, half h at +8 t + 4 h; SFB half h at +16 + 8 h
+// ring of the rows' scales in block layout: two K halves of up to 256 rows
+constexpr int kSfSlots = 6, kSfAhead = 4;   // slots, and units in flight (fewer)
+constexpr int kSfbHalf = 1024, kSfSlotBytes = 2 * kSfbHalf;
+// an epilogue warp's 16 tokens x 32 weight rows on their way to C; the pitch
+// of 80 bytes spreads stmatrix's and the reads' 16-byte parts over the banks
+constexpr int kOutPitch = 80, kOutBytes = 16 * kOutPitch;
+constexpr int kSfOff = kStageBudget, kOutOff = kSfOff + kSfSlots * kSfSlotBytes;
+constexpr int kSmemBytes = kOutOff + kEpiWarps * kOutBytes + 1024;
+constexpr int kMmaWarp0 = 1, kSfWarp = kMmaWarp0 + kPair;
+constexpr int kSfCol = kPair * kMaxTok, kSfCols = 32;   // per tile: SFA at +0 and +8 (alternate units), SFB at +16
 constexpr int kTmemCols = 512;
 constexpr int kSlotFloats = kPair * kMaxTok * 128;   // one CTA's part of a cut item
-static_assert(kPair * kMaxTok <= kSfCol && kSfCol + 32 <= kTmemCols, "TMEM budget");
-static_assert(kBOff % 1024 == 0 && kMaxTok % 16 == 0 && kMaxTok <= 256, "stage layout");
+static_assert(kSfCol + kPair * kSfCols <= kTmemCols, "TMEM budget");
+static_assert(stage_bytes(16) % 1024 == 0 && kMaxTok % 16 == 0 && kMaxTok <= 256, "stage layout");
 static_assert(kMaxStages * stage_bytes(16) <= kStageBudget, "stage budget");
+static_assert(kSfAhead < kSfSlots, "a slot is reused after its unit was signalled");
+static_assert(kSfWarp + 1 <= kEpiWarp0 && kEpiWarp0 % 4 == 0, "warp roles; warp index selects the TMEM lane quarter");
 static_assert(kSmemBytes + (3 * kMaxExperts + 1) * 4 + 1024 <= 232448, "shared memory budget");
 
 struct MxArgs {
@@ -65,7 +82,7 @@ struct MxArgs {
   const int32_t* counts;
   const int32_t* offsets;
   int* split_cnt;        // [kMxMaxCtas], zero between launches
-  float* partial;        // [2 * kMxMaxCtas][kSlotFloats]
+  float* partial;        // [2 * kMxMaxCtas][tile of the pair][tokens / 4][128 weight rows][4]
   uint16_t* C;
   int* status;
   int E, N, K, ldc, capacity, n_tiles, gate_up;
@@ -76,55 +93,53 @@ __device__ __forceinline__ int row_tiles(int cnt) { return (cnt + kMaxTok - 1) /
 // Rows of an expert's row tiles: equal to within the rounding to 16.
 __device__ __forceinline__ int tile_rows(int cnt, int n_rt) { return ((cnt + n_rt - 1) / n_rt + 15) & ~15; }
 
-// A role's walk over the CTA's range of (item, K unit).  Items: experts in
-// order; per expert, weight tile pairs; per pair, row tiles (the pair's
-// weights are in L2 for the second).
-struct Walk {
-  const int *cnts, *offs;
-  int E, n_tiles, units;
-  long long left;              // units of the range not yet taken
-  int e, cnt, n_rt, per, pair, rt, u0, u1;
+// A role's walk over the CTA's segments (an item and a run of its K units):
+// its range of the cut items, then its whole items.  Items: experts in order;
+// per expert, weight tile pairs; per pair, row tiles.
+struct Plan {
+  const int *prefix, *cnts, *offs;   // shared: first item, rows and first row of each expert
+  int E, n_tiles, units, items, cut; // cut: the items [0, cut) are cut into ranges
+  long long begin, end;              // this CTA's units of them
+};
 
-  __device__ void expert(int at) {
-    e = at;
-    cnt = cnts[at];
-    n_rt = row_tiles(cnt);
-    per = n_rt ? tile_rows(cnt, n_rt) : 0;
-  }
-  __device__ void cut() { u1 = left < units - u0 ? u0 + static_cast<int>(left) : units; }
-  __device__ Walk(const int* prefix, const int* c, const int* o, int E_, int tiles, int units_, long long begin,
-                  long long end)
-      : cnts(c), offs(o), E(E_), n_tiles(tiles), units(units_), left(end - begin) {
-    if (left <= 0) return;
-    const int item = static_cast<int>(begin / units);
-    u0 = static_cast<int>(begin - static_cast<long long>(item) * units);
-    int lo = 0, hi = E - 1;    // largest e with prefix[e] <= item
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (prefix[mid] <= item) lo = mid; else hi = mid - 1;
+struct Walk {
+  const Plan& p;
+  long long pos;                     // next unit of the range of cut items
+  int item, e;                       // current item and its expert
+  int row0, rows, pair, tiles, u0, u1;
+  bool more;
+
+  __device__ explicit Walk(const Plan& plan) : p(plan), pos(plan.begin), item(-1), e(0) { advance(); }
+  __device__ void advance() {
+    if (pos < p.end) {
+      item = static_cast<int>(pos / p.units);
+      u0 = static_cast<int>(pos - static_cast<long long>(item) * p.units);
+      const long long rest = p.end - pos;
+      u1 = rest < p.units - u0 ? u0 + static_cast<int>(rest) : p.units;
+      pos += u1 - u0;
+    } else {
+      item = item < p.cut ? p.cut + static_cast<int>(blockIdx.x) : item + static_cast<int>(gridDim.x);
+      u0 = 0;
+      u1 = p.units;
     }
-    expert(lo);
-    pair = (item - prefix[lo]) / n_rt;
-    rt = item - prefix[lo] - pair * n_rt;
-    cut();
-  }
-  __device__ void next() {
-    left -= u1 - u0;
-    if (left <= 0) return;
-    u0 = 0;
-    if (++rt == n_rt) {
-      rt = 0;
-      if (++pair * kPair >= n_tiles) {
-        pair = 0;
-        do expert(e + 1);      // units are left, so an expert with rows follows
-        while (cnt == 0);
+    more = item < p.items;
+    if (!more) return;
+    // the expert: largest e with prefix[e] <= item (items only grow)
+    if (p.prefix[e + 1] <= item) {
+      int lo = e + 1, hi = p.E - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.prefix[mid] <= item) lo = mid; else hi = mid - 1;
       }
+      e = lo;
     }
-    cut();
+    const int cnt = p.cnts[e], n_rt = row_tiles(cnt), local = item - p.prefix[e];
+    pair = n_rt == 1 ? local : local / n_rt;
+    const int rt = local - pair * n_rt, per = tile_rows(cnt, n_rt);
+    row0 = p.offs[e] + rt * per;
+    rows = min(per, cnt - rt * per);
+    tiles = min(kPair, p.n_tiles - kPair * pair);
   }
-  __device__ int row0() const { return offs[e] + rt * per; }
-  __device__ int rows() const { return min(per, cnt - rt * per); }
-  __device__ int tiles() const { return min(kPair, n_tiles - kPair * pair); }
 };
 
 // Whether `ok` holds in all threads of the epilogue warps.
@@ -141,35 +156,91 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
   return r != 0;
 }
 
-// 32 columns of accumulators (this lane's weight row `lrow` of tile `tile`)
-// into rows c0 .. of C; `out` is C's row of column 0, `n` the valid columns.
-__device__ __forceinline__ void store_columns(const MxArgs& a, const uint32_t (&v)[32], uint16_t* out, int tile,
-                                              int lrow, int n) {
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four 8 x 8 matrices of 16-bit values from the fragment layout (register i:
+// row lane / 4 of matrix i, columns 2 (lane % 4) and + 1), transposed: lane
+// 8 i + c gives the 16-byte place of matrix i's column c.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r0), "r"(r1),
+               "r"(r2), "r"(r3)
+               : "memory");
+}
+
+// Up to 32 tokens of a finished item to C: this warp's accumulators of its 32
+// weight rows (lo: rows 0-15 of the lane quarter, hi: rows 16-31, gate and up),
+// `n` tokens at `out`, through the warp's own staging rows.
+__device__ __forceinline__ void store_tokens(const MxArgs& a, const uint32_t (&lo)[16], const uint32_t (&hi)[16],
+                                             uint16_t* out, uint32_t stage_s, int tile, int q, int lane, int n) {
+  // lane 8 i + c: token c of its 8-token group, weight rows 8 (i & 1) on
+  const uint32_t dst = stage_s + ((lane & 7) + 8 * (lane >> 4)) * kOutPitch + ((lane >> 3) & 1) * 16;
+  // 16 bytes (8 columns of C) per lane: 2 or 4 lanes per token
+  const int sh = a.gate_up ? 1 : 2, part = lane & ((1 << sh) - 1);
+  const int col = (a.gate_up ? 64 * tile + 16 * q : kMxTileRows * tile + 32 * q) + 8 * part;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {   // tokens 16 p .. 16 p + 15
+    uint32_t l[4], h[4];          // [token group of 8][weight rows 0-7, 8-15]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * p + 2 * i;
+      const float l0 = __uint_as_float(lo[r]), l1 = __uint_as_float(lo[r + 1]);
+      const float h0 = __uint_as_float(hi[r]), h1 = __uint_as_float(hi[r + 1]);
+      l[i] = a.gate_up ? bf16_pair(silu_mul(l0, h0), silu_mul(l1, h1)) : bf16_pair(l0, l1);
+      h[i] = bf16_pair(h0, h1);
+    }
+    stmatrix_x4_trans(dst, l[0], l[1], l[2], l[3]);
+    if (!a.gate_up) stmatrix_x4_trans(dst + 32, h[0], h[1], h[2], h[3]);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int token = (lane >> sh) + j * (32 >> sh);
+      if (token < 16 && 16 * p + token < n && col < a.ldc) {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(stage_s + token * kOutPitch + 16 * part)
+                     : "memory");
+        *reinterpret_cast<uint4*>(out + static_cast<size_t>(16 * p + token) * a.ldc + col) = v;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// Eight tokens of a summed item (this lane's weight row `lrow` of tile
+// `tile`), `n` of them valid, at `out`.
+__device__ __forceinline__ void store_columns(const MxArgs& a, const float (&v)[8], uint16_t* out, int tile, int lrow,
+                                              int n) {
   if (a.gate_up) {
     // lanes 0-15 hold gate rows, 16-31 the up rows of the same indices: of
     // two columns, the low lanes finish the first and the high lanes the second
     const bool up = lrow & 16;
     const int col = (kMxTileRows / 2) * tile + 16 * (lrow / 32) + (lrow & 15);
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, up ? v[c] : v[c + 1], 16));
-      const float g = up ? other : __uint_as_float(v[c]);
-      const float h = __fdividef(g, 1.0f + __expf(-g)) * (up ? __uint_as_float(v[c + 1]) : other);
+    for (int c = 0; c < 8; c += 2) {
+      const float other = __shfl_xor_sync(0xffffffffu, up ? v[c] : v[c + 1], 16);
+      const float h = silu_mul(up ? other : v[c], up ? v[c + 1] : other);
       const int cc = c + (up ? 1 : 0);
       if (cc < n && col < a.ldc) out[static_cast<size_t>(cc) * a.ldc + col] = f32_to_bf16_rn(h);
     }
   } else {
     const int col = kMxTileRows * tile + lrow;
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-      if (c < n && col < a.ldc) out[static_cast<size_t>(c) * a.ldc + col] = f32_to_bf16_rn(__uint_as_float(v[c]));
+    for (int c = 0; c < 8; ++c)
+      if (c < n && col < a.ldc) out[static_cast<size_t>(c) * a.ldc + col] = f32_to_bf16_rn(v[c]);
   }
 }
 
 __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], sf_full[kMaxStages], empty[kMaxStages];
-  __shared__ __align__(8) uint64_t tfull[kMaxAcc], tempty[kMaxAcc], done_bar;
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], sf_full[kSfSlots], sf_empty[kSfSlots];
+  __shared__ __align__(8) uint64_t tfull[kMaxAcc], tempty[kMaxAcc], done_bar[kPair];
   __shared__ uint32_t tmem_base_s;
   __shared__ int prefix[kMaxExperts + 1];
   __shared__ int s_cnt[kMaxExperts], s_off[kMaxExperts];
@@ -185,14 +256,17 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     abort_flag = 0;
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kPair);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
       mbar_init(&sf_full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&sf_empty[s], kPair);
     }
     for (int b = 0; b < kMaxAcc; ++b) {
-      mbar_init(&tfull[b], 1);
+      mbar_init(&tfull[b], kPair);
       mbar_init(&tempty[b], kEpiWarps);
     }
-    mbar_init(&done_bar, 1);
+    for (int t = 0; t < kPair; ++t) mbar_init(&done_bar[t], 1);
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base_s, kTmemCols);
@@ -253,154 +327,211 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   }
   if (tid == kThreads - 1) prefix[a.E] = run;   // the last thread ends at the total
   __syncthreads();
-  const uint32_t tmem_base = tmem_base_s;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, tmem_base_s, 0);
 
+  tok = __shfl_sync(0xffffffffu, tok, 0);   // warp-uniform for the issuing warps
   const int units = mx_units(a.K);
-  const long long total = hdr_ok ? static_cast<long long>(prefix[a.E]) * units : 0;
-  // CTAs that take work: all, or as many as there are units (a range is
-  // never empty, so the parts of a cut item are in consecutive CTAs)
-  const long long G = total < gridDim.x ? total : gridDim.x;
-  const long long begin = blockIdx.x < G ? blockIdx.x * total / G : 0;
-  const long long end = blockIdx.x < G ? (blockIdx.x + 1) * total / G : 0;
+  Plan plan;
+  plan.prefix = prefix, plan.cnts = s_cnt, plan.offs = s_off;
+  plan.E = a.E, plan.n_tiles = a.n_tiles, plan.units = units;
+  plan.items = hdr_ok ? prefix[a.E] : 0;
+  plan.cut = plan.items % static_cast<int>(gridDim.x);
+  if (plan.cut > 0 && plan.items > plan.cut) plan.cut += gridDim.x;
+  // CTAs that share the cut items.  A range of u units costs u units' time and
+  // its item units / u parts to add; a part takes tok / 80 of a unit's time
+  // (measured 8 ns a token against 0.6 us), so u is at least the square root
+  // of units * tok / 80.  No range is empty: an item's parts are in
+  // consecutive CTAs.
+  const long long total = static_cast<long long>(plan.cut) * units;
+  const int least = max(1, static_cast<int>(sqrtf(units * tok / 80.f)));
+  const long long G = total > 0 ? max(1LL, min(static_cast<long long>(gridDim.x), total / least)) : 0;
+  plan.begin = blockIdx.x < G ? blockIdx.x * total / G : 0;
+  plan.end = blockIdx.x < G ? (blockIdx.x + 1) * total / G : 0;
   const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget / stage);
-  const int raw_off = kBOff + tok * kMxRowBytes, sfb_off = raw_off + tok * kMxRowScales;
   const int n_acc = min(kMaxAcc, kSfCol / (kPair * tok));
-  Walk w(prefix, s_cnt, s_off, a.E, a.n_tiles, units, begin, end);
+  Walk w(plan);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- copies
-    if (lane == 0) {
-      const uint8_t* row_scales = a.rows + static_cast<size_t>(units) * a.rows_padded * kMxRowBytes;
-      const size_t tile_bytes = static_cast<size_t>(units) * kMxUnitBytes;
-      int it = 0, st = 0, ph = 0;
-      for (; w.left > 0 && !abort_flag; w.next()) {
-        const int n16 = (w.rows() + 15) & ~15, tiles = w.tiles();
-        const uint8_t* wsrc =
-            a.w + kPackHeaderBytes + (static_cast<size_t>(w.e) * a.n_tiles + kPair * w.pair) * tile_bytes;
-        const size_t row0 = w.row0();
-        for (int u = w.u0; u < w.u1; ++u, ++it) {
-          if (it >= n_stages && !mbar_wait(&empty[st], ph ^ 1, a.status)) {
-            abort_flag = 1;
-            break;
-          }
-          uint8_t* dst = smem + st * stage;
-          const size_t row = static_cast<size_t>(u) * a.rows_padded + row0;
-          mbar_arrive_expect_tx(&full[st], tiles * kMxUnitBytes + n16 * (kMxRowBytes + kMxRowScales));
-          for (int t = 0; t < tiles; ++t)
-            bulk_g2s(dst + t * kMxUnitBytes, wsrc + t * tile_bytes + static_cast<size_t>(u) * kMxUnitBytes,
-                     kMxUnitBytes, &full[st]);
-          bulk_g2s(dst + kBOff, a.rows + row * kMxRowBytes, n16 * kMxRowBytes, &full[st]);
-          bulk_g2s(dst + raw_off, row_scales + row * kMxRowScales, n16 * kMxRowScales, &full[st]);
-          if (++st == n_stages) st = 0, ph ^= 1;
-        }
-      }
-      // every issued copy lands before the CTA can exit
-      for (int j = max(0, it - n_stages); j < it; ++j) mbar_wait(&full[j % n_stages], (j / n_stages) & 1, a.status);
-    }
-  } else if (warp == 2) {
-    // --------------------------------------------------- row scales to blocks
-    int st = 0, ph = 0;
-    for (; w.left > 0 && !abort_flag; w.next()) {
-      const int n16 = (w.rows() + 15) & ~15;
-      for (int u = w.u0; u < w.u1; ++u) {
-        bool ok = mbar_wait(&full[st], ph, a.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
+    // The whole warp runs the loop, one elected lane issues.
+    const size_t tile_bytes = static_cast<size_t>(units) * kMxUnitBytes;
+    int it = 0, st = 0, ph = 0;
+    for (; w.more && !abort_flag; w.advance()) {
+      const int n16 = __shfl_sync(0xffffffffu, (w.rows + 15) & ~15, 0);
+      const int tiles = __shfl_sync(0xffffffffu, w.tiles, 0);
+      const int u1 = __shfl_sync(0xffffffffu, w.u1, 0);
+      int u = __shfl_sync(0xffffffffu, w.u0, 0);
+      const uint8_t* wsrc = a.w + kPackHeaderBytes +
+                            (static_cast<size_t>(w.e) * a.n_tiles + kPair * w.pair) * tile_bytes +
+                            static_cast<size_t>(u) * tiles * kMxUnitBytes;
+      // the tile's rows: up to the end of their slab, then the next one's
+      const int head = min(n16, kMxSlabRows - __shfl_sync(0xffffffffu, w.row0, 0) % kMxSlabRows);
+      const uint8_t* rsrc = a.rows + mx_row_place(u, units, w.row0) * kMxRowBytes;
+      const uint8_t* rsrc2 = a.rows + mx_row_place(u, units, w.row0 + head) * kMxRowBytes;
+      for (; u < u1; ++u, ++it) {
+        if (it >= n_stages && !__all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, a.status))) {
           abort_flag = 1;
           break;
         }
-        uint8_t* base = smem + st * stage;
-        for (int r = lane; r < n16; r += 32) {
-          const uint2 v = *reinterpret_cast<const uint2*>(base + raw_off + r * kMxRowScales);
-          uint8_t* dst = base + sfb_off + (r / 128) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4;
-          *reinterpret_cast<uint32_t*>(dst) = v.x;
-          *reinterpret_cast<uint32_t*>(dst + kSfbHalf) = v.y;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_full[st]);
+        const uint32_t dst = smem0 + st * stage;
+        mbar_arrive_expect_tx_elect(&full[st], tiles * kMxUnitBytes + n16 * kMxRowBytes);
+        bulk_g2s_elect(dst, wsrc, tiles * kMxUnitBytes, &full[st]);
+        bulk_g2s_elect(dst + kBOff, rsrc, head * kMxRowBytes, &full[st]);
+        if (head < n16)
+          bulk_g2s_elect(dst + kBOff + head * kMxRowBytes, rsrc2, (n16 - head) * kMxRowBytes, &full[st]);
+        wsrc += tiles * kMxUnitBytes;
+        rsrc += kMxSlabRows * kMxRowBytes;
+        rsrc2 += kMxSlabRows * kMxRowBytes;
         if (++st == n_stages) st = 0, ph ^= 1;
       }
     }
-  } else if (warp == 1) {
+    // every issued copy lands before the CTA can exit
+    for (int j = max(0, it - n_stages); j < it; ++j) mbar_wait(&full[j % n_stages], (j / n_stages) & 1, a.status);
+  } else if (warp == kSfWarp) {
+    // --------------------------------------------------- row scales to blocks
+    // Slot reuse waits for the MMAs of a unit that was signalled already, so
+    // the wait always ends.
+    const uint8_t* row_scales = a.rows + units * a.rows_padded * kMxRowBytes;
+    int issued = 0, signalled = 0, in = 0, in_ph = 0, out = 0;
+    auto signal = [&] {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sf_full[out]);
+      ++signalled;
+      if (++out == kSfSlots) out = 0;
+    };
+    for (; w.more && !abort_flag; w.advance()) {
+      const int n16 = (w.rows + 15) & ~15;
+      // this lane's rows of the tile, 32 apart: those below `head` are in the
+      // first slab, the others in the next
+      const int head = kMxSlabRows - w.row0 % kMxSlabRows;
+      const uint8_t* src = row_scales + mx_row_place(w.u0, units, w.row0 + lane) * kMxRowScales;
+      const size_t slab = static_cast<size_t>(units - 1) * kMxSlabRows * kMxRowScales;
+      for (int u = w.u0; u < w.u1; ++u, ++issued) {
+        if (issued >= kSfSlots && !__all_sync(0xffffffffu, mbar_wait(&sf_empty[in], in_ph ^ 1, a.status))) {
+          abort_flag = 1;
+          break;
+        }
+        const uint32_t dst = smem0 + kSfOff + in * kSfSlotBytes + lane * 16;
+#pragma unroll
+        for (int i = 0; i < (kMaxTok + 31) / 32; ++i) {
+          const int r = 32 * i + lane;
+          if (r < n16) {
+            const uint8_t* at = src + 32 * i * kMxRowScales + (lane < head && r >= head ? slab : 0);
+            cp_async4(dst + (i / 4) * 512 + (i % 4) * 4, at);
+            cp_async4(dst + (i / 4) * 512 + (i % 4) * 4 + kSfbHalf, at + 4);
+          }
+        }
+        cp_async_commit();
+        src += kMxSlabRows * kMxRowScales;
+        if (++in == kSfSlots) in = 0, in_ph ^= 1;
+        if (issued + 1 - signalled == kSfAhead) {
+          cp_async_wait<kSfAhead - 1>();
+          signal();
+        }
+      }
+    }
+    cp_async_wait<0>();
+    while (signalled < issued && !abort_flag) signal();
+  } else if (warp >= kMmaWarp0 && warp < kMmaWarp0 + kPair) {
     // ------------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      int st = 0, ph = 0, acc = 0, use = 0;
-      bool issued = false;
-      for (; w.left > 0 && !abort_flag; w.next()) {
-        const int n16 = (w.rows() + 15) & ~15, tiles = w.tiles();
-        if (use >= 1 && !mbar_wait(&tempty[acc], (use - 1) & 1, a.status)) {
+    // One warp per weight tile; the whole warp runs the loop, one elected
+    // lane issues.  Both commit every unit and item, also a tile that the
+    // item lacks.
+    const int t = warp - kMmaWarp0;
+    int st = 0, ph = 0, slot = 0, sf_ph = 0, acc = 0, use = 0;
+    const uint32_t sfb = tmem_base + kSfCol + t * kSfCols + 16;
+    uint32_t sfa = sfb - 16;
+    bool issued = false;
+    for (; w.more && !abort_flag; w.advance()) {
+      const int n16 = __shfl_sync(0xffffffffu, (w.rows + 15) & ~15, 0);
+      const bool active = t < __shfl_sync(0xffffffffu, w.tiles, 0);
+      int left = __shfl_sync(0xffffffffu, w.u1 - w.u0, 0);
+      if (use >= 1 && !__all_sync(0xffffffffu, mbar_wait(&tempty[acc], (use - 1) & 1, a.status))) {
+        abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem_base + (acc * kPair + t) * tok;
+      const uint32_t idesc0 = idesc_mxf4(n16, 0), idesc2 = idesc_mxf4(n16, 2);
+      uint32_t accumulate = 0;
+      for (; left > 0; --left) {
+        if (!__all_sync(0xffffffffu, mbar_wait2(&full[st], ph, &sf_full[slot], sf_ph, a.status))) {
           abort_flag = 1;
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem_base + acc * kPair * tok, sf = tmem_base + kSfCol;
-        const uint32_t idesc[2] = {idesc_mxf4(n16, 0), idesc_mxf4(n16, 2)};
-        for (int u = w.u0; u < w.u1; ++u) {
-          if (!mbar_wait2(&full[st], ph, &sf_full[st], ph, a.status)) {
-            abort_flag = 1;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t base = smem0 + st * stage;
-          for (int t = 0; t < tiles; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              tc_cp_scales(sf + 8 * t + 4 * h, scales_desc(base + t * kMxUnitBytes + kMxTileBytes + 512 * h));
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tc_cp_scales(sf + 16 + 8 * h, scales_desc(base + sfb_off + kSfbHalf * h));
-            if (n16 > 128) tc_cp_scales(sf + 20 + 8 * h, scales_desc(base + sfb_off + kSfbHalf * h + 512));
-          }
-          const uint64_t ad = sw128_kmajor_desc(base), bd = sw128_kmajor_desc(base + kBOff);
-          for (int t = 0; t < tiles; ++t)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_mxf4(d + t * tok, ad + t * (kMxUnitBytes >> 4) + 2 * kk, bd + 2 * kk, idesc[kk & 1],
-                          sf + 8 * t + 4 * (kk >> 1), sf + 16 + 8 * (kk >> 1), u > w.u0 || kk ? 1u : 0u);
-          tc_commit(&empty[st]);
-          issued = true;
-          if (++st == n_stages) st = 0, ph ^= 1;
+        if (active) {
+          const uint32_t base = smem0 + st * stage, wt = base + t * kMxUnitBytes;
+          tc_mxf4_scales_elect<kSfbHalf>(scales_desc(smem0 + kSfOff + slot * kSfSlotBytes), sfb, n16 > 128);
+          tc_mxf4_unit_elect(d, sw128_kmajor_desc(wt), sw128_kmajor_desc(base + kBOff), scales_desc(wt + kMxTileBytes),
+                             sfa, sfb, idesc0, idesc2, accumulate);
         }
-        if (abort_flag) break;
-        tc_commit(&tfull[acc]);
-        if (++acc == n_acc) acc = 0, ++use;
+        tc_commit2_elect(&empty[st], &sf_empty[slot]);
+        sfa = 2 * sfb - 24 - sfa;   // the other of the two sets: sfb - 16, sfb - 8
+        accumulate = 1;
+        issued = true;
+        if (++st == n_stages) st = 0, ph ^= 1;
+        if (++slot == kSfSlots) slot = 0, sf_ph ^= 1;
       }
-      // all issued MMAs complete before TMEM can be freed
-      if (issued) {
-        tc_commit(&done_bar);
-        mbar_wait(&done_bar, 0, a.status);
-      }
+      if (abort_flag) break;
+      tc_commit_elect(&tfull[acc]);
+      if (++acc == n_acc) acc = 0, ++use;
+    }
+    // all issued MMAs complete before TMEM can be freed
+    if (issued) {
+      tc_commit_elect(&done_bar[t]);
+      mbar_wait(&done_bar[t], 0, a.status);
     }
   } else if (warp >= kEpiWarp0) {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3, lrow = 32 * q + lane;        // TMEM lane quarter; weight row of the tile
     const int t = (warp - kEpiWarp0) / 4;                // weight tile of the pair
+    const uint32_t out_stage = smem0 + kOutOff + (warp - kEpiWarp0) * kOutBytes;
     int acc = 0, use = 0;
-    for (; w.left > 0; w.next()) {
+    for (; w.more; w.advance()) {
       // all epilogue warps go on or stop together: barriers follow
       if (!epilogue_all(mbar_wait(&tfull[acc], use & 1, a.status))) {
         abort_flag = 1;
         break;
       }
       tc_fence_after();
-      const bool active = t < w.tiles();
-      const int rows = active ? w.rows() : 0;
+      const int rows = t < w.tiles ? w.rows : 0;
       const uint32_t taddr = tmem_base + (acc * kPair + t) * tok + (static_cast<uint32_t>(32 * q) << 16);
-      uint16_t* out = a.C + static_cast<size_t>(w.row0()) * a.ldc;
+      uint16_t* out = a.C + static_cast<size_t>(w.row0) * a.ldc;
       const bool whole = w.u0 == 0 && w.u1 == units;
-      const size_t part = static_cast<size_t>(t) * kMaxTok * 128 + lrow;
+      const size_t part = static_cast<size_t>(t) * kMaxTok * 128 + 4 * lrow;
       float* mine_p = a.partial + static_cast<size_t>(2 * blockIdx.x + (w.u0 == 0)) * kSlotFloats + part;
-      for (int c0 = 0; c0 < rows; c0 += 32) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(taddr + c0, v);
-        tmem_ld_wait();
-        if (whole) {
-          store_columns(a, v, out + static_cast<size_t>(c0) * a.ldc, kPair * w.pair + t, lrow, rows - c0);
-        } else {
+      if (whole) {
+        // the next 32 tokens' accumulators are on their way while these go out
+        uint32_t v[2][2][16];
+        auto load = [&](int c0, uint32_t(&x)[2][16]) {
+          tmem_ld_16x256b_x4(taddr + c0, x[0]);
+          tmem_ld_16x256b_x4(taddr + c0 + (16u << 16), x[1]);
+        };
+        auto store = [&](int c0, const uint32_t(&x)[2][16]) {
+          store_tokens(a, x[0], x[1], out + static_cast<size_t>(c0) * a.ldc, out_stage, kPair * w.pair + t, q, lane,
+                       rows - c0);
+        };
+        if (rows > 0) load(0, v[0]);
+        for (int c0 = 0; c0 < rows; c0 += 64) {
+          tmem_ld_wait();
+          if (c0 + 32 < rows) load(c0 + 32, v[1]);
+          store(c0, v[0]);
+          if (c0 + 32 >= rows) break;
+          tmem_ld_wait();
+          if (c0 + 64 < rows) load(c0 + 64, v[0]);
+          store(c0 + 32, v[1]);
+        }
+      } else {
+        for (int c0 = 0; c0 < rows; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(taddr + c0, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c0 + c < rows) mine_p[(c0 + c) * 128] = __uint_as_float(v[c]);
+          for (int c = 0; c < 32; c += 4)
+            if (c0 + c < rows)
+              *reinterpret_cast<uint4*>(mine_p + (c0 + c) * 128) = make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
         }
       }
       tc_fence_before();
@@ -409,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       if (++acc == n_acc) acc = 0, ++use;
       if (whole) continue;
       // a cut item: the CTA that arrives last adds the parts in K order
-      const long long i0 = end - w.left - w.u0;          // the item's units are [i0, i0 + units)
+      const long long i0 = static_cast<long long>(w.item) * units;   // its units are [i0, i0 + units)
       const int first = static_cast<int>(((i0 + 1) * G - 1) / total);
       const int last = static_cast<int>(((i0 + units) * G - 1) / total);
       __threadfence();
@@ -422,33 +553,32 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       epilogue_all(true);
       if (!last_flag) continue;
       __threadfence();
-      for (int c0 = 0; c0 < rows; c0 += 32) {
-        float f[32];
+      // eight tokens at a time, six parts' loads in flight (parts past the
+      // last one and tokens past the rows are loaded again, not added)
+      constexpr int kParts = 6;
+      for (int c0 = 0; c0 < rows; c0 += 8) {
+        float f[8];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) f[c] = 0.f;
-        for (int p0 = first; p0 <= last; p0 += 4) {      // four parts' loads in flight
+        for (int c = 0; c < 8; ++c) f[c] = 0.f;
+        const int c4 = c0 + 4 < rows ? 512 : 0;
+        for (int p0 = first; p0 <= last; p0 += kParts) {
+          float4 x[kParts][2];
 #pragma unroll
-          for (int h = 0; h < 32; h += 8) {
-            if (c0 + h >= rows) break;
-            float x[4][8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int p = min(p0 + i, last);
-              const float* src = a.partial + static_cast<size_t>(2 * p + (p == first)) * kSlotFloats + part;
-#pragma unroll
-              for (int c = 0; c < 8; ++c) x[i][c] = c0 + h + c < rows ? ld_cg(src + (c0 + h + c) * 128) : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (p0 + i <= last)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) f[h + c] += x[i][c];
+          for (int i = 0; i < kParts; ++i) {
+            const int p = min(p0 + i, last);
+            const float* src =
+                a.partial + static_cast<size_t>(2 * p + (p == first)) * kSlotFloats + part + c0 * 128;
+            x[i][0] = ld_cg_f4(src);
+            x[i][1] = ld_cg_f4(src + c4);
           }
-        }
-        uint32_t v[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(f[c]);
-        store_columns(a, v, out + static_cast<size_t>(c0) * a.ldc, kPair * w.pair + t, lrow, rows - c0);
+          for (int i = 0; i < kParts; ++i)
+            if (p0 + i <= last) {
+              f[0] += x[i][0].x, f[1] += x[i][0].y, f[2] += x[i][0].z, f[3] += x[i][0].w;
+              f[4] += x[i][1].x, f[5] += x[i][1].y, f[6] += x[i][1].z, f[7] += x[i][1].w;
+            }
+        }
+        store_columns(a, f, out + static_cast<size_t>(c0) * a.ldc, kPair * w.pair + t, lrow, rows - c0);
       }
     }
   }

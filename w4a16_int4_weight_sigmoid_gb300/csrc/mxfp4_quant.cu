@@ -149,9 +149,9 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, lon
                                                                  const int32_t* pos, int topk, const int32_t* ntpp,
                                                                  int rows, uint8_t* __restrict__ out) {
   const int g = blockIdx.x * kThreads + threadIdx.x, lane = threadIdx.x & 31;
-  const size_t padded = mx_rows_padded(rows);
-  uint8_t* out_scales = out + static_cast<size_t>(mx_units(K)) * padded * kMxRowBytes;
-  const bool in_unit = g < mx_units(K) * (kMxUnitK / kRun), in = g < K / kRun;
+  const int units = mx_units(K);
+  uint8_t* out_scales = out + units * mx_rows_padded(rows) * kMxRowBytes;
+  const bool in_unit = g < units * (kMxUnitK / kRun), in = g < K / kRun;
   const int unit = g / (kMxUnitK / kRun), chunk = (g / 2) % kMxRowScales;
   grid_dep_wait();
   grid_dep_launch();
@@ -175,10 +175,11 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, lon
     uint32_t scale;
     const uint2 q = quantize_run(v, scale);
     for (; left; left &= left - 1) {
-      const size_t r = __shfl_sync(0xffffffffu, p, __ffs(left) - 1);
+      const uint32_t r = __shfl_sync(0xffffffffu, p, __ffs(left) - 1);
       if (in_unit) {
-        reinterpret_cast<uint2*>(out + mx_chunk_offset(unit, padded, r, chunk))[g & 1] = q;
-        if ((g & 1) == 0) out_scales[(unit * padded + r) * kMxRowScales + chunk] = static_cast<uint8_t>(scale);
+        const size_t at = mx_row_place(unit, units, r);
+        reinterpret_cast<uint2*>(out + at * kMxRowBytes + 16 * (chunk ^ (r & 7)))[g & 1] = q;
+        if ((g & 1) == 0) out_scales[at * kMxRowScales + chunk] = static_cast<uint8_t>(scale);
       }
     }
   }
@@ -215,7 +216,9 @@ __global__ void mx_prepack_kernel(const uint8_t* __restrict__ codes, const uint8
     q = reinterpret_cast<const uint4*>(codes)[at];
     s = scales[at];
   }
-  uint8_t* dst = out + kPackHeaderBytes + unit_id * kMxUnitBytes;
+  const long long pair_tiles = min(2, tiles - tile / 2 * 2);
+  const long long place = (e * tiles + tile / 2 * 2) * units + u * pair_tiles + tile % 2;
+  uint8_t* dst = out + kPackHeaderBytes + place * kMxUnitBytes;
   *reinterpret_cast<uint4*>(dst + r * kMxRowBytes + 16 * (c ^ (r & 7))) = q;
   dst[kMxTileBytes + (c / 4) * 512 + (r % 32) * 16 + (r / 32) * 4 + c % 4] = s;
 }

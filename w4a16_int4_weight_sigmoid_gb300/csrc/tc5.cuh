@@ -54,24 +54,65 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T, MXFP4 inputs (E2M1, K = 64, one
-// E8M0 scale per 32 of K, read from TMEM), FP32 accumulate, one CTA.
-__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+// One K = 256 unit of a block-scaled MXFP4 product (E2M1 operands, an E8M0
+// scale per 32 of K), issued by one elected lane of a converged warp in one
+// block: an instruction of its own election took about 60 cycles to issue,
+// longer than its MMA ran.  M = 128 rows of A times N columns of B.
+//   a, b      SW128 K-major descriptors (a K = 64 step is 32 bytes on)
+//   fa, fb    scales_desc of A's two 512-byte scale blocks (128 of K each)
+//             and of B's (kHalf bytes apart; 512 more for N > 128)
+//   sfa, sfb  TMEM columns for them: 4 per block of A, 8 per block of B
+// tcgen05.cp copies 512 bytes (32 rows of 16 B) to four columns, the 32 lanes
+// repeated in all four lane quarters: byte k of column c, lane i is scale k
+// of row 32 c + i.  It executes in order with the MMAs of the same thread.
+#define CHORD_MXF4_MMA(dst, a, b, id, sa, sb, acc) \
+  "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [" dst "], " a ", " b ", " id ", [" sa "], [" sb "], " acc ";\n\t"
+#define CHORD_CP_SCALES(dst, src) "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [" dst "], " src ";\n\t"
+__device__ __forceinline__ void tc_mxf4_unit_elect(uint32_t d, uint64_t a, uint64_t b, uint64_t fa, uint32_t sfa,
+                                                   uint32_t sfb, uint32_t idesc0, uint32_t idesc2,
+                                                   uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      "{\n\t.reg .pred e, p, q;\n\t.reg .b32 r, sa, sb;\n\t.reg .b64 f, a1, a2, a3, b1, b2, b3;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %8, 0;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "add.s32 sa, %4, 4;\n\tadd.s32 sb, %5, 8;\n\tadd.s64 f, %3, 32;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      CHORD_CP_SCALES("%4", "%3")
+      CHORD_CP_SCALES("sa", "f")
+      CHORD_MXF4_MMA("%0", "%1", "%2", "%6", "%4", "%5", "p")
+      CHORD_MXF4_MMA("%0", "a1", "b1", "%7", "%4", "%5", "q")
+      CHORD_MXF4_MMA("%0", "a2", "b2", "%6", "sa", "sb", "q")
+      CHORD_MXF4_MMA("%0", "a3", "b3", "%7", "sa", "sb", "q")
+      "}" ::"r"(d), "l"(a), "l"(b), "l"(fa), "r"(sfa), "r"(sfb), "r"(idesc0), "r"(idesc2), "r"(accumulate)
       : "memory");
 }
-// 512 bytes of shared memory (32 rows of 16 B) -> four TMEM columns, the 32
-// lanes repeated in all four lane quarters: the layout of 128 rows' scales
-// (byte k of column c, lane i = scale k of row 32 c + i).  Executes in order
-// with the tcgen05.mma of the same thread.
-__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// B's scales of a unit: two blocks, four when N > 128.
+template <int kHalf>
+__device__ __forceinline__ void tc_mxf4_scales_elect(uint64_t fb, uint32_t sfb, bool wide) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b32 r, s1, s2, s3;\n\t.reg .b64 f1, f2, f3;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "add.s32 s1, %1, 8;\n\tadd.s32 s2, %1, 4;\n\tadd.s32 s3, %1, 12;\n\t"
+      "add.s64 f1, %0, %3;\n\tadd.s64 f2, %0, 32;\n\tadd.s64 f3, f1, 32;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      CHORD_CP_SCALES("%1", "%0")
+      CHORD_CP_SCALES("s1", "f1")
+      "and.pred e, e, p;\n\t"
+      CHORD_CP_SCALES("s2", "f2")
+      CHORD_CP_SCALES("s3", "f3")
+      "}" ::"l"(fb), "r"(sfb), "r"(wide ? 1u : 0u), "n"(kHalf >> 4)
+      : "memory");
+}
+#undef CHORD_MXF4_MMA
+#undef CHORD_CP_SCALES
+__device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
 }
 // Arrive on `bar` once every tcgen05.mma issued so far by this thread completes.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
@@ -80,6 +121,26 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
                : "memory");
 }
 
+__device__ __forceinline__ void tc_commit2_elect(uint64_t* bar0, uint64_t* bar1) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(smem_u32(bar0)),
+      "r"(smem_u32(bar1))
+      : "memory");
+}
+// 16 lanes x 32 columns -> 16 registers per thread: with g = lane / 4 and
+// t = lane % 4, registers {4i, 4i+1} are (lane g, columns 8i + 2t, 8i + 2t + 1)
+// and {4i+2, 4i+3} the same columns of lane g + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 // 32 lanes x 32 consecutive columns of 32-bit TMEM cells -> 32 registers per thread.
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -136,7 +197,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Descriptor of a scale block for tc_cp_scales: no swizzle, rows of 16 B,
+// Descriptor of a scale block for tcgen05.cp: no swizzle, rows of 16 B,
 // 8-row groups 128 B apart.
 __device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
   return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128u >> 4) << 32) |
