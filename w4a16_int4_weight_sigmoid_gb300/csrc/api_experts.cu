@@ -187,6 +187,9 @@ int chord_mxfp4_moe_gemm(const void* rows, size_t rows_bytes, const void* packed
   if (epilogue == CHORD_EPI_SILU_MUL && N % 16 != 0)
     return fail(CHORD_ERR_INVALID_ARG, "SiLU*mul needs N %% 16 == 0 (N=%d)", N);
   if (capacity > (1u << 30)) return fail(CHORD_ERR_INVALID_ARG, "%zu rows: too many", capacity);
+  // item and unit counts fit 32 bits with room
+  if (K > (1 << 24) || (capacity / 16 + E_local) * (static_cast<size_t>(N) / 256 + 1) > (1u << 30))
+    return fail(CHORD_ERR_INVALID_ARG, "K=%d or %zu rows x N=%d: too large", K, capacity, N);
   if (capacity == 0) return CHORD_OK;
   if (!rows || !packed_w || !expert_counts || !expert_offsets || !C) return fail(CHORD_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(rows) || !aligned16(packed_w) || !aligned16(C))

@@ -39,6 +39,8 @@
 // TMEM: accumulators from column 0, scales from column 480.
 // Every mbarrier wait is bounded; on a timeout the CTA records
 // CHORD_ERR_TIMEOUT, drains its own copies and MMAs, frees TMEM and exits.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "mxfp4.cuh"
@@ -91,7 +93,9 @@ struct MxArgs {
 
 __device__ __forceinline__ int row_tiles(int cnt) { return (cnt + kMaxTok - 1) / kMaxTok; }
 // Rows of an expert's row tiles: equal to within the rounding to 16.
-__device__ __forceinline__ int tile_rows(int cnt, int n_rt) { return ((cnt + n_rt - 1) / n_rt + 15) & ~15; }
+__device__ __forceinline__ int tile_rows(int cnt, int n_rt) {
+  return ((n_rt > 1 ? (cnt + n_rt - 1) / n_rt : cnt) + 15) & ~15;
+}
 
 // A role's walk over the CTA's segments (an item and a run of its K units):
 // its range of the cut items, then its whole items.  Items: experts in order;
@@ -99,12 +103,13 @@ __device__ __forceinline__ int tile_rows(int cnt, int n_rt) { return ((cnt + n_r
 struct Plan {
   const int *prefix, *cnts, *offs;   // shared: first item, rows and first row of each expert
   int E, n_tiles, units, items, cut; // cut: the items [0, cut) are cut into ranges
-  long long begin, end;              // this CTA's units of them
+  int begin, end;                    // this CTA's units of them
 };
 
+// Used by whole warps (the search for the expert is one ballot of 32).
 struct Walk {
   const Plan& p;
-  long long pos;                     // next unit of the range of cut items
+  int pos;                           // next unit of the range of cut items
   int item, e;                       // current item and its expert
   int row0, rows, pair, tiles, u0, u1;
   bool more;
@@ -112,10 +117,9 @@ struct Walk {
   __device__ explicit Walk(const Plan& plan) : p(plan), pos(plan.begin), item(-1), e(0) { advance(); }
   __device__ void advance() {
     if (pos < p.end) {
-      item = static_cast<int>(pos / p.units);
-      u0 = static_cast<int>(pos - static_cast<long long>(item) * p.units);
-      const long long rest = p.end - pos;
-      u1 = rest < p.units - u0 ? u0 + static_cast<int>(rest) : p.units;
+      item = pos / p.units;
+      u0 = pos - item * p.units;
+      u1 = min(p.units, u0 + p.end - pos);
       pos += u1 - u0;
     } else {
       item = item < p.cut ? p.cut + static_cast<int>(blockIdx.x) : item + static_cast<int>(gridDim.x);
@@ -125,13 +129,15 @@ struct Walk {
     more = item < p.items;
     if (!more) return;
     // the expert: largest e with prefix[e] <= item (items only grow)
-    if (p.prefix[e + 1] <= item) {
-      int lo = e + 1, hi = p.E - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.prefix[mid] <= item) lo = mid; else hi = mid - 1;
+    const int lane = threadIdx.x & 31;
+    while (true) {
+      const int at = e + 1 + lane;
+      const uint32_t past = __ballot_sync(0xffffffffu, at > p.E || p.prefix[at] > item);
+      if (past) {
+        e += __ffs(past) - 1;
+        break;
       }
-      e = lo;
+      e += 32;
     }
     const int cnt = p.cnts[e], n_rt = row_tiles(cnt), local = item - p.prefix[e];
     pair = n_rt == 1 ? local : local / n_rt;
@@ -273,11 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   // programmatic launch: nothing above touches global memory
   grid_dep_wait();
   grid_dep_launch();
-  if (tid == 0) {
-    const int32_t* h = reinterpret_cast<const int32_t*>(a.w);
-    hdr_ok = ld_ca(h) == static_cast<int>(kMxMagic) && ld_ca(h + 1) == static_cast<int>(kMxVersion) &&
-             ld_ca(h + 2) >= a.E && ld_ca(h + 3) == a.N && ld_ca(h + 4) == a.K && ld_ca(h + 5) == a.gate_up;
-    if (!hdr_ok) set_status(a.status, CHORD_ERR_PREPACK_MISMATCH);
+  uint4 h0{}, h1{};   // the weights' header, on its way while the counts are read
+  if (tid == kThreads - 1) {
+    h0 = ld_cg_v4(a.w);
+    h1 = ld_cg_v4(a.w + 16);
   }
 
   // first item of each expert, and the largest row tile: thread i covers
@@ -298,6 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     s_off[e] = off;
     mine += n_pairs * row_tiles(cnt);
     if (cnt) most = max(most, tile_rows(cnt, row_tiles(cnt)));
+  }
+  if (tid == kThreads - 1) {
+    hdr_ok = h0.x == kMxMagic && h0.y == kMxVersion && static_cast<int>(h0.z) >= a.E &&
+             static_cast<int>(h0.w) == a.N && static_cast<int>(h1.x) == a.K && static_cast<int>(h1.y) == a.gate_up;
+    if (!hdr_ok) set_status(a.status, CHORD_ERR_PREPACK_MISMATCH);
   }
   int inc = mine;
 #pragma unroll
@@ -342,11 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   // (measured 8 ns a token against 0.6 us), so u is at least the square root
   // of units * tok / 80.  No range is empty: an item's parts are in
   // consecutive CTAs.
-  const long long total = static_cast<long long>(plan.cut) * units;
+  const int total = plan.cut * units;   // the host keeps this far below 2^31
   const int least = max(1, static_cast<int>(sqrtf(units * tok / 80.f)));
-  const long long G = total > 0 ? max(1LL, min(static_cast<long long>(gridDim.x), total / least)) : 0;
-  plan.begin = blockIdx.x < G ? blockIdx.x * total / G : 0;
-  plan.end = blockIdx.x < G ? (blockIdx.x + 1) * total / G : 0;
+  const int G = total > 0 ? max(1, min(static_cast<int>(gridDim.x), total / least)) : 0;
+  auto range = [&](int c) { return static_cast<int>(static_cast<long long>(c) * total / G); };
+  plan.begin = blockIdx.x < G ? range(blockIdx.x) : 0;
+  plan.end = blockIdx.x < G ? range(blockIdx.x + 1) : 0;
   const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget / stage);
   const int n_acc = min(kMaxAcc, kSfCol / (kPair * tok));
   Walk w(plan);
@@ -490,8 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     const uint32_t out_stage = smem0 + kOutOff + (warp - kEpiWarp0) * kOutBytes;
     int acc = 0, use = 0;
     for (; w.more; w.advance()) {
-      // all epilogue warps go on or stop together: barriers follow
-      if (!epilogue_all(mbar_wait(&tfull[acc], use & 1, a.status))) {
+      // through the cut items the epilogue warps go on or stop together:
+      // barriers follow
+      bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], use & 1, a.status));
+      if (w.item < plan.cut) ok = epilogue_all(ok);
+      if (!ok) {
         abort_flag = 1;
         break;
       }
@@ -540,9 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       if (++acc == n_acc) acc = 0, ++use;
       if (whole) continue;
       // a cut item: the CTA that arrives last adds the parts in K order
-      const long long i0 = static_cast<long long>(w.item) * units;   // its units are [i0, i0 + units)
-      const int first = static_cast<int>(((i0 + 1) * G - 1) / total);
-      const int last = static_cast<int>(((i0 + units) * G - 1) / total);
+      const int i0 = w.item * units;                     // its units are [i0, i0 + units)
+      const int first = static_cast<int>((static_cast<long long>(i0 + 1) * G - 1) / total);
+      const int last = static_cast<int>((static_cast<long long>(i0 + units) * G - 1) / total);
       __threadfence();
       epilogue_all(true);
       if (tid == 32 * kEpiWarp0) {
@@ -553,33 +567,38 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       epilogue_all(true);
       if (!last_flag) continue;
       __threadfence();
-      // eight tokens at a time, six parts' loads in flight (parts past the
-      // last one and tokens past the rows are loaded again, not added)
-      constexpr int kParts = 6;
-      for (int c0 = 0; c0 < rows; c0 += 8) {
-        float f[8];
+      // Twelve 16-byte loads in flight: six parts of eight tokens, or twelve
+      // parts of four where an item has more (one token's items have ten).
+      // Parts past the last and tokens past the rows are loaded again, not added.
+      auto add = [&](auto parts_c, auto tokens_c) {
+        constexpr int kParts = decltype(parts_c)::value, kQuads = decltype(tokens_c)::value / 4;
+        for (int c0 = 0; c0 < rows; c0 += 4 * kQuads) {
+          float f[8] = {};
+          for (int p0 = first; p0 <= last; p0 += kParts) {
+            float4 x[kParts][kQuads];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] = 0.f;
-        const int c4 = c0 + 4 < rows ? 512 : 0;
-        for (int p0 = first; p0 <= last; p0 += kParts) {
-          float4 x[kParts][2];
+            for (int i = 0; i < kParts; ++i) {
+              const int p = min(p0 + i, last);
+              const float* src =
+                  a.partial + static_cast<size_t>(2 * p + (p == first)) * kSlotFloats + part + c0 * 128;
 #pragma unroll
-          for (int i = 0; i < kParts; ++i) {
-            const int p = min(p0 + i, last);
-            const float* src =
-                a.partial + static_cast<size_t>(2 * p + (p == first)) * kSlotFloats + part + c0 * 128;
-            x[i][0] = ld_cg_f4(src);
-            x[i][1] = ld_cg_f4(src + c4);
-          }
-#pragma unroll
-          for (int i = 0; i < kParts; ++i)
-            if (p0 + i <= last) {
-              f[0] += x[i][0].x, f[1] += x[i][0].y, f[2] += x[i][0].z, f[3] += x[i][0].w;
-              f[4] += x[i][1].x, f[5] += x[i][1].y, f[6] += x[i][1].z, f[7] += x[i][1].w;
+              for (int c = 0; c < kQuads; ++c) x[i][c] = ld_cg_f4(src + (c0 + 4 * c < rows ? 512 * c : 0));
             }
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+              if (p0 + i <= last)
+#pragma unroll
+                for (int c = 0; c < kQuads; ++c) {
+                  f[4 * c] += x[i][c].x, f[4 * c + 1] += x[i][c].y;
+                  f[4 * c + 2] += x[i][c].z, f[4 * c + 3] += x[i][c].w;
+                }
+          }
+          store_columns(a, f, out + static_cast<size_t>(c0) * a.ldc, kPair * w.pair + t, lrow,
+                        min(rows - c0, 4 * kQuads));
         }
-        store_columns(a, f, out + static_cast<size_t>(c0) * a.ldc, kPair * w.pair + t, lrow, rows - c0);
-      }
+      };
+      if (last - first < 6) add(std::integral_constant<int, 6>{}, std::integral_constant<int, 8>{});
+      else add(std::integral_constant<int, 12>{}, std::integral_constant<int, 4>{});
     }
   }
 
