@@ -10,16 +10,18 @@
 //     decoding and prefill.  Every SM draws its operands from L2 at about
 //     60 GB/s, which bounds all sizes above a few dozen rows per expert: a
 //     second weight tile on the same rows brings 66 KB for what took 100;
-//   * most items are dealt whole and in turn, so that CTAs at work at one time
+//   * items are dealt whole and in turn, so that CTAs at work at one time
 //     share weights and rows in L2 (a contiguous run of items per CTA spread
-//     the live weights over more than L2: many rows per expert 346 us).  Those
-//     that do not divide evenly among the CTAs come first, with one whole
-//     round more: their K units of 256 are cut into one range per CTA of equal
-//     length to within a unit.  One token's few items spread over all SMs in
-//     the same way.  An item that a range boundary cuts is summed by the CTA
+//     the live weights over more than L2: many rows per expert 346 us).  The
+//     items that do not divide evenly among the CTAs (or all, when there are
+//     fewer) come first and are divided further.  With up to kSplitTok rows
+//     per tile, along K: their K units of 256 are cut into ranges of equal
+//     length to within a unit, one per CTA, so one token's few items spread
+//     over all SMs; an item that a range boundary cuts is summed by the CTA
 //     that finishes last, from FP32 partials in workspace, in K order, so
-//     results do not depend on timing.  The extra round keeps the parts of an
-//     item at two or three (8 items left over in 19 parts each: 245 us);
+//     results do not depend on timing.  With more rows adding partials costs
+//     more than the work (8 prefill items in 19 parts each: 110 us), and they
+//     are divided into single weight tiles and runs of rows instead;
 //   * per unit one bulk copy brings the pair's weight rows with their scales
 //     (34 KB, contiguous, already swizzled), one or two the rows;
 //   * the rows' scales lie in row order in memory, and a row tile may start at
@@ -33,12 +35,16 @@
 //     has a weight row's values of two adjacent tokens (and gate and up of
 //     the same index), packs them and turns them with stmatrix.trans, so that
 //     C is written 16 bytes per lane;
+//   * one warp decodes the items and hands them to the others through a ring of
+//     eight words each (decoded by every role itself, finding an item took
+//     1600 cycles, as long as a short item's work);
 //   * stages and accumulators are laid out for the launch's largest row tile,
 //     which every CTA finds from the counts: decoding has five stages and four
 //     accumulators, a full tile three stages and one accumulator.
 // TMEM: accumulators from column 0, scales from column 480.
-// Every mbarrier wait is bounded; on a timeout the CTA records
-// CHORD_ERR_TIMEOUT, drains its own copies and MMAs, frees TMEM and exits.
+// Every mbarrier wait is bounded.  A warp whose wait runs out records
+// CHORD_ERR_TIMEOUT and stops, so the others' waits run out in turn; the CTA
+// drains its own copies and MMAs, frees TMEM and exits.
 #include <type_traits>
 
 #include "common.cuh"
@@ -53,7 +59,10 @@ constexpr int kMaxTok = 224;
 constexpr int kPair = 2;               // weight tiles per item
 constexpr int kMaxStages = 5, kMaxAcc = 4;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 4 * kPair, kEpiThreads = 32 * kEpiWarps;
-constexpr int kThreads = 32 * kEpiWarp0 + kEpiThreads;
+constexpr int kItemWarp = kEpiWarp0 + kEpiWarps;
+constexpr int kThreads = 32 * (kItemWarp + 1);
+constexpr int kItemSlots = 8;
+constexpr int kItemReaders = 1 + kPair + 1 + kEpiWarps;   // copies, MMAs, scales, epilogue
 constexpr int kMaxExperts = 1024;
 // stage: weight tiles with their scales | rows
 constexpr int kBOff = kPair * kMxUnitBytes;
@@ -70,7 +79,9 @@ constexpr int kSmemBytes = kOutOff + kEpiWarps * kOutBytes + 1024;
 constexpr int kMmaWarp0 = 1, kSfWarp = kMmaWarp0 + kPair;
 constexpr int kSfCol = kPair * kMaxTok, kSfCols = 32;   // per tile: SFA at +0 and +8 (alternate units), SFB at +16
 constexpr int kTmemCols = 512;
-constexpr int kSlotFloats = kPair * kMaxTok * 128;   // one CTA's part of a cut item
+constexpr int kSplitTok = 48;          // largest row tile whose items are cut along K
+constexpr int kSlotFloats = kPair * kSplitTok * 128;   // one CTA's part of a cut item
+static_assert(kSplitTok % 16 == 0, "whole runs of rows");
 static_assert(kSfCol + kPair * kSfCols <= kTmemCols, "TMEM budget");
 static_assert(stage_bytes(16) % 1024 == 0 && kMaxTok % 16 == 0 && kMaxTok <= 256, "stage layout");
 static_assert(kMaxStages * stage_bytes(16) <= kStageBudget, "stage budget");
@@ -87,48 +98,89 @@ struct MxArgs {
   float* partial;        // [2 * kMxMaxCtas][tile of the pair][tokens / 4][128 weight rows][4]
   uint16_t* C;
   int* status;
-  int E, N, K, ldc, capacity, n_tiles, gate_up;
+  int E, N, K, ldc, capacity, n_tiles, max_tok;
   size_t rows_padded;
 };
 
-__device__ __forceinline__ int row_tiles(int cnt) { return (cnt + kMaxTok - 1) / kMaxTok; }
+// Largest row tile.  A full tile's accumulators fill TMEM, so its epilogue
+// (3.2 us) is not hidden; tiles of 96 have two accumulators and four stages,
+// but draw the weights from L2 twice as often (0.8 us against 0.6 us per unit
+// and 224 rows).  They even out at about 15 units.
+constexpr int kShortTok = 96, kShortUnits = 14;
+inline int largest_tile(int units) { return units <= kShortUnits ? kShortTok : kMaxTok; }
+__device__ __forceinline__ int row_tiles(int cnt, int max_tok) { return (cnt + max_tok - 1) / max_tok; }
 // Rows of an expert's row tiles: equal to within the rounding to 16.
 __device__ __forceinline__ int tile_rows(int cnt, int n_rt) {
   return ((n_rt > 1 ? (cnt + n_rt - 1) / n_rt : cnt) + 15) & ~15;
 }
 
-// A role's walk over the CTA's segments (an item and a run of its K units):
-// its range of the cut items, then its whole items.  Items: experts in order;
-// per expert, weight tile pairs; per pair, row tiles.
+// A role's walk over the CTA's segments (an item or a part of one, and a run
+// of its K units): its share of the divided items [0, cut), then its whole
+// items.  Items: experts in order; per expert, weight tile pairs; per pair,
+// row tiles.
 struct Plan {
   const int *prefix, *cnts, *offs;   // shared: first item, rows and first row of each expert
-  int E, n_tiles, units, items, cut; // cut: the items [0, cut) are cut into ranges
-  int begin, end;                    // this CTA's units of them
+  int E, n_tiles, units, max_tok, items, cut;
+  int begin, end;                    // along K: this CTA's units of the divided items
+  int chunks;                        // by rows: runs per single tile (0: along K)
 };
 
-// Used by whole warps (the search for the expert is one ballot of 32).
+// A segment as the roles read it (two 16-byte words).
+struct alignas(16) Seg {
+  int item, e, row0, rows;           // rows 0: the end of the work
+  int tile, tiles, u0, u1;           // first weight tile and tiles; K units
+};
+
+// Run by the item warp (the search for the expert is one ballot of 32).
 struct Walk {
   const Plan& p;
-  int pos;                           // next unit of the range of cut items
-  int item, e;                       // current item and its expert
-  int row0, rows, pair, tiles, u0, u1;
+  int pos;                           // next unit, or next (item, tile, run of rows), of the divided items
+  int item, e;
+  int row0, rows, tile, tiles, u0, u1;
   bool more;
 
-  __device__ explicit Walk(const Plan& plan) : p(plan), pos(plan.begin), item(-1), e(0) { advance(); }
+  __device__ explicit Walk(const Plan& plan)
+      : p(plan), pos(plan.chunks ? static_cast<int>(blockIdx.x) : plan.begin), item(-1), e(0) {
+    advance();
+  }
   __device__ void advance() {
-    if (pos < p.end) {
-      item = pos / p.units;
-      u0 = pos - item * p.units;
-      u1 = min(p.units, u0 + p.end - pos);
-      pos += u1 - u0;
-    } else {
-      item = item < p.cut ? p.cut + static_cast<int>(blockIdx.x) : item + static_cast<int>(gridDim.x);
+    if (item >= p.cut) {             // whole items, the common case
+      item += gridDim.x;
+      more = item < p.items;
+      if (more) locate();
+      return;
+    }
+    do {
+      int part = -1;
       u0 = 0;
       u1 = p.units;
-    }
-    more = item < p.items;
-    if (!more) return;
-    // the expert: largest e with prefix[e] <= item (items only grow)
+      if (p.chunks && pos < kPair * p.chunks * p.cut) {
+        item = pos / (kPair * p.chunks);
+        part = pos - item * (kPair * p.chunks);
+        pos += gridDim.x;
+      } else if (!p.chunks && pos < p.end) {
+        item = pos / p.units;
+        u0 = pos - item * p.units;
+        u1 = min(p.units, u0 + p.end - pos);
+        pos += u1 - u0;
+      } else {
+        item = p.cut + static_cast<int>(blockIdx.x);
+      }
+      more = item < p.items;
+      if (!more) return;
+      locate();
+      if (part >= 0) {               // one tile, one run of rows
+        const int t = part / p.chunks, c = part - t * p.chunks;
+        const int run = ((rows + p.chunks - 1) / p.chunks + 15) & ~15;
+        tile += t;
+        tiles = min(1, tiles - t);
+        row0 += c * run;
+        rows = min(run, rows - c * run);
+      }
+    } while (rows <= 0 || tiles <= 0);
+  }
+  // The item's expert: the largest e with prefix[e] <= item (items only grow).
+  __device__ void locate() {
     const int lane = threadIdx.x & 31;
     while (true) {
       const int at = e + 1 + lane;
@@ -139,12 +191,38 @@ struct Walk {
       }
       e += 32;
     }
-    const int cnt = p.cnts[e], n_rt = row_tiles(cnt), local = item - p.prefix[e];
-    pair = n_rt == 1 ? local : local / n_rt;
-    const int rt = local - pair * n_rt, per = tile_rows(cnt, n_rt);
-    row0 = p.offs[e] + rt * per;
-    rows = min(per, cnt - rt * per);
-    tiles = min(kPair, p.n_tiles - kPair * pair);
+    const int cnt = p.cnts[e], local = item - p.prefix[e];
+    row0 = p.offs[e];
+    rows = cnt;
+    tile = kPair * local;
+    if (cnt > p.max_tok) {           // several row tiles (divisions: about 100 cycles each)
+      const int n_rt = row_tiles(cnt, p.max_tok), pair = local / n_rt;
+      const int rt = local - pair * n_rt, per = tile_rows(cnt, n_rt);
+      row0 += rt * per;
+      rows = min(per, cnt - rt * per);
+      tile = kPair * pair;
+    }
+    tiles = min(kPair, p.n_tiles - tile);
+  }
+};
+
+// A role's end of the item ring.
+struct ItemRing {
+  uint64_t *full, *empty;
+  const Seg* slots;
+  int slot, ph;
+  // The next segment: false at the end of the work or on a timeout.  All
+  // lanes of the calling warp take it; lane 0 releases the slot.
+  __device__ __forceinline__ bool next(Seg& s, int* status) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], ph, status))) return false;
+    const int4* src = reinterpret_cast<const int4*>(&slots[slot]);
+    const int4 lo = src[0], hi = src[1];
+    s.item = lo.x, s.e = lo.y, s.row0 = lo.z, s.rows = lo.w;
+    s.tile = hi.x, s.tiles = hi.y, s.u0 = hi.z, s.u1 = hi.w;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[slot]);
+    if (++slot == kItemSlots) slot = 0, ph ^= 1;
+    return s.rows > 0;
   }
 };
 
@@ -182,13 +260,14 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, ui
 // Up to 32 tokens of a finished item to C: this warp's accumulators of its 32
 // weight rows (lo: rows 0-15 of the lane quarter, hi: rows 16-31, gate and up),
 // `n` tokens at `out`, through the warp's own staging rows.
+template <bool kGateUp>
 __device__ __forceinline__ void store_tokens(const MxArgs& a, const uint32_t (&lo)[16], const uint32_t (&hi)[16],
                                              uint16_t* out, uint32_t stage_s, int tile, int q, int lane, int n) {
   // lane 8 i + c: token c of its 8-token group, weight rows 8 (i & 1) on
   const uint32_t dst = stage_s + ((lane & 7) + 8 * (lane >> 4)) * kOutPitch + ((lane >> 3) & 1) * 16;
   // 16 bytes (8 columns of C) per lane: 2 or 4 lanes per token
-  const int sh = a.gate_up ? 1 : 2, part = lane & ((1 << sh) - 1);
-  const int col = (a.gate_up ? 64 * tile + 16 * q : kMxTileRows * tile + 32 * q) + 8 * part;
+  const int sh = kGateUp ? 1 : 2, part = lane & ((1 << sh) - 1);
+  const int col = (kGateUp ? 64 * tile + 16 * q : kMxTileRows * tile + 32 * q) + 8 * part;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {   // tokens 16 p .. 16 p + 15
     uint32_t l[4], h[4];          // [token group of 8][weight rows 0-7, 8-15]
@@ -197,11 +276,11 @@ __device__ __forceinline__ void store_tokens(const MxArgs& a, const uint32_t (&l
       const int r = 8 * p + 2 * i;
       const float l0 = __uint_as_float(lo[r]), l1 = __uint_as_float(lo[r + 1]);
       const float h0 = __uint_as_float(hi[r]), h1 = __uint_as_float(hi[r + 1]);
-      l[i] = a.gate_up ? bf16_pair(silu_mul(l0, h0), silu_mul(l1, h1)) : bf16_pair(l0, l1);
+      l[i] = kGateUp ? bf16_pair(silu_mul(l0, h0), silu_mul(l1, h1)) : bf16_pair(l0, l1);
       h[i] = bf16_pair(h0, h1);
     }
     stmatrix_x4_trans(dst, l[0], l[1], l[2], l[3]);
-    if (!a.gate_up) stmatrix_x4_trans(dst + 32, h[0], h[1], h[2], h[3]);
+    if (!kGateUp) stmatrix_x4_trans(dst + 32, h[0], h[1], h[2], h[3]);
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -221,9 +300,10 @@ __device__ __forceinline__ void store_tokens(const MxArgs& a, const uint32_t (&l
 
 // Eight tokens of a summed item (this lane's weight row `lrow` of tile
 // `tile`), `n` of them valid, at `out`.
+template <bool kGateUp>
 __device__ __forceinline__ void store_columns(const MxArgs& a, const float (&v)[8], uint16_t* out, int tile, int lrow,
                                               int n) {
-  if (a.gate_up) {
+  if (kGateUp) {
     // lanes 0-15 hold gate rows, 16-31 the up rows of the same indices: of
     // two columns, the low lanes finish the first and the high lanes the second
     const bool up = lrow & 16;
@@ -243,23 +323,24 @@ __device__ __forceinline__ void store_columns(const MxArgs& a, const float (&v)[
   }
 }
 
+template <bool kGateUp>
 __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], sf_full[kSfSlots], sf_empty[kSfSlots];
   __shared__ __align__(8) uint64_t tfull[kMaxAcc], tempty[kMaxAcc], done_bar[kPair];
+  __shared__ __align__(8) uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+  __shared__ Seg item_slots[kItemSlots];
   __shared__ uint32_t tmem_base_s;
   __shared__ int prefix[kMaxExperts + 1];
   __shared__ int s_cnt[kMaxExperts], s_off[kMaxExperts];
   __shared__ int warp_sum[kThreads / 32], warp_max[kThreads / 32];
   __shared__ int hdr_ok, last_flag;
-  __shared__ volatile int abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (smem0 - smem_u32(smem_raw));
 
   if (tid == 0) {
-    abort_flag = 0;
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kPair);
@@ -273,6 +354,10 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       mbar_init(&tempty[b], kEpiWarps);
     }
     for (int t = 0; t < kPair; ++t) mbar_init(&done_bar[t], 1);
+    for (int q = 0; q < kItemSlots; ++q) {
+      mbar_init(&item_full[q], 1);
+      mbar_init(&item_empty[q], kItemReaders);
+    }
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base_s, kTmemCols);
@@ -301,12 +386,13 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     }
     s_cnt[e] = cnt;
     s_off[e] = off;
-    mine += n_pairs * row_tiles(cnt);
-    if (cnt) most = max(most, tile_rows(cnt, row_tiles(cnt)));
+    const int n_rt = row_tiles(cnt, a.max_tok);
+    mine += n_pairs * n_rt;
+    if (cnt) most = max(most, tile_rows(cnt, n_rt));
   }
   if (tid == kThreads - 1) {
     hdr_ok = h0.x == kMxMagic && h0.y == kMxVersion && static_cast<int>(h0.z) >= a.E &&
-             static_cast<int>(h0.w) == a.N && static_cast<int>(h1.x) == a.K && static_cast<int>(h1.y) == a.gate_up;
+             static_cast<int>(h0.w) == a.N && static_cast<int>(h1.x) == a.K && static_cast<int>(h1.y) == (kGateUp ? 1 : 0);
     if (!hdr_ok) set_status(a.status, CHORD_ERR_PREPACK_MISMATCH);
   }
   int inc = mine;
@@ -333,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     const int e = tid * per + i;
     if (e >= a.E) break;
     prefix[e] = run;
-    run += n_pairs * row_tiles(s_cnt[e]);
+    run += n_pairs * row_tiles(s_cnt[e], a.max_tok);
   }
   if (tid == kThreads - 1) prefix[a.E] = run;   // the last thread ends at the total
   __syncthreads();
@@ -343,16 +429,19 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   const int units = mx_units(a.K);
   Plan plan;
   plan.prefix = prefix, plan.cnts = s_cnt, plan.offs = s_off;
-  plan.E = a.E, plan.n_tiles = a.n_tiles, plan.units = units;
+  plan.E = a.E, plan.n_tiles = a.n_tiles, plan.units = units, plan.max_tok = a.max_tok;
   plan.items = hdr_ok ? prefix[a.E] : 0;
   plan.cut = plan.items % static_cast<int>(gridDim.x);
-  if (plan.cut > 0 && plan.items > plan.cut) plan.cut += gridDim.x;
-  // CTAs that share the cut items.  A range of u units costs u units' time and
-  // its item units / u parts to add; a part takes tok / 80 of a unit's time
-  // (measured 8 ns a token against 0.6 us), so u is at least the square root
-  // of units * tok / 80.  No range is empty: an item's parts are in
-  // consecutive CTAs.
-  const int total = plan.cut * units;   // the host keeps this far below 2^31
+  // Divided by rows: about one (tile, run of rows) for each CTA.  (With a
+  // single unit nothing is cut along K and there are no partials.)
+  plan.chunks = tok > kSplitTok && units > 1 && plan.cut > 0
+                    ? min(max(static_cast<int>(gridDim.x) / (kPair * plan.cut), 1), tok / 16) : 0;
+  // Divided along K.  A range of u units costs u units' time and its item
+  // units / u parts to add; a part takes tok / 80 of a unit's time (measured
+  // 8 ns a token against 0.6 us), so u is at least the square root of
+  // units * tok / 80.  No range is empty: an item's parts are in consecutive
+  // CTAs.
+  const int total = plan.chunks ? 0 : plan.cut * units;   // the host keeps this far below 2^31
   const int least = max(1, static_cast<int>(sqrtf(units * tok / 80.f)));
   const int G = total > 0 ? max(1, min(static_cast<int>(gridDim.x), total / least)) : 0;
   auto range = [&](int c) { return static_cast<int>(static_cast<long long>(c) * total / G); };
@@ -360,37 +449,36 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   plan.end = blockIdx.x < G ? range(blockIdx.x + 1) : 0;
   const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget / stage);
   const int n_acc = min(kMaxAcc, kSfCol / (kPair * tok));
-  Walk w(plan);
+  ItemRing items{item_full, item_empty, item_slots, 0, 0};
+  Seg w;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- copies
     // The whole warp runs the loop, one elected lane issues.
     const size_t tile_bytes = static_cast<size_t>(units) * kMxUnitBytes;
     int it = 0, st = 0, ph = 0;
-    for (; w.more && !abort_flag; w.advance()) {
-      const int n16 = __shfl_sync(0xffffffffu, (w.rows + 15) & ~15, 0);
-      const int tiles = __shfl_sync(0xffffffffu, w.tiles, 0);
-      const int u1 = __shfl_sync(0xffffffffu, w.u1, 0);
-      int u = __shfl_sync(0xffffffffu, w.u0, 0);
+    bool ok = true;
+    while (ok && items.next(w, a.status)) {
+      const int n16 = (w.rows + 15) & ~15;
+      int u = w.u0;
+      const int t0 = w.tile % kPair;
+      const int step = min(kPair, a.n_tiles - (w.tile - t0)) * kMxUnitBytes;   // the pair's unit
       const uint8_t* wsrc = a.w + kPackHeaderBytes +
-                            (static_cast<size_t>(w.e) * a.n_tiles + kPair * w.pair) * tile_bytes +
-                            static_cast<size_t>(u) * tiles * kMxUnitBytes;
+                            (static_cast<size_t>(w.e) * a.n_tiles + w.tile - t0) * tile_bytes +
+                            static_cast<size_t>(u) * step + t0 * kMxUnitBytes;
       // the tile's rows: up to the end of their slab, then the next one's
-      const int head = min(n16, kMxSlabRows - __shfl_sync(0xffffffffu, w.row0, 0) % kMxSlabRows);
+      const int head = min(n16, kMxSlabRows - w.row0 % kMxSlabRows);
       const uint8_t* rsrc = a.rows + mx_row_place(u, units, w.row0) * kMxRowBytes;
       const uint8_t* rsrc2 = a.rows + mx_row_place(u, units, w.row0 + head) * kMxRowBytes;
-      for (; u < u1; ++u, ++it) {
-        if (it >= n_stages && !__all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, a.status))) {
-          abort_flag = 1;
-          break;
-        }
+      for (; u < w.u1; ++u, ++it) {
+        if (it >= n_stages && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, a.status)))) break;
         const uint32_t dst = smem0 + st * stage;
-        mbar_arrive_expect_tx_elect(&full[st], tiles * kMxUnitBytes + n16 * kMxRowBytes);
-        bulk_g2s_elect(dst, wsrc, tiles * kMxUnitBytes, &full[st]);
+        mbar_arrive_expect_tx_elect(&full[st], w.tiles * kMxUnitBytes + n16 * kMxRowBytes);
+        bulk_g2s_elect(dst, wsrc, w.tiles * kMxUnitBytes, &full[st]);
         bulk_g2s_elect(dst + kBOff, rsrc, head * kMxRowBytes, &full[st]);
         if (head < n16)
           bulk_g2s_elect(dst + kBOff + head * kMxRowBytes, rsrc2, (n16 - head) * kMxRowBytes, &full[st]);
-        wsrc += tiles * kMxUnitBytes;
+        wsrc += step;
         rsrc += kMxSlabRows * kMxRowBytes;
         rsrc2 += kMxSlabRows * kMxRowBytes;
         if (++st == n_stages) st = 0, ph ^= 1;
@@ -404,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     // the wait always ends.
     const uint8_t* row_scales = a.rows + units * a.rows_padded * kMxRowBytes;
     int issued = 0, signalled = 0, in = 0, in_ph = 0, out = 0;
+    bool ok = true;
     auto signal = [&] {
       fence_proxy_async_smem();
       __syncwarp();
@@ -411,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       ++signalled;
       if (++out == kSfSlots) out = 0;
     };
-    for (; w.more && !abort_flag; w.advance()) {
+    while (ok && items.next(w, a.status)) {
       const int n16 = (w.rows + 15) & ~15;
       // this lane's rows of the tile, 32 apart: those below `head` are in the
       // first slab, the others in the next
@@ -419,10 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       const uint8_t* src = row_scales + mx_row_place(w.u0, units, w.row0 + lane) * kMxRowScales;
       const size_t slab = static_cast<size_t>(units - 1) * kMxSlabRows * kMxRowScales;
       for (int u = w.u0; u < w.u1; ++u, ++issued) {
-        if (issued >= kSfSlots && !__all_sync(0xffffffffu, mbar_wait(&sf_empty[in], in_ph ^ 1, a.status))) {
-          abort_flag = 1;
+        if (issued >= kSfSlots && !(ok = __all_sync(0xffffffffu, mbar_wait(&sf_empty[in], in_ph ^ 1, a.status))))
           break;
-        }
         const uint32_t dst = smem0 + kSfOff + in * kSfSlotBytes + lane * 16;
 #pragma unroll
         for (int i = 0; i < (kMaxTok + 31) / 32; ++i) {
@@ -443,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       }
     }
     cp_async_wait<0>();
-    while (signalled < issued && !abort_flag) signal();
+    while (ok && signalled < issued) signal();
   } else if (warp >= kMmaWarp0 && warp < kMmaWarp0 + kPair) {
     // ------------------------------------------------------------------ MMAs
     // One warp per weight tile; the whole warp runs the loop, one elected
@@ -453,24 +540,17 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     int st = 0, ph = 0, slot = 0, sf_ph = 0, acc = 0, use = 0;
     const uint32_t sfb = tmem_base + kSfCol + t * kSfCols + 16;
     uint32_t sfa = sfb - 16;
-    bool issued = false;
-    for (; w.more && !abort_flag; w.advance()) {
-      const int n16 = __shfl_sync(0xffffffffu, (w.rows + 15) & ~15, 0);
-      const bool active = t < __shfl_sync(0xffffffffu, w.tiles, 0);
-      int left = __shfl_sync(0xffffffffu, w.u1 - w.u0, 0);
-      if (use >= 1 && !__all_sync(0xffffffffu, mbar_wait(&tempty[acc], (use - 1) & 1, a.status))) {
-        abort_flag = 1;
-        break;
-      }
-      tc_fence_after();
+    bool issued = false, ok = true;
+    while (ok && items.next(w, a.status)) {
+      const int n16 = (w.rows + 15) & ~15;
+      const bool active = t < w.tiles;
       const uint32_t d = tmem_base + (acc * kPair + t) * tok;
       const uint32_t idesc0 = idesc_mxf4(n16, 0), idesc2 = idesc_mxf4(n16, 2);
       uint32_t accumulate = 0;
-      for (; left > 0; --left) {
-        if (!__all_sync(0xffffffffu, mbar_wait2(&full[st], ph, &sf_full[slot], sf_ph, a.status))) {
-          abort_flag = 1;
-          break;
-        }
+      if (use >= 1) ok = mbar_wait(&tempty[acc], (use - 1) & 1, a.status);
+      for (int left = w.u1 - w.u0; left > 0; --left) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait2(&full[st], ph, &sf_full[slot], sf_ph, a.status));
+        if (!ok) break;
         tc_fence_after();
         if (active) {
           const uint32_t base = smem0 + st * stage, wt = base + t * kMxUnitBytes;
@@ -485,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
         if (++st == n_stages) st = 0, ph ^= 1;
         if (++slot == kSfSlots) slot = 0, sf_ph ^= 1;
       }
-      if (abort_flag) break;
+      if (!ok) break;
       tc_commit_elect(&tfull[acc]);
       if (++acc == n_acc) acc = 0, ++use;
     }
@@ -494,48 +574,63 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       tc_commit_elect(&done_bar[t]);
       mbar_wait(&done_bar[t], 0, a.status);
     }
-  } else if (warp >= kEpiWarp0) {
+  } else if (warp == kItemWarp) {
+    // ----------------------------------------------------------------- items
+    Walk walk(plan);
+    int slot = 0, ph = 0;
+    for (bool first = true, more = true; more;) {
+      if (!first && !__all_sync(0xffffffffu, mbar_wait_backoff(&item_empty[slot], ph ^ 1, a.status))) break;
+      more = walk.more;
+      if (lane == 0) {
+        Seg& s = item_slots[slot];
+        s.item = walk.item, s.e = walk.e, s.row0 = walk.row0, s.rows = more ? walk.rows : 0;
+        s.tile = walk.tile, s.tiles = walk.tiles, s.u0 = walk.u0, s.u1 = walk.u1;
+        mbar_arrive(&item_full[slot]);   // release: the segment is visible to the waiters
+      }
+      if (more) walk.advance();
+      if (++slot == kItemSlots) slot = 0, ph ^= 1, first = false;
+    }
+  } else {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3, lrow = 32 * q + lane;        // TMEM lane quarter; weight row of the tile
     const int t = (warp - kEpiWarp0) / 4;                // weight tile of the pair
     const uint32_t out_stage = smem0 + kOutOff + (warp - kEpiWarp0) * kOutBytes;
     int acc = 0, use = 0;
-    for (; w.more; w.advance()) {
-      // through the cut items the epilogue warps go on or stop together:
-      // barriers follow
-      bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], use & 1, a.status));
-      if (w.item < plan.cut) ok = epilogue_all(ok);
-      if (!ok) {
-        abort_flag = 1;
-        break;
+    // A wait that ran out ends a warp; through the segments cut along K, whose
+    // handling has barriers, the epilogue warps end together.
+    int cut_left = plan.end > plan.begin ? (plan.end - 1) / units - plan.begin / units + 1 : 0;
+    while (true) {
+      const bool on = items.next(w, a.status);
+      bool ok = on && __all_sync(0xffffffffu, mbar_wait(&tfull[acc], use & 1, a.status));
+      if (cut_left > 0) {
+        --cut_left;
+        ok = epilogue_all(ok);
       }
+      if (!ok) break;
       tc_fence_after();
       const int rows = t < w.tiles ? w.rows : 0;
       const uint32_t taddr = tmem_base + (acc * kPair + t) * tok + (static_cast<uint32_t>(32 * q) << 16);
       uint16_t* out = a.C + static_cast<size_t>(w.row0) * a.ldc;
       const bool whole = w.u0 == 0 && w.u1 == units;
-      const size_t part = static_cast<size_t>(t) * kMaxTok * 128 + 4 * lrow;
+      const size_t part = static_cast<size_t>(t) * kSplitTok * 128 + 4 * lrow;
       float* mine_p = a.partial + static_cast<size_t>(2 * blockIdx.x + (w.u0 == 0)) * kSlotFloats + part;
       if (whole) {
         // the next 32 tokens' accumulators are on their way while these go out
-        uint32_t v[2][2][16];
-        auto load = [&](int c0, uint32_t(&x)[2][16]) {
-          tmem_ld_16x256b_x4(taddr + c0, x[0]);
-          tmem_ld_16x256b_x4(taddr + c0 + (16u << 16), x[1]);
+        uint32_t next[2][16];
+        auto load = [&](int c0) {
+          tmem_ld_16x256b_x4(taddr + c0, next[0]);
+          tmem_ld_16x256b_x4(taddr + c0 + (16u << 16), next[1]);
         };
-        auto store = [&](int c0, const uint32_t(&x)[2][16]) {
-          store_tokens(a, x[0], x[1], out + static_cast<size_t>(c0) * a.ldc, out_stage, kPair * w.pair + t, q, lane,
-                       rows - c0);
-        };
-        if (rows > 0) load(0, v[0]);
-        for (int c0 = 0; c0 < rows; c0 += 64) {
+        if (rows > 0) load(0);
+#pragma unroll 1
+        for (int c0 = 0; c0 < rows; c0 += 32) {
           tmem_ld_wait();
-          if (c0 + 32 < rows) load(c0 + 32, v[1]);
-          store(c0, v[0]);
-          if (c0 + 32 >= rows) break;
-          tmem_ld_wait();
-          if (c0 + 64 < rows) load(c0 + 64, v[0]);
-          store(c0 + 32, v[1]);
+          uint32_t v[2][16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[0][i] = next[0][i], v[1][i] = next[1][i];
+          if (c0 + 32 < rows) load(c0 + 32);
+          store_tokens<kGateUp>(a, v[0], v[1], out + static_cast<size_t>(c0) * a.ldc, out_stage, w.tile + t, q, lane,
+                                rows - c0);
         }
       } else {
         for (int c0 = 0; c0 < rows; c0 += 32) {
@@ -593,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
                   f[4 * c + 2] += x[i][c].z, f[4 * c + 3] += x[i][c].w;
                 }
           }
-          store_columns(a, f, out + static_cast<size_t>(c0) * a.ldc, kPair * w.pair + t, lrow,
+          store_columns<kGateUp>(a, f, out + static_cast<size_t>(c0) * a.ldc, w.tile + t, lrow,
                         min(rows - c0, 4 * kQuads));
         }
       };
@@ -625,9 +720,10 @@ cudaError_t mxfp4_gemm_launch(const uint8_t* rows, const uint8_t* w, int E, int 
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kMxMaxCtas * sizeof(int));
   a.C = C, a.status = status;
   a.E = E, a.N = N, a.K = K, a.ldc = gate_up ? N / 2 : N, a.capacity = capacity;
-  a.n_tiles = mx_tiles(N), a.gate_up = gate_up ? 1 : 0;
+  a.n_tiles = mx_tiles(N), a.max_tok = largest_tile(mx_units(K));
   a.rows_padded = mx_rows_padded(capacity);
-  cudaError_t err = ensure_smem_limit<mxfp4_gemm_kernel>(kSmemBytes);
+  cudaError_t err = gate_up ? ensure_smem_limit<mxfp4_gemm_kernel<true>>(kSmemBytes)
+                            : ensure_smem_limit<mxfp4_gemm_kernel<false>>(kSmemBytes);
   if (err != cudaSuccess) return err;
   static int sms[64] = {0};
   int dev = 0;
@@ -638,7 +734,7 @@ cudaError_t mxfp4_gemm_launch(const uint8_t* rows, const uint8_t* w, int E, int 
     err = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
   }
-  return launch_kernel(mxfp4_gemm_kernel, dim3(sms[dev] < kMxMaxCtas ? sms[dev] : kMxMaxCtas), dim3(kThreads),
+  return launch_kernel(gate_up ? mxfp4_gemm_kernel<true> : mxfp4_gemm_kernel<false>, dim3(sms[dev] < kMxMaxCtas ? sms[dev] : kMxMaxCtas), dim3(kThreads),
                        kSmemBytes, st, true, a);
 }
 
