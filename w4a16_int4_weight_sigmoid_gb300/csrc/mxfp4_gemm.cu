@@ -71,9 +71,9 @@ constexpr int kStageBudget = 3 * stage_bytes(kMaxTok);
 // ring of the rows' scales in block layout: two K halves of up to 256 rows
 constexpr int kSfSlots = 6, kSfAhead = 4;   // slots, and units in flight (fewer)
 constexpr int kSfbHalf = 1024, kSfSlotBytes = 2 * kSfbHalf;
-// an epilogue warp's 16 tokens x 32 weight rows on their way to C; the pitch
+// an epilogue warp's 32 tokens x 32 weight rows on their way to C; the pitch
 // of 80 bytes spreads stmatrix's and the reads' 16-byte parts over the banks
-constexpr int kOutPitch = 80, kOutBytes = 16 * kOutPitch;
+constexpr int kOutPitch = 80, kOutBytes = 32 * kOutPitch;
 constexpr int kSfOff = kStageBudget, kOutOff = kSfOff + kSfSlots * kSfSlotBytes;
 constexpr int kSmemBytes = kOutOff + kEpiWarps * kOutBytes + 1024;
 constexpr int kMmaWarp0 = 1, kSfWarp = kMmaWarp0 + kPair;
@@ -87,7 +87,7 @@ static_assert(stage_bytes(16) % 1024 == 0 && kMaxTok % 16 == 0 && kMaxTok <= 256
 static_assert(kMaxStages * stage_bytes(16) <= kStageBudget, "stage budget");
 static_assert(kSfAhead < kSfSlots, "a slot is reused after its unit was signalled");
 static_assert(kSfWarp + 1 <= kEpiWarp0 && kEpiWarp0 % 4 == 0, "warp roles; warp index selects the TMEM lane quarter");
-static_assert(kSmemBytes + (3 * kMaxExperts + 1) * 4 + 1024 <= 232448, "shared memory budget");
+static_assert(kSmemBytes + (kMaxExperts + 1) * 4 + 1024 <= 232448, "shared memory budget");
 
 struct MxArgs {
   const uint8_t* w;
@@ -119,7 +119,8 @@ __device__ __forceinline__ int tile_rows(int cnt, int n_rt) {
 // items.  Items: experts in order; per expert, weight tile pairs; per pair,
 // row tiles.
 struct Plan {
-  const int *prefix, *cnts, *offs;   // shared: first item, rows and first row of each expert
+  const int* prefix;                 // shared: first item of each expert
+  const int32_t *cnts, *offs;        // rows and first row of each expert (checked where it has items)
   int E, n_tiles, units, max_tok, items, cut;
   int begin, end;                    // along K: this CTA's units of the divided items
   int chunks;                        // by rows: runs per single tile (0: along K)
@@ -191,8 +192,8 @@ struct Walk {
       }
       e += 32;
     }
-    const int cnt = p.cnts[e], local = item - p.prefix[e];
-    row0 = p.offs[e];
+    const int cnt = ld_ca(p.cnts + e), local = item - p.prefix[e];
+    row0 = ld_ca(p.offs + e);
     rows = cnt;
     tile = kPair * local;
     if (cnt > p.max_tok) {           // several row tiles (divisions: about 100 cycles each)
@@ -266,7 +267,8 @@ __device__ __forceinline__ void store_tokens(const MxArgs& a, const uint32_t (&l
   // lane 8 i + c: token c of its 8-token group, weight rows 8 (i & 1) on
   const uint32_t dst = stage_s + ((lane & 7) + 8 * (lane >> 4)) * kOutPitch + ((lane >> 3) & 1) * 16;
   // 16 bytes (8 columns of C) per lane: 2 or 4 lanes per token
-  const int sh = kGateUp ? 1 : 2, part = lane & ((1 << sh) - 1);
+  constexpr int sh = kGateUp ? 1 : 2;
+  const int part = lane & ((1 << sh) - 1);
   const int col = (kGateUp ? 64 * tile + 16 * q : kMxTileRows * tile + 32 * q) + 8 * part;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {   // tokens 16 p .. 16 p + 15
@@ -279,23 +281,25 @@ __device__ __forceinline__ void store_tokens(const MxArgs& a, const uint32_t (&l
       l[i] = kGateUp ? bf16_pair(silu_mul(l0, h0), silu_mul(l1, h1)) : bf16_pair(l0, l1);
       h[i] = bf16_pair(h0, h1);
     }
-    stmatrix_x4_trans(dst, l[0], l[1], l[2], l[3]);
-    if (!kGateUp) stmatrix_x4_trans(dst + 32, h[0], h[1], h[2], h[3]);
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int token = (lane >> sh) + j * (32 >> sh);
-      if (token < 16 && 16 * p + token < n && col < a.ldc) {
-        uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(stage_s + token * kOutPitch + 16 * part)
-                     : "memory");
-        *reinterpret_cast<uint4*>(out + static_cast<size_t>(16 * p + token) * a.ldc + col) = v;
-      }
-    }
-    __syncwarp();
+    stmatrix_x4_trans(dst + 16 * p * kOutPitch, l[0], l[1], l[2], l[3]);
+    if (!kGateUp) stmatrix_x4_trans(dst + 16 * p * kOutPitch + 32, h[0], h[1], h[2], h[3]);
   }
+  __syncwarp();
+  uint4 v[1 << sh];
+#pragma unroll
+  for (int j = 0; j < (1 << sh); ++j)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w)
+                 : "r"(stage_s + ((lane >> sh) + j * (32 >> sh)) * kOutPitch + 16 * part)
+                 : "memory");
+  if (col < a.ldc) {
+#pragma unroll
+    for (int j = 0; j < (1 << sh); ++j) {
+      const int token = (lane >> sh) + j * (32 >> sh);
+      if (token < n) *reinterpret_cast<uint4*>(out + static_cast<size_t>(token) * a.ldc + col) = v[j];
+    }
+  }
+  __syncwarp();
 }
 
 // Eight tokens of a summed item (this lane's weight row `lrow` of tile
@@ -332,7 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   __shared__ Seg item_slots[kItemSlots];
   __shared__ uint32_t tmem_base_s;
   __shared__ int prefix[kMaxExperts + 1];
-  __shared__ int s_cnt[kMaxExperts], s_off[kMaxExperts];
   __shared__ int warp_sum[kThreads / 32], warp_max[kThreads / 32];
   __shared__ int hdr_ok, last_flag;
 
@@ -384,9 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       set_status(a.status, CHORD_ERR_INVALID_ARG);   // not an aligned order of `capacity` rows
       cnt = 0;
     }
-    s_cnt[e] = cnt;
-    s_off[e] = off;
     const int n_rt = row_tiles(cnt, a.max_tok);
+    prefix[e] = mine;
     mine += n_pairs * n_rt;
     if (cnt) most = max(most, tile_rows(cnt, n_rt));
   }
@@ -418,17 +420,16 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   for (int i = 0; i < per; ++i) {
     const int e = tid * per + i;
     if (e >= a.E) break;
-    prefix[e] = run;
-    run += n_pairs * row_tiles(s_cnt[e], a.max_tok);
+    prefix[e] += run;
   }
-  if (tid == kThreads - 1) prefix[a.E] = run;   // the last thread ends at the total
+  if (tid == kThreads - 1) prefix[a.E] = run + mine;   // the last thread ends at the total
   __syncthreads();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, tmem_base_s, 0);
 
   tok = __shfl_sync(0xffffffffu, tok, 0);   // warp-uniform for the issuing warps
   const int units = mx_units(a.K);
   Plan plan;
-  plan.prefix = prefix, plan.cnts = s_cnt, plan.offs = s_off;
+  plan.prefix = prefix, plan.cnts = a.counts, plan.offs = a.offsets;
   plan.E = a.E, plan.n_tiles = a.n_tiles, plan.units = units, plan.max_tok = a.max_tok;
   plan.items = hdr_ok ? prefix[a.E] : 0;
   plan.cut = plan.items % static_cast<int>(gridDim.x);
