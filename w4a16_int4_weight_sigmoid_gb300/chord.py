@@ -1,19 +1,25 @@
-"""Thin Python binding of libchord_moe.so (ctypes).
+"""Thin Python binding of libchord_moe.so (ctypes, and a small extension).
 
 Argument marshalling only: every function here checks tensor dtypes and
 devices, passes raw device pointers and the current CUDA stream to the C
 entry point of the same name, and raises ChordError on a non-zero status.
-All computation happens in the library's CUDA kernels; there is no CPU
-fallback, and a missing library is an error.
+The rows in expert order and the MXFP4 operators are called from layers that
+run a dozen of them per step, so their checks and marshalling are in C++
+(csrc_py/binding.cpp, built as _chord.so).  All computation happens in the
+library's CUDA kernels; there is no CPU fallback, and a missing library is an
+error.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
 
-LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libchord_moe.so")
+_HERE = os.path.dirname(os.path.abspath(__file__))
+LIB_PATH = os.path.join(_HERE, "libchord_moe.so")
+EXT_PATH = os.path.join(_HERE, "_chord.so")
 
 CHORD_OK = 0
 CHORD_ERR_INVALID_ARG = -1
@@ -28,7 +34,9 @@ CHORD_EPI_STORE = 0
 CHORD_EPI_SILU_MUL = 1
 CHORD_EPI_WEIGHTED_ADD = 2
 
-CHORD_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+CHORD_DTYPE_BF16 = 0
+CHORD_DTYPE_FP16 = 1
+CHORD_DTYPE_FP32 = 2
 
 CHORD_PATH_AUTO = 0
 CHORD_PATH_SMALL_M = 1
@@ -108,6 +116,23 @@ def lib():
             fn.argtypes = args
         _lib = L
     return _lib
+
+
+_ext_module = None
+
+
+def _ext():
+    """Load the extension (once).  Raises if it has not been built."""
+    global _ext_module
+    if _ext_module is None:
+        lib()
+        if not os.path.exists(EXT_PATH):
+            raise RuntimeError(f"{EXT_PATH} is missing: build it with "
+                               "w4a16_int4_weight_sigmoid_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("_chord", EXT_PATH)
+        _ext_module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_ext_module)
+    return _ext_module
 
 
 def _check(rc: int):
@@ -377,102 +402,56 @@ def chord_moe_layer(x, logits, bias, w13_packed, w2_packed, H: int, I: int, E_to
 
 
 # ------------------------------------------- rows in expert order, and MXFP4
-def _rows(t, name, cols=None, rows=None, dtype=None):
-    """A 2-D CUDA tensor of rows with unit column stride: (pointer, dtype code, row stride).
-    A row length (cols) or row count (rows) that does not match is an error."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    kind, shape, stride = t.dtype, t.shape, t.stride()
-    code = CHORD_DTYPE.get(kind)
-    if code is None or (dtype is not None and kind != dtype):
-        raise TypeError(f"{name} must be {dtype or 'bfloat16, float16 or float32'}, got {kind}")
-    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be a matrix of rows with unit column stride")
-    n, h = shape
-    if cols is not None and h != cols:
-        raise ValueError(f"{name}'s rows hold {h} values, need {cols}")
-    if rows is not None and n != rows:
-        raise ValueError(f"{name} has {n} rows, need {rows}")
-    # the row stride of a single row means nothing
-    return t.data_ptr(), code, stride[0] if n > 1 else max(stride[0], h)
-
-
-def _count(t, n, name, dtype=torch.int32):
-    """A contiguous CUDA tensor of n values of `dtype`."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} values")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t.data_ptr()
-
+# Row matrices are 2-D with unit column stride and any row stride.
 
 def chord_moe_permute(x, sorted_positions, sorted_token_ids, num_tokens_post_padded, topk: int, out, stream=None):
     """out[p(t, j)] = x[t] for every local assignment; padding rows become zeros.
     x [M, H], out [capacity, H] of one type (BF16, FP16, FP32), any row strides."""
-    px, dt, lx = _rows(x, "x")
-    M, H = x.shape
-    po, _, lo = _rows(out, "out", H, None, x.dtype)
-    _check(lib().chord_moe_permute(px, dt, lx, _count(sorted_positions, M * topk, "sorted_positions"),
-                                   _count(sorted_token_ids, out.shape[0], "sorted_token_ids"),
-                                   _count(num_tokens_post_padded, 1, "num_tokens_post_padded"), M, topk, H,
-                                   out.shape[0], po, lo, _stream(stream)))
+    rc = (_ext_module or _ext()).permute(x, sorted_positions, sorted_token_ids, num_tokens_post_padded, topk, out,
+                                         None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def chord_moe_permute_backward(dout, sorted_positions, topk: int, dx, stream=None):
     """dx[t] = sum over the local assignments of dout[p(t, j)].  dout [capacity, H], dx [M, H]."""
-    pd, dt, ld = _rows(dout, "dout")
-    M, H = dx.shape
-    px, _, lx = _rows(dx, "dx", dout.shape[1], None, dout.dtype)
-    _check(lib().chord_moe_permute_backward(pd, dt, ld, _count(sorted_positions, M * topk, "sorted_positions"), M,
-                                            topk, H, dout.shape[0], px, lx, _stream(stream)))
+    rc = (_ext_module or _ext()).permute_backward(dout, sorted_positions, topk, dx,
+                                                  None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def chord_moe_unpermute(y, topk_weights, sorted_positions, out, stream=None):
     """out[t] = sum over the local assignments of topk_weights[t, j] * y[p(t, j)].
     y [capacity, H], topk_weights FP32 [M, topk], out [M, H]."""
-    py, dt, ly = _rows(y, "y")
-    M, k = topk_weights.shape
-    po, _, lo = _rows(out, "out", y.shape[1], M, y.dtype)
-    _check(lib().chord_moe_unpermute(py, dt, ly, _ptr(topk_weights, torch.float32, "topk_weights"),
-                                     _count(sorted_positions, M * k, "sorted_positions"), M, k, y.shape[1],
-                                     y.shape[0], po, lo, _stream(stream)))
+    rc = (_ext_module or _ext()).unpermute(y, topk_weights, sorted_positions, out,
+                                           None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def chord_moe_unpermute_backward(dout, y, topk_weights, sorted_positions, sorted_token_ids, num_tokens_post_padded,
                                  dy, dweights, stream=None):
     """dy[p(t, j)] = topk_weights[t, j] * dout[t], padding rows zeros; dweights[t, j] = <dout[t], y[p(t, j)]>."""
-    M, k = topk_weights.shape
-    pd, dt, ld = _rows(dout, "dout", None, M)
-    H = dout.shape[1]
-    py, _, ly = _rows(y, "y", H, None, dout.dtype)
-    cap = y.shape[0]
-    po, _, lo = _rows(dy, "dy", H, cap, dout.dtype)
-    _check(lib().chord_moe_unpermute_backward(
-        pd, py, dt, ld, ly, _ptr(topk_weights, torch.float32, "topk_weights"),
-        _count(sorted_positions, M * k, "sorted_positions"), _count(sorted_token_ids, cap, "sorted_token_ids"),
-        _count(num_tokens_post_padded, 1, "num_tokens_post_padded"), M, k, H, cap, po, lo,
-        _count(dweights, M * k, "dweights", torch.float32), _stream(stream)))
+    rc = (_ext_module or _ext()).unpermute_backward(dout, y, topk_weights, sorted_positions, sorted_token_ids,
+                                                    num_tokens_post_padded, dy, dweights,
+                                                    None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def chord_mxfp4_quantize(x, codes, scales, stream=None):
     """x [rows, K] (BF16, FP16, FP32) -> codes uint8 [rows, K/2], scales uint8 [rows, K/32]."""
-    px, dt, lx = _rows(x, "x")
-    rows, K = x.shape
-    _check(lib().chord_mxfp4_quantize(px, dt, lx, rows, K, _count(codes, rows * K // 2, "codes", torch.uint8),
-                                      _count(scales, rows * K // 32, "scales", torch.uint8), _stream(stream)))
+    rc = (_ext_module or _ext()).quantize(x, codes, scales, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def chord_mxfp4_dequantize(codes, scales, out, stream=None):
     """The values of codes and scales, out [rows, K] (BF16, FP16, FP32)."""
-    po, dt, lo = _rows(out, "out")
-    rows, K = out.shape
-    _check(lib().chord_mxfp4_dequantize(_count(codes, rows * K // 2, "codes", torch.uint8),
-                                        _count(scales, rows * K // 32, "scales", torch.uint8), rows, K, po, dt, lo,
-                                        _stream(stream)))
+    rc = (_ext_module or _ext()).dequantize(codes, scales, out, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def chord_mxfp4_rows_bytes(capacity: int, K: int) -> int:
@@ -484,12 +463,10 @@ def chord_mxfp4_quantize_rows(x, sorted_positions, topk: int, num_tokens_post_pa
     """Token rows x [M, K] quantised into the product's row operand `rows` (uint8,
     chord_mxfp4_rows_bytes(capacity, K)): token t to its rows sorted_positions[t, :]; with
     sorted_positions None, row r of x to row r below num_tokens_post_padded (topk unused)."""
-    px, dt, lx = _rows(x, "x")
-    M, K = x.shape
-    pos = None if sorted_positions is None else _count(sorted_positions, M * topk, "sorted_positions")
-    nt = None if num_tokens_post_padded is None else _count(num_tokens_post_padded, 1, "num_tokens_post_padded")
-    _check(lib().chord_mxfp4_quantize_rows(px, dt, lx, M, K, pos, topk, nt, capacity,
-                                           _ptr(rows, torch.uint8, "rows"), rows.numel(), _stream(stream)))
+    rc = (_ext_module or _ext()).quantize_rows(x, sorted_positions, topk, num_tokens_post_padded, capacity, rows,
+                                               None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def chord_mxfp4_prepack_bytes(E: int, N: int, K: int) -> int:
@@ -499,9 +476,10 @@ def chord_mxfp4_prepack_bytes(E: int, N: int, K: int) -> int:
 def chord_mxfp4_prepack(codes, scales, gate_up: bool, packed, stream=None):
     """codes uint8 [E, N, K/2] and scales uint8 [E, N, K/32] -> the product's weight operand."""
     E, N, K2 = codes.shape
-    _check(lib().chord_mxfp4_prepack(_ptr(codes, torch.uint8, "codes"),
-                                     _count(scales, E * N * K2 // 16, "scales", torch.uint8), E, N, 2 * K2,
-                                     int(gate_up), _ptr(packed, torch.uint8, "packed"), packed.numel(),
+    if scales.numel() != E * N * K2 // 16:
+        raise ValueError(f"scales must hold {E * N * K2 // 16} values")
+    _check(lib().chord_mxfp4_prepack(_ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"), E, N,
+                                     2 * K2, int(gate_up), _ptr(packed, torch.uint8, "packed"), packed.numel(),
                                      _stream(stream)))
 
 
@@ -513,14 +491,8 @@ def chord_mxfp4_moe_gemm(rows, packed_w, E_local: int, N: int, K: int, expert_co
                          epilogue: int, C, workspace, dev_status=None, stream=None):
     """C [capacity, N or N/2] BF16 = the experts' product of the quantised rows; workspace: uint8 tensor of
     chord_mxfp4_moe_gemm_workspace_bytes() bytes, zeroed once when allocated."""
-    cols = N // 2 if epilogue == CHORD_EPI_SILU_MUL else N
-    if not isinstance(C, torch.Tensor) or C.dtype != torch.bfloat16 or tuple(C.shape) != (capacity, cols):
-        raise ValueError(f"chord_mxfp4_moe_gemm: C must be bfloat16 [{capacity}, {cols}]")
-    if not isinstance(packed_w, torch.Tensor) or packed_w.numel() < chord_mxfp4_prepack_bytes(E_local, N, K):
-        raise ValueError("chord_mxfp4_moe_gemm: packed_w is smaller than E_local, N and K need")
-    _check(lib().chord_mxfp4_moe_gemm(
-        _ptr(rows, torch.uint8, "rows"), rows.numel(), _ptr(packed_w, torch.uint8, "packed_w"), E_local, N, K,
-        _count(expert_counts, E_local, "expert_counts"),
-        _count(expert_offsets, E_local + 1, "expert_offsets"), capacity, epilogue, _ptr(C, None, "C"),
-        _ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"),
-        _stream(stream)))
+    rc = (_ext_module or _ext()).moe_gemm(rows, packed_w, E_local, N, K, expert_counts, expert_offsets, capacity,
+                                          epilogue, C, workspace, dev_status,
+                                          None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)

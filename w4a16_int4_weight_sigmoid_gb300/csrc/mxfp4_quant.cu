@@ -89,22 +89,32 @@ __device__ __forceinline__ uint2 quantize_run(const Run<T>& r, uint32_t& scale) 
 }
 
 // ---------------------------------------------------------------- row-major
-// CTA column: a run of each thread; rows blockIdx.y, + gridDim.y, ...
+// CTA column: a run of each thread; rows blockIdx.y, + gridDim.y, ..., two at
+// a time so that the second's loads are in flight while the first is worked on.
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const T* x, long long ldx, long long rows, int K,
                                                             uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
   const int g = blockIdx.x * kThreads + threadIdx.x;
   const bool in = g < K / kRun;
-  for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
-    Run<T> v = {};
-    if (in) load_run<kWide>(x + r * ldx + kRun * g, v);
+  auto load = [&](long long r, Run<T>& v) {
+    v = Run<T>{};
+    if (in && r < rows) load_run<kWide>(x + r * ldx + kRun * g, v);
+  };
+  auto store = [&](long long r, const Run<T>& v) {
     uint32_t scale;
     const uint2 q = quantize_run(v, scale);
-    if (in) {
+    if (in && r < rows) {
       reinterpret_cast<uint2*>(codes + r * (K / 2))[g] = q;
       if ((g & 1) == 0) scales[r * (K / kMxBlock) + g / 2] = static_cast<uint8_t>(scale);
     }
+  };
+  for (long long r = blockIdx.y; r < rows; r += 2 * gridDim.y) {
+    Run<T> v0, v1;
+    load(r, v0);
+    load(r + gridDim.y, v1);
+    store(r, v0);
+    store(r + gridDim.y, v1);
   }
 }
 
@@ -114,25 +124,40 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const uint8_t* __r
                                                               int K, T* __restrict__ out, long long ldo) {
   const int g = blockIdx.x * kThreads + threadIdx.x;
   if (g >= K / kRun) return;
-  for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(codes + r * (K / 2)) + g);
-    const uint32_t code = __ldg(scales + r * (K / kMxBlock) + g / 2);
-    // 2^(code - 127): code 0 is subnormal, 255 is NaN
-    const float scale = __uint_as_float(code == 255u ? 0x7FC00000u : code == 0u ? 0x00400000u : code << 23);
-    uint32_t h[8];
-    e2m1x8_to_f16(q.x, *reinterpret_cast<uint32_t(*)[4]>(h));
-    e2m1x8_to_f16(q.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
-    Run<T> o;
+  constexpr int kRows = 4;   // rows in flight
+  for (long long r = blockIdx.y; r < rows; r += kRows * gridDim.y) {
+    uint2 q[kRows];
+    uint32_t code[kRows];
 #pragma unroll
-    for (int i = 0; i < kRun; ++i)
-      from_f32(o.e[i], __half2float(__ushort_as_half(static_cast<uint16_t>(h[i / 2] >> (16 * (i & 1))))) * scale);
-    T* dst = out + r * ldo + kRun * g;
-    if (kWide) {
+    for (int j = 0; j < kRows; ++j) {
+      const long long row = r + static_cast<long long>(j) * gridDim.y;
+      if (row < rows) {
+        q[j] = __ldg(reinterpret_cast<const uint2*>(codes + row * (K / 2)) + g);
+        code[j] = __ldg(scales + row * (K / kMxBlock) + g / 2);
+      }
+    }
 #pragma unroll
-      for (int i = 0; i < Run<T>::kWords; i += 8) st_32(reinterpret_cast<uint32_t*>(dst) + i, o.w + i);
-    } else {
+    for (int j = 0; j < kRows; ++j) {
+      const long long row = r + static_cast<long long>(j) * gridDim.y;
+      if (row >= rows) break;
+      // 2^(code - 127): code 0 is subnormal, 255 is NaN
+      const float scale =
+          __uint_as_float(code[j] == 255u ? 0x7FC00000u : code[j] == 0u ? 0x00400000u : code[j] << 23);
+      uint32_t h[8];
+      e2m1x8_to_f16(q[j].x, *reinterpret_cast<uint32_t(*)[4]>(h));
+      e2m1x8_to_f16(q[j].y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+      Run<T> o;
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) dst[i] = o.e[i];
+      for (int i = 0; i < kRun; ++i)
+        from_f32(o.e[i], __half2float(__ushort_as_half(static_cast<uint16_t>(h[i / 2] >> (16 * (i & 1))))) * scale);
+      T* dst = out + row * ldo + kRun * g;
+      if (kWide) {
+#pragma unroll
+        for (int i = 0; i < Run<T>::kWords; i += 8) st_32(reinterpret_cast<uint32_t*>(dst) + i, o.w + i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) dst[i] = o.e[i];
+      }
     }
   }
 }
@@ -164,14 +189,16 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, lon
     }
     return p < rows ? p : -1;
   };
-  int p_next = position(blockIdx.y);
-  for (int t = blockIdx.y; t < n; t += gridDim.y) {
-    const int p = p_next;
-    uint32_t left = __ballot_sync(0xffffffffu, p >= 0);
-    Run<T> v = {};
+  // two tokens alternate, so that the next one's values and the positions of
+  // the one after it are in flight
+  auto load = [&](int p, Run<T>& v, int t) {
+    v = Run<T>{};
+    const uint32_t left = __ballot_sync(0xffffffffu, p >= 0);
     if (left && in) load_run<kWide>(x + t * ldx + kRun * g, v);
-    p_next = position(t + gridDim.y);
-    if (!left) continue;
+    return left;
+  };
+  auto store = [&](int p, uint32_t left, const Run<T>& v) {
+    if (!left) return;
     uint32_t scale;
     const uint2 q = quantize_run(v, scale);
     for (; left; left &= left - 1) {
@@ -182,6 +209,19 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const T* x, lon
         if ((g & 1) == 0) out_scales[at * kMxRowScales + chunk] = static_cast<uint8_t>(scale);
       }
     }
+  };
+  const int step = gridDim.y;
+  Run<T> v0, v1;
+  int p0 = position(blockIdx.y), p1 = position(blockIdx.y + step);
+  uint32_t left0 = load(p0, v0, blockIdx.y);
+  for (int t = blockIdx.y; t < n; t += 2 * step) {
+    const int p2 = position(t + 2 * step), p3 = position(t + 3 * step);
+    const uint32_t left1 = load(p1, v1, t + step);
+    store(p0, left0, v0);
+    left0 = load(p2, v0, t + 2 * step);
+    store(p1, left1, v1);
+    p0 = p2;
+    p1 = p3;
   }
 }
 
