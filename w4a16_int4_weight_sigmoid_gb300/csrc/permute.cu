@@ -12,10 +12,12 @@
 // weight gradient: FP32 in a fixed tree), each result rounded once, so
 // results do not depend on the launch.
 //
-// Rows are moved in accesses of V elements.  V is 16 bytes where every base,
-// row stride and row length allows it; otherwise the largest power of two
-// they share, down to one element.
+// Rows are moved in accesses of B bytes: 32 where every base, row stride and
+// row length allows it, otherwise the largest power of two they share, down
+// to one element.  All kernels are programmatic launches that touch no memory
+// before the work ahead of them in the stream has completed.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -39,73 +41,101 @@ struct RowArgs {
   int M, topk, H, rows;     // rows: capacity of the expert order
 };
 
+constexpr int kThreads = 128;
+// CTAs per SM that permute is compiled for, and its grid in such waves: 8192
+// rows of 7168 took 48.3 us with one wave, 45.7 with two, 43.6 with four (the
+// CTAs' shares even out) and 49.2 with a CTA for every token.
+constexpr int kCtas = 12, kWaves = 4;
+
 // ------------------------------------------------------------ padding rows
 // Zeros in the padding rows (sorted >= M * topk) of the aligned order: CTA b
-// of nb takes every nb-th run of kPadRows rows below the padded total.
-constexpr int kPadRows = 16;
+// of nb takes every nb-th run of kPadRows rows below the padded total, all
+// threads on one row (a warp on a row of its own took 25 us at 64 tokens).
+constexpr int kPadRows = 8;
 
-template <typename T, int V>
-__device__ __forceinline__ void zero_padding(const RowArgs& a, int b, int nb) {
-  const int n = min(__ldg(a.ntpp), a.rows), sentinel = a.M * a.topk;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  Vec<T, V> z;
-#pragma unroll
-  for (int i = 0; i < V; ++i) from_f32(z.e[i], 0.f);
-  for (int r0 = b * kPadRows; r0 < n; r0 += nb * kPadRows)
-    for (int r = r0 + warp; r < min(n, r0 + kPadRows); r += warps) {
-      if (__ldg(a.sorted + r) < sentinel) continue;
-      auto* dst = reinterpret_cast<Vec<T, V>*>(static_cast<T*>(a.out) + r * a.ldo);
-      for (int c = lane; c < a.H / V; c += 32) dst[c] = z;
+template <int B>
+__device__ __forceinline__ void zero_padding(const RowArgs& a, int row_bytes, long long out_stride, int b, int nb) {
+  const int lane = threadIdx.x & 31, sentinel = a.M * a.topk;
+  const int total = ld_ca(a.ntpp);
+  const Chunk<B> z{};
+  for (int r0 = b * kPadRows; r0 < a.rows; r0 += nb * kPadRows) {
+    // the entry is read before the total is known: entries past the total
+    // exist, and are dropped
+    const int r = r0 + lane, f = lane < kPadRows && r < a.rows ? ld_ca(a.sorted + r) : 0;
+    if (r0 >= total) break;
+    uint32_t pad = __ballot_sync(0xffffffffu, lane < kPadRows && r < min(total, a.rows) && f >= sentinel);
+    for (; pad; pad &= pad - 1) {
+      uint8_t* dst = static_cast<uint8_t*>(a.out) + (r0 + __ffs(pad) - 1) * out_stride;
+      for (int c = threadIdx.x * B; c < row_bytes; c += kThreads * B) store_chunk<B>(dst + c, z);
     }
+  }
 }
 
 // ----------------------------------------------------------------- permute
-// CTA (t, chunk) below the padding CTAs: VPT accesses of each thread of
-// token t's row are loaded, then stored to each of its rows.
-template <typename T, int V, int VPT, int THREADS>
-__global__ void __launch_bounds__(THREADS) permute_kernel(RowArgs a, int pad_ctas) {
-  if (static_cast<int>(blockIdx.x) < pad_ctas) {
-    if (blockIdx.y == 0) zero_padding<T, V>(a, blockIdx.x, pad_ctas);
+// Copies, so element types do not matter.  A thread moves one access of a
+// token's row to each of its rows; CTAs walk over the tokens, the next one's
+// row and the positions of the one after it in flight.  The CTAs of the last
+// `pad_y` grid rows zero the padding.
+template <int B>
+__global__ void __launch_bounds__(kThreads, kCtas) permute_kernel(RowArgs a, int row_bytes, long long x_stride,
+                                                                  long long out_stride, int pad_y) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, step = gridDim.y - pad_y;
+  if (static_cast<int>(blockIdx.y) >= step) {
+    zero_padding<B>(a, row_bytes, out_stride, (blockIdx.y - step) * gridDim.x + blockIdx.x, pad_y * gridDim.x);
     return;
   }
-  const int t = blockIdx.x - pad_ctas, lane = threadIdx.x & 31;
-  int p = -1;
-  if (lane < a.topk) p = __ldg(a.pos + static_cast<long long>(t) * a.topk + lane);
-  if (p >= a.rows) p = -1;
-  const uint32_t local = __ballot_sync(0xffffffffu, p >= 0);
-  if (!local) return;
-  const int nv = a.H / V, c0 = blockIdx.y * THREADS * VPT + threadIdx.x;
-  const auto* src = reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(a.x) + t * a.ldx);
-  Vec<T, V> v[VPT];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-    if (c0 + i * THREADS < nv) v[i] = src[c0 + i * THREADS];
-  for (uint32_t left = local; left; left &= left - 1) {
-    const long long row = __shfl_sync(0xffffffffu, p, __ffs(left) - 1);
-    auto* dst = reinterpret_cast<Vec<T, V>*>(static_cast<T*>(a.out) + row * a.ldo);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (c0 + i * THREADS < nv) dst[c0 + i * THREADS] = v[i];
+  const int c = (blockIdx.x * kThreads + threadIdx.x) * B;
+  const bool in = c < row_bytes;
+  auto position = [&](int t) {
+    const int p = t < a.M && lane < a.topk ? ld_ca(a.pos + static_cast<long long>(t) * a.topk + lane) : -1;
+    return p < a.rows ? p : -1;
+  };
+  auto load = [&](int p, Chunk<B>& v, int t) {
+    const uint32_t left = __ballot_sync(0xffffffffu, p >= 0);
+    if (left && in) load_chunk<B>(static_cast<const uint8_t*>(a.x) + t * x_stride + c, v);
+    return left;
+  };
+  auto store = [&](int p, uint32_t left, const Chunk<B>& v) {
+    for (; left; left &= left - 1) {
+      const long long row = __shfl_sync(0xffffffffu, p, __ffs(left) - 1);
+      if (in) store_chunk<B>(static_cast<uint8_t*>(a.out) + row * out_stride + c, v);
+    }
+  };
+  Chunk<B> v0, v1;
+  int p0 = position(blockIdx.y), p1 = position(blockIdx.y + step);
+  uint32_t left0 = load(p0, v0, blockIdx.y);
+  for (int t = blockIdx.y; t < a.M; t += 2 * step) {
+    const int p2 = position(t + 2 * step), p3 = position(t + 3 * step);
+    const uint32_t left1 = load(p1, v1, t + step);
+    store(p0, left0, v0);
+    left0 = load(p2, v0, t + 2 * step);
+    store(p1, left1, v1);
+    p0 = p2;
+    p1 = p3;
   }
 }
 
 // ---------------------------------------------------- weighted sum of rows
-// CTA (t, chunk): VPT accesses per thread of the token's local rows, ROWS
-// rows in flight, added in increasing j.
-template <typename T, int V, int VPT, int THREADS, bool kWeighted>
-__global__ void __launch_bounds__(THREADS) combine_kernel(RowArgs a) {
-  constexpr int kRows = VPT >= 4 ? 2 : 4;
+// CTA (t, chunk): VPT accesses per thread of the token's local rows,
+// four rows in flight, added in increasing j.
+template <typename T, int B, int VPT, bool kWeighted>
+__global__ void __launch_bounds__(kThreads) combine_kernel(RowArgs a) {
+  constexpr int V = B / sizeof(T), kRows = 4;
   __shared__ int s_pos[kMaxTopk];
   __shared__ float s_w[kMaxTopk];
   __shared__ int s_n;
   const int t = blockIdx.x, tid = threadIdx.x;
+  grid_dep_wait();
+  grid_dep_launch();
   if (tid < 32) {
     int p = -1;
     float wj = 1.f;
     if (tid < a.topk) {
       const long long o = static_cast<long long>(t) * a.topk + tid;
-      p = __ldg(a.pos + o);
-      if (kWeighted) wj = __ldg(a.w + o);
+      p = ld_ca(a.pos + o);
+      if (kWeighted) wj = ld_ca(a.w + o);
     }
     if (p >= a.rows) p = -1;
     const uint32_t local = __ballot_sync(0xffffffffu, p >= 0);
@@ -117,21 +147,21 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(RowArgs a) {
     if (tid == 0) s_n = __popc(local);
   }
   __syncthreads();
-  const int n = s_n, nv = a.H / V, c0 = blockIdx.y * THREADS * VPT + tid;
+  const int n = s_n, nv = a.H / V, c0 = blockIdx.y * kThreads * VPT + tid;
   float acc[VPT][V];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[i][e] = 0.f;
   for (int j0 = 0; j0 < n; j0 += kRows) {
-    Vec<T, V> v[kRows][VPT];
+    Chunk<B> v[kRows][VPT];
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
       if (j0 + r < n) {
-        const auto* src = reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(a.y) + s_pos[j0 + r] * a.ldy);
+        const T* src = static_cast<const T*>(a.y) + s_pos[j0 + r] * a.ldy;
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-          if (c0 + i * THREADS < nv) v[r][i] = src[c0 + i * THREADS];
+          if (c0 + i * kThreads < nv) load_chunk<B>(src + V * (c0 + i * kThreads), v[r][i]);
       }
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
@@ -139,65 +169,72 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(RowArgs a) {
         const float wj = s_w[j0 + r];
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-          if (c0 + i * THREADS < nv)
+          if (c0 + i * kThreads < nv)
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-              acc[i][e] = kWeighted ? fmaf(wj, to_f32(v[r][i].e[e]), acc[i][e]) : acc[i][e] + to_f32(v[r][i].e[e]);
+            for (int e = 0; e < V; ++e) {
+              const float y = chunk_f32<T, B>(v[r][i], e);
+              acc[i][e] = kWeighted ? fmaf(wj, y, acc[i][e]) : acc[i][e] + y;
+            }
       }
   }
-  auto* dst = reinterpret_cast<Vec<T, V>*>(static_cast<T*>(a.out) + t * a.ldo);
+  T* dst = static_cast<T*>(a.out) + t * a.ldo;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
-    if (c0 + i * THREADS < nv) {
-      Vec<T, V> o;
-#pragma unroll
-      for (int e = 0; e < V; ++e) from_f32(o.e[e], acc[i][e]);
-      dst[c0 + i * THREADS] = o;
+    if (c0 + i * kThreads < nv) {
+      Chunk<B> o;
+      f32_chunk<T, B>(o, acc[i]);
+      store_chunk<B>(dst + V * (c0 + i * kThreads), o);
     }
 }
 
 // ------------------------------------------------- gradient of the weighted sum
-// CTA (t, s) below the padding CTAs: assignments j = s, s + S, ... of token t
+// CTA (t, s) after the padding CTAs: assignments j = s, s + S, ... of token t
 // (S = gridDim.y).  One pass over dout[t] and y[p] gives both dy[p] and the
 // dot product; dout[t] comes from L1 for every j after the first.
-template <typename T, int V, int THREADS>
-__global__ void __launch_bounds__(THREADS) unpermute_backward_kernel(RowArgs a, int pad_ctas) {
+template <typename T, int B>
+__global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a, int pad_ctas) {
+  constexpr int V = B / sizeof(T), kUnroll = B >= 32 ? 2 : 4;
+  __shared__ float s_part[kMaxTopk][kThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dep_wait();
+  grid_dep_launch();
   if (static_cast<int>(blockIdx.x) < pad_ctas) {
-    if (blockIdx.y == 0) zero_padding<T, V>(a, blockIdx.x, pad_ctas);
+    if (blockIdx.y == 0)
+      zero_padding<B>(a, a.H * static_cast<int>(sizeof(T)), a.ldo * static_cast<long long>(sizeof(T)),
+                      blockIdx.x, pad_ctas);
     return;
   }
-  constexpr int kUnroll = 4;
-  __shared__ float s_part[kMaxTopk][THREADS / 32];
-  const int t = blockIdx.x - pad_ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nv = a.H / V;
-  const auto* g = reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(a.x) + t * a.ldx);
+  const int t = blockIdx.x - pad_ctas, nv = a.H / V;
+  const T* g = static_cast<const T*>(a.x) + t * a.ldx;
   for (int j = blockIdx.y; j < a.topk; j += gridDim.y) {
     const long long f = static_cast<long long>(t) * a.topk + j;
-    const int p = __ldg(a.pos + f);
+    const int p = ld_ca(a.pos + f);
+    const float wj = ld_ca(a.w + f);
     float dot = 0.f;
     if (p >= 0 && p < a.rows) {
-      const float wj = __ldg(a.w + f);
-      const auto* y = reinterpret_cast<const Vec<T, V>*>(static_cast<const T*>(a.y) + p * a.ldy);
-      auto* dy = reinterpret_cast<Vec<T, V>*>(static_cast<T*>(a.out) + p * a.ldo);
-      for (int c0 = tid; c0 < nv; c0 += kUnroll * THREADS) {
-        Vec<T, V> vg[kUnroll], vy[kUnroll];
+      const T* y = static_cast<const T*>(a.y) + p * a.ldy;
+      T* dy = static_cast<T*>(a.out) + p * a.ldo;
+      for (int c0 = tid; c0 < nv; c0 += kUnroll * kThreads) {
+        Chunk<B> vg[kUnroll], vy[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
-          if (c0 + i * THREADS < nv) {
-            vg[i] = g[c0 + i * THREADS];
-            vy[i] = y[c0 + i * THREADS];
+          if (c0 + i * kThreads < nv) {
+            load_chunk<B>(g + V * (c0 + i * kThreads), vg[i]);
+            load_chunk<B>(y + V * (c0 + i * kThreads), vy[i]);
           }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
-          if (c0 + i * THREADS < nv) {
-            Vec<T, V> o;
+          if (c0 + i * kThreads < nv) {
+            float d[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-              const float gv = to_f32(vg[i].e[e]);
-              dot = fmaf(gv, to_f32(vy[i].e[e]), dot);
-              from_f32(o.e[e], wj * gv);
+              const float gv = chunk_f32<T, B>(vg[i], e);
+              dot = fmaf(gv, chunk_f32<T, B>(vy[i], e), dot);
+              d[e] = wj * gv;
             }
-            dy[c0 + i * THREADS] = o;
+            Chunk<B> o;
+            f32_chunk<T, B>(o, d);
+            store_chunk<B>(dy + V * (c0 + i * kThreads), o);
           }
       }
     }
@@ -206,10 +243,10 @@ __global__ void __launch_bounds__(THREADS) unpermute_backward_kernel(RowArgs a, 
     if (lane == 0) s_part[j][warp] = dot;
   }
   __syncthreads();
-  for (int j = blockIdx.y + tid * gridDim.y; j < a.topk; j += THREADS * gridDim.y) {
+  for (int j = blockIdx.y + tid * gridDim.y; j < a.topk; j += kThreads * gridDim.y) {
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) sum += s_part[j][i];
+    for (int i = 0; i < kThreads / 32; ++i) sum += s_part[j][i];
     a.dw[static_cast<long long>(t) * a.topk + j] = sum;
   }
 }
@@ -222,78 +259,66 @@ int sm_count() {
   return sms[dev] > 0 ? sms[dev] : 1;
 }
 
-constexpr int kThreads = 128;
-
-// CTAs for the padding rows: enough for every run, at most one per SM.
-int padding_ctas(int rows) { return std::min((rows + kPadRows - 1) / kPadRows, sm_count()); }
-
-enum class Op { kPermute, kPermuteBackward, kUnpermute, kUnpermuteBackward };
-
-template <typename T, int V>
-cudaError_t launch_rows(Op op, const RowArgs& a, cudaStream_t st) {
-  const int nv = a.H / V;
-  // accesses per thread: a whole row per CTA where there are at least four
-  // CTAs per SM, otherwise smaller chunks
-  auto chunks = [&](int vpt) { return (nv + kThreads * vpt - 1) / (kThreads * vpt); };
-  int vpt = 8;
-  while (vpt > 1 && static_cast<long long>(a.M) * chunks(vpt) < 4LL * sm_count()) vpt /= 2;
-  if (op == Op::kPermute) {
-    const int pad = padding_ctas(a.rows);
-    const dim3 grid(a.M + pad, chunks(vpt));
-    switch (vpt) {
-      case 8: permute_kernel<T, V, 8, kThreads><<<grid, kThreads, 0, st>>>(a, pad); break;
-      case 4: permute_kernel<T, V, 4, kThreads><<<grid, kThreads, 0, st>>>(a, pad); break;
-      case 2: permute_kernel<T, V, 2, kThreads><<<grid, kThreads, 0, st>>>(a, pad); break;
-      default: permute_kernel<T, V, 1, kThreads><<<grid, kThreads, 0, st>>>(a, pad);
-    }
-  } else if (op == Op::kUnpermuteBackward) {
-    const int pad = padding_ctas(a.rows);
-    int split = 1;
-    while (split < a.topk && static_cast<long long>(a.M) * split < 4LL * sm_count()) split *= 2;
-    unpermute_backward_kernel<T, V, kThreads><<<dim3(a.M + pad, std::min(split, a.topk)), kThreads, 0, st>>>(a, pad);
-  } else {
-    const dim3 grid(a.M, chunks(vpt));
-    const bool w = op == Op::kUnpermute;
-    switch (vpt) {
-      case 8:
-        if (w) combine_kernel<T, V, 8, kThreads, true><<<grid, kThreads, 0, st>>>(a);
-        else combine_kernel<T, V, 8, kThreads, false><<<grid, kThreads, 0, st>>>(a);
-        break;
-      case 4:
-        if (w) combine_kernel<T, V, 4, kThreads, true><<<grid, kThreads, 0, st>>>(a);
-        else combine_kernel<T, V, 4, kThreads, false><<<grid, kThreads, 0, st>>>(a);
-        break;
-      case 2:
-        if (w) combine_kernel<T, V, 2, kThreads, true><<<grid, kThreads, 0, st>>>(a);
-        else combine_kernel<T, V, 2, kThreads, false><<<grid, kThreads, 0, st>>>(a);
-        break;
-      default:
-        if (w) combine_kernel<T, V, 1, kThreads, true><<<grid, kThreads, 0, st>>>(a);
-        else combine_kernel<T, V, 1, kThreads, false><<<grid, kThreads, 0, st>>>(a);
-    }
-  }
-  return cudaGetLastError();
+template <int B>
+cudaError_t launch_permute(const RowArgs& a, int elem, cudaStream_t st) {
+  const int row_bytes = a.H * elem;
+  const int columns = (row_bytes / B + kThreads - 1) / kThreads;
+  // tokens at once: what is resident; up to a fifth of the CTAs zero padding
+  const int slots = std::max(1, std::min(kWaves * kCtas * sm_count() / columns, 60000));
+  const int tokens = std::min(a.M, slots);
+  const int runs = (a.rows + kPadRows - 1) / kPadRows;
+  const int pad_y = std::max(1, std::min(slots / 5, (runs + columns - 1) / columns));
+  return launch_kernel(permute_kernel<B>, dim3(columns, tokens + pad_y), dim3(kThreads), 0, st, true, a, row_bytes,
+                       a.ldx * elem, a.ldo * elem, pad_y);
 }
 
-template <typename T>
-cudaError_t launch_access(Op op, const RowArgs& a, int bytes, cudaStream_t st) {
-  constexpr int kE = sizeof(T);
-  switch (bytes / kE) {
-    case 16 / kE: return launch_rows<T, 16 / kE>(op, a, st);
-    case 8 / kE: return launch_rows<T, 8 / kE>(op, a, st);
-    case 4 / kE: return launch_rows<T, 4 / kE>(op, a, st);
-    default: return launch_rows<T, 1>(op, a, st);
-  }
+template <typename T, int B>
+cudaError_t launch_combine(const RowArgs& a, cudaStream_t st) {
+  const int nv = a.H / (B / static_cast<int>(sizeof(T)));
+  // accesses per thread: many where there are at least four CTAs per SM then
+  constexpr int kFew = B >= 16 ? 1 : 4, kMany = 2 * kFew;
+  const int many = (nv + kMany * kThreads - 1) / (kMany * kThreads), few = (nv + kFew * kThreads - 1) / (kFew * kThreads);
+  if (static_cast<long long>(a.M) * many >= 4LL * sm_count())
+    return launch_kernel(a.w ? combine_kernel<T, B, kMany, true> : combine_kernel<T, B, kMany, false>,
+                         dim3(a.M, many), dim3(kThreads), 0, st, true, a);
+  return launch_kernel(a.w ? combine_kernel<T, B, kFew, true> : combine_kernel<T, B, kFew, false>, dim3(a.M, few),
+                       dim3(kThreads), 0, st, true, a);
 }
 
-cudaError_t launch_dtype(Op op, const RowArgs& a, int dtype, cudaStream_t st) {
-  const size_t es = dtype_bytes(dtype);
-  int bytes = row_access_bytes(a.out, a.ldo, a.H, es);
-  if (a.x) bytes = std::min(bytes, row_access_bytes(a.x, a.ldx, a.H, es));
-  if (a.y) bytes = std::min(bytes, row_access_bytes(a.y, a.ldy, a.H, es));
-  if (dtype == CHORD_DTYPE_BF16) return launch_access<Bf16>(op, a, bytes, st);
-  if (dtype == CHORD_DTYPE_FP16) return launch_access<Fp16>(op, a, bytes, st);
-  return launch_access<float>(op, a, bytes, st);
+template <typename T, int B>
+cudaError_t launch_unpermute_backward(const RowArgs& a, cudaStream_t st) {
+  const int pad = std::min((a.rows + kPadRows - 1) / kPadRows, 2 * sm_count());
+  int split = 1;
+  while (split < a.topk && static_cast<long long>(a.M) * split < 4LL * sm_count()) split *= 2;
+  return launch_kernel(unpermute_backward_kernel<T, B>, dim3(a.M + pad, std::min(split, a.topk)), dim3(kThreads), 0,
+                       st, true, a, pad);
+}
+
+// Access size shared by all row matrices of the call.
+int access_bytes(const RowArgs& a, size_t es) {
+  int bytes = row_access_bytes(a.out, a.ldo, a.H, es, 32);
+  if (a.x) bytes = std::min(bytes, row_access_bytes(a.x, a.ldx, a.H, es, 32));
+  if (a.y) bytes = std::min(bytes, row_access_bytes(a.y, a.ldy, a.H, es, 32));
+  return bytes;
+}
+
+// Calls f(element type, access size); access sizes below the element's do
+// not occur (bases and strides are element-aligned).
+template <typename F>
+cudaError_t with_access(int dtype, int bytes, F f) {
+  auto typed = [&](auto t) {
+    using T = decltype(t);
+    switch (bytes) {
+      case 32: return f(t, std::integral_constant<int, 32>{});
+      case 16: return f(t, std::integral_constant<int, 16>{});
+      case 8: return f(t, std::integral_constant<int, 8>{});
+      case 4: return f(t, std::integral_constant<int, 4>{});
+      default: return f(t, std::integral_constant<int, static_cast<int>(sizeof(T))>{});
+    }
+  };
+  if (dtype == CHORD_DTYPE_BF16) return typed(Bf16{});
+  if (dtype == CHORD_DTYPE_FP16) return typed(Fp16{});
+  return typed(0.f);
 }
 
 }  // namespace
@@ -304,7 +329,14 @@ cudaError_t moe_permute_launch(const void* x, int dtype, long long ldx, const in
   RowArgs a{};
   a.x = x, a.ldx = ldx, a.pos = pos, a.sorted = sorted, a.ntpp = ntpp, a.out = out, a.ldo = ldo;
   a.M = M, a.topk = topk, a.H = H, a.rows = rows;
-  return launch_dtype(Op::kPermute, a, dtype, st);
+  const int es = static_cast<int>(dtype_bytes(dtype));
+  switch (access_bytes(a, es)) {
+    case 32: return launch_permute<32>(a, es, st);
+    case 16: return launch_permute<16>(a, es, st);
+    case 8: return launch_permute<8>(a, es, st);
+    case 4: return launch_permute<4>(a, es, st);
+    default: return launch_permute<2>(a, es, st);
+  }
 }
 
 cudaError_t moe_combine_launch(const void* y, int dtype, long long ldy, const float* w, const int32_t* pos, int M,
@@ -312,7 +344,9 @@ cudaError_t moe_combine_launch(const void* y, int dtype, long long ldy, const fl
   RowArgs a{};
   a.y = y, a.ldy = ldy, a.w = w, a.pos = pos, a.out = out, a.ldo = ldo;
   a.M = M, a.topk = topk, a.H = H, a.rows = rows;
-  return launch_dtype(w ? Op::kUnpermute : Op::kPermuteBackward, a, dtype, st);
+  return with_access(dtype, access_bytes(a, dtype_bytes(dtype)), [&](auto t, auto b) {
+    return launch_combine<decltype(t), decltype(b)::value>(a, st);
+  });
 }
 
 cudaError_t moe_unpermute_backward_launch(const void* dout, const void* y, int dtype, long long ldd, long long ldy,
@@ -322,7 +356,9 @@ cudaError_t moe_unpermute_backward_launch(const void* dout, const void* y, int d
   RowArgs a{};
   a.x = dout, a.ldx = ldd, a.y = y, a.ldy = ldy, a.w = w, a.pos = pos, a.sorted = sorted, a.ntpp = ntpp;
   a.out = dy, a.ldo = ldo, a.dw = dw, a.M = M, a.topk = topk, a.H = H, a.rows = rows;
-  return launch_dtype(Op::kUnpermuteBackward, a, dtype, st);
+  return with_access(dtype, access_bytes(a, dtype_bytes(dtype)), [&](auto t, auto b) {
+    return launch_unpermute_backward<decltype(t), decltype(b)::value>(a, st);
+  });
 }
 
 }  // namespace chord
