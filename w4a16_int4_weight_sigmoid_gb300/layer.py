@@ -1,8 +1,11 @@
-"""Device-resident W4A16 MoE layer: prepacked weights + workspace + one call.
+"""Device-resident MoE layers, and the expert order for training.
 
 Memory management and marshalling only (torch allocates, the library
-computes): weights are uploaded once and repacked on the device by
-chord_w4a16_prepack; forward() is one chord_moe_layer call.
+computes).  W4A16MoELayer uploads its weights once, repacked on the device by
+chord_w4a16_prepack; forward() is one chord_moe_layer call.  MXFP4MoELayer
+keeps MXFP4 weights and runs the experts with both operands in 4 bits.
+ExpertOrder holds a routing's aligned expert order, and permute_rows /
+unpermute_rows move rows into it and back with gradients.
 """
 from __future__ import annotations
 
@@ -62,4 +65,160 @@ class W4A16MoELayer:
                               self.expert_begin, self.E_local, self.topk, out, self.workspace(M),
                               topk_weights_out, topk_ids_out, tuning=tuning,
                               dev_status=self.dev_status, stream=stream)
+        return out
+
+
+class ExpertOrder:
+    """The aligned order of the assignments of M tokens to topk of E_total experts, on
+    one shard (local experts [expert_begin, +E_local)); route() fills it.
+
+    topk_weights [M, topk] FP32 and topk_ids [M, topk]; sorted_token_ids [capacity],
+    sorted_positions [M * topk], num_tokens_post_padded [1], expert_counts [E_local]
+    and expert_offsets [E_local + 1], as chord_moe_align defines them."""
+
+    def __init__(self, M: int, topk: int, expert_begin: int, E_local: int, block_m: int = 16, device="cuda"):
+        self.M, self.topk, self.expert_begin, self.E_local, self.block_m = M, topk, expert_begin, E_local, block_m
+        self.capacity = chord.chord_moe_align_capacity(M, topk, E_local, block_m)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.topk_weights = torch.empty((M, topk), dtype=torch.float32, device=device)
+        self.topk_ids = torch.empty((M, topk), **i32)
+        self.sorted_token_ids = torch.empty(self.capacity, **i32)
+        self.sorted_positions = torch.empty(M * topk, **i32)
+        self.expert_ids = torch.empty(self.capacity // block_m, **i32)
+        self.num_tokens_post_padded = torch.empty(1, **i32)
+        self.expert_counts = torch.empty(E_local, **i32)
+        self.expert_offsets = torch.empty(E_local + 1, **i32)
+        nbytes = chord.chord_moe_align_workspace_bytes(M, topk, E_local)
+        self._ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+    def route(self, logits, bias, stream=None):
+        """Top-k routing of logits [M, E_total] and the order, on the device."""
+        chord.chord_moe_route_align(logits, bias, self.topk, self.expert_begin, self.E_local, self.block_m,
+                                    self.topk_weights, self.topk_ids, self.sorted_token_ids, self.expert_ids,
+                                    self.num_tokens_post_padded, self.expert_counts, self.expert_offsets,
+                                    self.sorted_positions, self._ws, stream=stream)
+        return self
+
+
+def _unit_columns(g):
+    """A gradient as rows with unit column stride (that of a sum has stride 0 everywhere)."""
+    return g if g.stride(1) == 1 or g.shape[1] == 1 else g.contiguous()
+
+
+class _Permute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, order):
+        ctx.order = order
+        # rows past the padded total are not written by the call: zeros
+        out = torch.zeros((order.capacity, x.shape[1]), dtype=x.dtype, device=x.device)
+        chord.chord_moe_permute(x, order.sorted_positions, order.sorted_token_ids, order.num_tokens_post_padded,
+                                order.topk, out)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        dout = _unit_columns(dout)
+        dx = torch.empty((ctx.order.M, dout.shape[1]), dtype=dout.dtype, device=dout.device)
+        chord.chord_moe_permute_backward(dout, ctx.order.sorted_positions, ctx.order.topk, dx)
+        return dx, None
+
+
+class _Unpermute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, weights, order):
+        ctx.order = order
+        ctx.save_for_backward(y, weights)
+        out = torch.empty((order.M, y.shape[1]), dtype=y.dtype, device=y.device)
+        chord.chord_moe_unpermute(y, weights, order.sorted_positions, out)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        y, weights = ctx.saved_tensors
+        o, dout = ctx.order, _unit_columns(dout)
+        dy, dw = torch.zeros_like(y, memory_format=torch.contiguous_format), torch.empty_like(weights)
+        chord.chord_moe_unpermute_backward(dout, y, weights, o.sorted_positions, o.sorted_token_ids,
+                                           o.num_tokens_post_padded, dy, dw)
+        return dy, dw, None
+
+
+def permute_rows(x, order: ExpertOrder):
+    """x [M, H] -> rows [order.capacity, H] in expert order, zeros elsewhere; differentiable."""
+    return _Permute.apply(x, order)
+
+
+def unpermute_rows(y, weights, order: ExpertOrder):
+    """The weighted sum of rows y [order.capacity, H] back to tokens [M, H]; differentiable
+    in y and in weights FP32 [M, topk]."""
+    return _Unpermute.apply(y, weights, order)
+
+
+def quantize_mxfp4(w, stream=None):
+    """[..., K] BF16, FP16 or FP32 on the device -> MXFP4 codes uint8 [..., K/2] and scales uint8 [..., K/32]."""
+    K = w.shape[-1]
+    codes = torch.empty((*w.shape[:-1], K // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((*w.shape[:-1], K // 32), dtype=torch.uint8, device=w.device)
+    chord.chord_mxfp4_quantize(w.reshape(-1, K), codes, scales, stream=stream)
+    return codes, scales
+
+
+class MXFP4MoELayer:
+    """One expert shard of a MoE layer whose experts run in MXFP4 on both operands:
+    route and align, rows quantised into expert order, gate/up product with SiLU * up,
+    rows quantised again, down product, weighted sum back to tokens.
+
+    w13: (codes [E_local, 2I, H/2], scales [E_local, 2I, H/32]), rows 0..I-1 gate and
+    I..2I-1 up; w2: (codes [E_local, H, I/2], scales [E_local, H, I/32]), as
+    quantize_mxfp4 gives them, on the device.  Calls share the layer's buffers, so they
+    follow one another on one stream."""
+
+    def __init__(self, w13, w2, E_total: int, expert_begin: int, topk: int):
+        (q13, s13), (q2, s2) = w13, w2
+        self.device = q13.device
+        self.E_local, twoI, self.H, self.I = q13.shape[0], q13.shape[1], 2 * q13.shape[2], 2 * q2.shape[2]
+        if twoI != 2 * self.I or q2.shape[:2] != (self.E_local, self.H):
+            raise ValueError("w13 must be [E_local, 2I, H/2] and w2 [E_local, H, I/2]")
+        self.E_total, self.expert_begin, self.topk = E_total, expert_begin, topk
+        self.w13 = self._prepack(q13, s13, True)
+        self.w2 = self._prepack(q2, s2, False)
+        self._ws = torch.zeros(chord.chord_mxfp4_moe_gemm_workspace_bytes(), dtype=torch.uint8, device=self.device)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._M = -1
+
+    def _prepack(self, codes, scales, gate_up):
+        E, N, K2 = codes.shape
+        packed = torch.empty(chord.chord_mxfp4_prepack_bytes(E, N, 2 * K2), dtype=torch.uint8, device=self.device)
+        chord.chord_mxfp4_prepack(codes, scales, gate_up, packed)
+        return packed
+
+    def _buffers(self, M: int):
+        if M != self._M:
+            self.order = ExpertOrder(M, self.topk, self.expert_begin, self.E_local, device=self.device)
+            cap = self.order.capacity
+            u8 = dict(dtype=torch.uint8, device=self.device)
+            self._rows = torch.empty(max(chord.chord_mxfp4_rows_bytes(cap, self.H),
+                                         chord.chord_mxfp4_rows_bytes(cap, self.I)), **u8)
+            self.h = torch.empty((cap, self.I), dtype=torch.bfloat16, device=self.device)
+            self.y = torch.empty((cap, self.H), dtype=torch.bfloat16, device=self.device)
+            self._M = M
+        return self.order
+
+    def forward(self, x, logits, bias, out=None, stream=None):
+        """x [M, H] (BF16, FP16 or FP32), logits FP32 [M, E_total], bias FP32 [E_total] -> out [M, H] BF16."""
+        M = x.shape[0]
+        if out is None:
+            out = torch.empty((M, self.H), dtype=torch.bfloat16, device=self.device)
+        if M == 0:
+            return out
+        o = self._buffers(M).route(logits, bias, stream=stream)
+        cap, n = o.capacity, o.num_tokens_post_padded
+        chord.chord_mxfp4_quantize_rows(x, o.sorted_positions, self.topk, n, cap, self._rows, stream=stream)
+        chord.chord_mxfp4_moe_gemm(self._rows, self.w13, self.E_local, 2 * self.I, self.H, o.expert_counts,
+                                   o.expert_offsets, cap, chord.CHORD_EPI_SILU_MUL, self.h, self._ws,
+                                   self.dev_status, stream=stream)
+        chord.chord_mxfp4_quantize_rows(self.h, None, 1, n, cap, self._rows, stream=stream)
+        chord.chord_mxfp4_moe_gemm(self._rows, self.w2, self.E_local, self.H, self.I, o.expert_counts,
+                                   o.expert_offsets, cap, chord.CHORD_EPI_STORE, self.y, self._ws,
+                                   self.dev_status, stream=stream)
+        chord.chord_moe_unpermute(self.y, o.topk_weights, o.sorted_positions, out, stream=stream)
         return out
