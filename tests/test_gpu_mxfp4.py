@@ -117,6 +117,32 @@ def test_quantize_extremes():
     assert np.array_equal(got[keep].astype(np.float64), values(code, s)[keep])
 
 
+@pytest.mark.parametrize("name", ["bf16", "fp16"])
+def test_quantize_extremes_of_16_bits(name):
+    """Each power of two of the type as a block's maximum, subnormals included, with ties and
+    the type's largest value: the scaled values stay exact in 16 bits."""
+    dtype = TYPES[name]
+    lo, hi = (-133, 127) if name == "bf16" else (-24, 15)
+    n = hi - lo + 1
+    x = torch.zeros((n + 1, 32), dtype=torch.float64)
+    for i, e in enumerate(range(lo, hi + 1)):
+        x[i] = torch.tensor([1, -1, 0.75, 0.625, -0.375, 0.4375, 0.0625, 0.1875, 0.3125, -0.21875, 0, -0.0,
+                             0.25, 0.5, 0.125, 1e-3] * 2, dtype=torch.float64) * 2.0 ** e
+    x[n] = torch.finfo(dtype).max
+    x[n, 1::2] = -torch.finfo(dtype).max
+    x = x.to(dtype).cuda()
+    codes = torch.empty((n + 1, 16), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((n + 1, 1), dtype=torch.uint8, device="cuda")
+    chord.chord_mxfp4_quantize(x, codes, scales)
+    code, s = ref_quantize(x.double().cpu().numpy())
+    assert np.array_equal(scales.cpu().numpy(), s)
+    assert np.array_equal(codes.cpu().numpy(), pack(code))
+    for i, bad in enumerate((float("inf"), float("-inf"), float("nan"))):
+        x[i, 5 * i] = bad
+    chord.chord_mxfp4_quantize(x, codes, scales)
+    assert (scales[:3] == 255).all() and (codes[:3] == 0).all() and (scales[3:] != 255).all()
+
+
 def test_quantize_strides():
     """Rows inside a wider, unaligned buffer, and one row for all (stride 0)."""
     base = inputs(9, 512, torch.bfloat16, 3)

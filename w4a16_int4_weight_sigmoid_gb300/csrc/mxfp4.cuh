@@ -75,6 +75,18 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
+__device__ __forceinline__ uint32_t e2m1x8_from_f16(const uint32_t (&h)[4]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b0, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b1, %2;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b2, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b3, %4;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]));
+  return r;
+}
 // The inverse: eight codes as FP16 pairs (exact).
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t q, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"

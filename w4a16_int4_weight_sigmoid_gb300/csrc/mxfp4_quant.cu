@@ -2,12 +2,13 @@
 // into the experts' product's operand (with the permutation into expert
 // order), and the weights' repacking.
 //
-// A thread holds 16 consecutive values (one 32-byte load for 16-bit types);
-// two threads hold a block of 32, whose largest magnitude takes one shuffle.
-// The maximum is taken on the bit patterns of |x| (ordered like the values,
-// infinities and NaNs above all finite ones; 16-bit types two to a register),
-// and the scale is a power of two, so x / scale and its rounding to E2M1 are
-// exact operations.
+// A thread holds a whole block: 32 consecutive values (two 32-byte loads for
+// 16-bit types), so the block's maximum needs no other lane, its codes are
+// one 16-byte store, and what a row costs beside its values (positions,
+// addresses) is paid by half the threads that a block shared by two needs.
+// The maximum is taken on |x| with NaNs above all (16-bit types two to a
+// register), and the scale is a power of two, so x / scale and its rounding
+// to E2M1 are exact operations.
 #include <algorithm>
 
 #include "common.cuh"
@@ -20,12 +21,13 @@ namespace {
 
 constexpr int kThreads = 128;
 // CTAs per SM that the kernels are compiled for, and the grid in such waves,
-// each CTA walking on to its next row: dequantising 8192 x 7168 took 27.4 us
-// with one wave, 25.5 with two, 24.4 with four, 34.2 with a CTA for every row.
+// each CTA walking on to its next row.  8192 x 7168 BF16: dequantising took
+// 25.0 us with two waves, 23.9 with four, 34 with a CTA for every row;
+// rows into expert order (8 ranks' share) 19.8 us with two, 21.0 with four.
 template <typename T>
-constexpr int kCtas = sizeof(T) == 4 ? 8 : 12;
-constexpr int kWaves = 4;
-constexpr int kRun = 16;   // values per thread
+constexpr int kCtas = sizeof(T) == 4 ? 5 : 8;
+constexpr int kWaves = 4, kRowWaves = 2;
+constexpr int kRun = kMxBlock;   // values per thread
 
 // kRun consecutive values as 32-bit words; kWide: 32-byte aligned.
 template <typename T>
@@ -53,36 +55,74 @@ __device__ __forceinline__ void load_run(const T* p, Run<T>& r) {
   }
 }
 
-// Bits of the largest |x| as FP32.
+// Bits of the largest |x| as FP32; a NaN's where there is one.
 __device__ __forceinline__ uint32_t run_max(const Run<float>& r) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kRun; ++i) m = max(m, r.w[i] & 0x7FFFFFFFu);
   return m;
 }
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b, Bf16) {
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  return a;
+}
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b, Fp16) {
+  asm("max.NaN.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  return a;
+}
 template <typename T>
 __device__ __forceinline__ uint32_t run_max(const Run<T>& r) {
-  uint32_t m = 0;
+  uint32_t m = r.w[0];
 #pragma unroll
-  for (int i = 0; i < Run<T>::kWords; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
+  for (int i = 1; i < Run<T>::kWords; ++i) m = max_abs2(m, r.w[i], T{});
   T t;
-  t.v = static_cast<uint16_t>(max(m & 0xFFFFu, m >> 16));
+  t.v = static_cast<uint16_t>(max(m & 0x7FFFu, (m >> 16) & 0x7FFFu));
   return __float_as_uint(to_f32(t));
 }
 
-// This thread's 16 codes and the scale code of the block that it shares with
-// its neighbour lane.  All lanes of the warp call it.
-template <typename T>
-__device__ __forceinline__ uint2 quantize_run(const Run<T>& r, uint32_t& scale) {
-  uint32_t m = run_max(r);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  scale = mx_scale_code(m);
-  const float inv = scale == 255u ? 0.f : mx_inverse_scale(scale);
-  float v[kRun];
+// Codes of eight values (words r.w[n..]) times 2^(127 - code).  The product
+// is exact wherever it is not far below the smallest midpoint, in the input's
+// own type for the 16-bit ones.
+__device__ __forceinline__ uint32_t scaled_codes(const Run<float>& r, int n, uint32_t code) {
+  const float inv = mx_inverse_scale(code);
+  float v[8];
 #pragma unroll
-  for (int i = 0; i < kRun; ++i) v[i] = to_f32(r.e[i]) * inv;
-  uint2 q = make_uint2(e2m1x8(v), e2m1x8(v + 8));
-  if (scale == 255u) q = make_uint2(0, 0);   // an infinity or a NaN in the block
+  for (int i = 0; i < 8; ++i) v[i] = r.e[n + i] * inv;
+  return e2m1x8(v);
+}
+__device__ __forceinline__ uint32_t scaled_codes(const Run<Bf16>& r, int n, uint32_t code) {
+  const uint32_t inv = min(254u, 254u - code) * 0x00800080u;   // the exponent field of both halves
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t p;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p) : "r"(r.w[n / 2 + i]), "r"(inv));
+    v[2 * i] = __uint_as_float(p << 16);
+    v[2 * i + 1] = __uint_as_float(p & 0xFFFF0000u);
+  }
+  return e2m1x8(v);
+}
+__device__ __forceinline__ uint32_t scaled_codes(const Run<Fp16>& r, int n, uint32_t code) {
+  // 127 - code is -13 .. 26 for FP16's range: two factors within FP16's own
+  const int k = 127 - static_cast<int>(code), k0 = min(k, 15), k1 = min(k - k0, 15);
+  const uint32_t f0 = static_cast<uint32_t>(max(k0 + 15, 1)) * 0x04000400u;
+  const uint32_t f1 = static_cast<uint32_t>(k1 + 15) * 0x04000400u;
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(r.w[n / 2 + i]), "r"(f0));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h[i]) : "r"(f1));
+  }
+  return e2m1x8_from_f16(h);
+}
+
+// The 32 codes of a block and its scale code.
+template <typename T>
+__device__ __forceinline__ uint4 quantize_run(const Run<T>& r, uint32_t& scale) {
+  scale = mx_scale_code(run_max(r));
+  uint4 q = make_uint4(scaled_codes(r, 0, scale), scaled_codes(r, 8, scale), scaled_codes(r, 16, scale),
+                       scaled_codes(r, 24, scale));
+  if (scale == 255u) q = make_uint4(0, 0, 0, 0);   // an infinity or a NaN in the block
   return q;
 }
 
@@ -98,19 +138,18 @@ __global__ void __launch_bounds__(kThreads, kCtas<T>) quantize_kernel(const T* x
   grid_dep_wait();
   grid_dep_launch();
   auto load = [&](long long r, Run<T>& v) {
-    v = Run<T>{};
     if (in && r < rows) load_run<kWide>(x + r * ldx + kRun * g, v);
   };
   auto store = [&](long long r, const Run<T>& v) {
     uint32_t scale;
-    const uint2 q = quantize_run(v, scale);
     if (in && r < rows) {
-      reinterpret_cast<uint2*>(codes + r * (K / 2))[g] = q;
-      if ((g & 1) == 0) scales[r * (K / kMxBlock) + g / 2] = static_cast<uint8_t>(scale);
+      const uint4 q = quantize_run(v, scale);
+      reinterpret_cast<uint4*>(codes + r * (K / 2))[g] = q;
+      scales[r * (K / kMxBlock) + g] = static_cast<uint8_t>(scale);
     }
   };
   for (long long r = blockIdx.y; r < rows; r += 2 * gridDim.y) {
-    Run<T> v0, v1;
+    Run<T> v0{}, v1{};
     load(r, v0);
     load(r + gridDim.y, v1);
     store(r, v0);
@@ -126,18 +165,16 @@ __global__ void __launch_bounds__(kThreads, kCtas<T>) dequantize_kernel(const ui
   grid_dep_wait();
   grid_dep_launch();
   if (g >= K / kRun) return;
-  constexpr int kRows = 4;   // rows in flight
+  constexpr int kRows = 2;   // rows in flight
   for (long long r = blockIdx.y; r < rows; r += kRows * gridDim.y) {
-    uint2 q[kRows];
+    Chunk<16> q[kRows];
     uint32_t code[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       const long long row = r + static_cast<long long>(j) * gridDim.y;
       if (row < rows) {
-        Chunk<8> c;
-        load_chunk<8>(codes + row * (K / 2) + 8 * g, c);
-        q[j] = make_uint2(c.w[0], c.w[1]);
-        asm volatile("ld.global.u8 %0, [%1];" : "=r"(code[j]) : "l"(scales + row * (K / kMxBlock) + g / 2));
+        load_chunk<16>(codes + row * (K / 2) + 16 * g, q[j]);
+        asm volatile("ld.global.u8 %0, [%1];" : "=r"(code[j]) : "l"(scales + row * (K / kMxBlock) + g));
       }
     }
 #pragma unroll
@@ -147,20 +184,27 @@ __global__ void __launch_bounds__(kThreads, kCtas<T>) dequantize_kernel(const ui
       // 2^(code - 127): code 0 is subnormal, 255 is NaN
       const float scale =
           __uint_as_float(code[j] == 255u ? 0x7FC00000u : code[j] == 0u ? 0x00400000u : code[j] << 23);
-      uint32_t h[8];
-      e2m1x8_to_f16(q[j].x, *reinterpret_cast<uint32_t(*)[4]>(h));
-      e2m1x8_to_f16(q[j].y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
-      Run<T> o;
-#pragma unroll
-      for (int i = 0; i < kRun; ++i)
-        from_f32(o.e[i], __half2float(__ushort_as_half(static_cast<uint16_t>(h[i / 2] >> (16 * (i & 1))))) * scale);
       T* dst = out + row * ldo + kRun * g;
-      if (kWide) {
+      constexpr int kPart = 32 / sizeof(T);   // values per 32-byte store
 #pragma unroll
-        for (int i = 0; i < Run<T>::kWords / 8; ++i) store_chunk<32>(reinterpret_cast<uint8_t*>(dst) + 32 * i, o.c[i]);
-      } else {
+      for (int c = 0; c < kRun / kPart; ++c) {
+        float f[kPart];
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) dst[i] = o.e[i];
+        for (int w = 0; w < kPart / 8; ++w) {
+          uint32_t h[4];
+          e2m1x8_to_f16(q[j].w[c * (kPart / 8) + w], h);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            f[8 * w + i] = __half2float(__ushort_as_half(static_cast<uint16_t>(h[i / 2] >> (16 * (i & 1))))) * scale;
+        }
+        if constexpr (kWide) {
+          Chunk<32> o;
+          f32_chunk<T, 32>(o, f);
+          store_chunk<32>(dst + kPart * c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPart; ++i) from_f32(dst[kPart * c + i], f[i]);
+        }
       }
     }
   }
@@ -181,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<T>) quantize_rows_kernel(const
   const int units = mx_units(K);
   uint8_t* out_scales = out + units * mx_rows_padded(rows) * kMxRowBytes;
   const bool in_unit = g < units * (kMxUnitK / kRun), in = g < K / kRun;
-  const int unit = g / (kMxUnitK / kRun), chunk = (g / 2) % kMxRowScales;
+  const int unit = g / kMxRowScales, chunk = g % kMxRowScales;
   grid_dep_wait();
   grid_dep_launch();
   const int n = pos ? M : min(min(ld_ca(ntpp), rows), M);
@@ -195,8 +239,12 @@ __global__ void __launch_bounds__(kThreads, kCtas<T>) quantize_rows_kernel(const
   };
   // two tokens alternate, so that the next one's values and the positions of
   // the one after it are in flight
+  // this thread's place in a row of slab 0; a slab and a row further on
+  uint8_t* out_g = out + static_cast<size_t>(unit) * kMxSlabRows * kMxRowBytes;
+  uint8_t* scale_g = out_scales + static_cast<size_t>(unit) * kMxSlabRows * kMxRowScales + chunk;
+  const uint32_t slab_rows = units * kMxSlabRows;
   auto load = [&](int p, Run<T>& v, int t) {
-    v = Run<T>{};
+    if (!in) v = Run<T>{};   // K's padding
     const uint32_t left = __ballot_sync(0xffffffffu, p >= 0);
     if (left && in) load_run<kWide>(x + t * ldx + kRun * g, v);
     return left;
@@ -204,13 +252,13 @@ __global__ void __launch_bounds__(kThreads, kCtas<T>) quantize_rows_kernel(const
   auto store = [&](int p, uint32_t left, const Run<T>& v) {
     if (!left) return;
     uint32_t scale;
-    const uint2 q = quantize_run(v, scale);
+    const uint4 q = quantize_run(v, scale);
     for (; left; left &= left - 1) {
       const uint32_t r = __shfl_sync(0xffffffffu, p, __ffs(left) - 1);
       if (in_unit) {
-        const size_t at = mx_row_place(unit, units, r);
-        reinterpret_cast<uint2*>(out + at * kMxRowBytes + 16 * (chunk ^ (r & 7)))[g & 1] = q;
-        if ((g & 1) == 0) out_scales[at * kMxRowScales + chunk] = static_cast<uint8_t>(scale);
+        const size_t at = static_cast<size_t>(r / kMxSlabRows) * slab_rows + r % kMxSlabRows;
+        *reinterpret_cast<uint4*>(out_g + at * kMxRowBytes + 16 * (chunk ^ (r & 7))) = q;
+        scale_g[at * kMxRowScales] = static_cast<uint8_t>(scale);
       }
     }
   };
@@ -268,10 +316,10 @@ __global__ void mx_prepack_kernel(const uint8_t* __restrict__ codes, const uint8
 }
 
 template <typename T>
-dim3 grid_for(int columns, long long rows) {
+dim3 grid_for(int columns, long long rows, int waves) {
   static int sms = 0;
   if (!sms) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, 0);
-  const long long most = std::max(1LL, static_cast<long long>(kWaves) * kCtas<T> * sms / columns);
+  const long long most = std::max(1LL, static_cast<long long>(waves) * kCtas<T> * sms / columns);
   return dim3(columns, static_cast<unsigned>(std::min({rows, most, 65535LL})));
 }
 
@@ -280,7 +328,7 @@ cudaError_t quantize_t(const void* x, long long ldx, long long rows, int K, uint
                        cudaStream_t st) {
   const bool wide = row_access_bytes(x, ldx, K, sizeof(T), 32) == 32;
   return launch_kernel(wide ? quantize_kernel<T, true> : quantize_kernel<T, false>,
-                       grid_for<T>((K / kRun + kThreads - 1) / kThreads, rows), dim3(kThreads), 0, st, true,
+                       grid_for<T>((K / kRun + kThreads - 1) / kThreads, rows, kWaves), dim3(kThreads), 0, st, true,
                        static_cast<const T*>(x), ldx, rows, K, codes, scales);
 }
 
@@ -289,7 +337,7 @@ cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, long long 
                          cudaStream_t st) {
   const bool wide = row_access_bytes(out, ldo, K, sizeof(T), 32) == 32;
   return launch_kernel(wide ? dequantize_kernel<T, true> : dequantize_kernel<T, false>,
-                       grid_for<T>((K / kRun + kThreads - 1) / kThreads, rows), dim3(kThreads), 0, st, true, codes,
+                       grid_for<T>((K / kRun + kThreads - 1) / kThreads, rows, kWaves), dim3(kThreads), 0, st, true, codes,
                        scales, rows, K, static_cast<T*>(out), ldo);
 }
 
@@ -298,7 +346,7 @@ cudaError_t quantize_rows_t(const void* x, long long ldx, int M, int K, const in
                             const int32_t* ntpp, int rows, uint8_t* out, cudaStream_t st) {
   const bool wide = row_access_bytes(x, ldx, K, sizeof(T), 32) == 32;
   return launch_kernel(wide ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>,
-                       grid_for<T>((mx_units(K) * (kMxUnitK / kRun) + kThreads - 1) / kThreads, M), dim3(kThreads), 0,
+                       grid_for<T>((mx_units(K) * (kMxUnitK / kRun) + kThreads - 1) / kThreads, M, kRowWaves), dim3(kThreads), 0,
                        st, true, static_cast<const T*>(x), ldx, M, K, pos, topk, ntpp, rows, out);
 }
 
