@@ -140,8 +140,9 @@ struct Walk {
   int row0, rows, tile, tiles, u0, u1;
   bool more;
 
-  __device__ explicit Walk(const Plan& plan)
-      : p(plan), pos(plan.chunks ? static_cast<int>(blockIdx.x) : plan.begin), item(-1), e(0) {
+  // e0: the expert of the CTA's first segment
+  __device__ Walk(const Plan& plan, int e0)
+      : p(plan), pos(plan.chunks ? static_cast<int>(blockIdx.x) : plan.begin), item(-1), e(e0) {
     advance();
   }
   __device__ void advance() {
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   __shared__ uint32_t tmem_base_s;
   __shared__ int prefix[kMaxExperts + 1];
   __shared__ int warp_sum[kThreads / 32], warp_max[kThreads / 32];
-  __shared__ int hdr_ok, last_flag;
+  __shared__ int hdr_ok, last_flag, first_expert;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -375,23 +376,28 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
 
   // first item of each expert, and the largest row tile: thread i covers
   // experts [i * per, (i + 1) * per)
+  constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
   const int per = (a.E + kThreads - 1) / kThreads;
   const int n_pairs = (a.n_tiles + kPair - 1) / kPair;
-  int mine = 0, most = 16;
-  for (int i = 0; i < per; ++i) {
+  int mine = 0, most = 16, own[kPer + 1];   // items before each of the thread's experts
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
     const int e = tid * per + i;
-    if (e >= a.E) break;
+    own[i] = mine;
+    if (i >= per || e >= a.E) continue;
     int cnt = ld_ca(a.counts + e);
     const int off = ld_ca(a.offsets + e);
     if (cnt < 0 || off < 0 || off % 8 != 0 || cnt > a.capacity || off > a.capacity - cnt) {
       set_status(a.status, CHORD_ERR_INVALID_ARG);   // not an aligned order of `capacity` rows
       cnt = 0;
     }
-    const int n_rt = row_tiles(cnt, a.max_tok);
-    prefix[e] = mine;
-    mine += n_pairs * n_rt;
-    if (cnt) most = max(most, tile_rows(cnt, n_rt));
+    if (cnt > 0) {
+      const int n_rt = cnt <= a.max_tok ? 1 : row_tiles(cnt, a.max_tok);
+      mine += n_pairs * n_rt;
+      most = max(most, tile_rows(cnt, n_rt));
+    }
   }
+  own[kPer] = mine;
   if (tid == kThreads - 1) {
     hdr_ok = h0.x == kMxMagic && h0.y == kMxVersion && static_cast<int>(h0.z) >= a.E &&
              static_cast<int>(h0.w) == a.N && static_cast<int>(h1.x) == a.K && static_cast<int>(h1.y) == (kGateUp ? 1 : 0);
@@ -411,43 +417,69 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int run = inc - mine, tok = 16;
+  // every warp adds up the warps' sums itself
+  int sum = lane < kThreads / 32 ? warp_sum[lane] : 0;
+  int tok = lane < kThreads / 32 ? warp_max[lane] : 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) run += warp_sum[i];
-    tok = max(tok, warp_max[i]);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += t;
   }
-  for (int i = 0; i < per; ++i) {
+  tok = __reduce_max_sync(0xffffffffu, tok);
+  const int run = inc - mine + (warp ? __shfl_sync(0xffffffffu, sum, warp - 1) : 0);
+
+  const int units = mx_units(a.K), ctas = gridDim.x, cta = blockIdx.x;
+  Plan plan;
+  plan.prefix = prefix, plan.cnts = a.counts, plan.offs = a.offsets;
+  plan.E = a.E, plan.n_tiles = a.n_tiles, plan.units = units, plan.max_tok = a.max_tok;
+  plan.items = hdr_ok ? __shfl_sync(0xffffffffu, sum, 31) : 0;
+  plan.cut = plan.items % ctas;
+  // Divided by rows: about one (tile, run of rows) for each CTA.  (With a
+  // single unit nothing is cut along K and there are no partials.)
+  plan.chunks = tok > kSplitTok && units > 1 && plan.cut > 0 ? min(max(ctas / (kPair * plan.cut), 1), tok / 16) : 0;
+  // Divided along K: where two or more CTAs come to an item, each item into as
+  // many equal parts, so that a CTA has one segment to hand over; otherwise
+  // all items' units into one range per CTA.  A part of u units costs u units'
+  // time and its item units / u parts to add; a part takes tok / 80 of a
+  // unit's time (measured 8 ns a token against 0.6 us), so u is at least the
+  // square root of units * tok / 80.  No part is empty, and an item's parts
+  // are in consecutive CTAs.
+  const int total = plan.chunks ? 0 : plan.cut * units;   // the host keeps this far below 2^31
+  const int least = max(1, static_cast<int>(sqrtf(units * tok / 80.f)));
+  int parts = 0, ranges = 0;
+  plan.begin = plan.end = 0;
+  if (total > 0) {
+    parts = min(ctas / plan.cut, units / least);
+    if (parts >= 2) {
+      const int item = cta / parts, part = cta - item * parts;
+      if (item < plan.cut) {
+        plan.begin = item * units + part * units / parts;
+        plan.end = item * units + (part + 1) * units / parts;
+      }
+    } else {
+      parts = 0;
+      ranges = max(1, min(ctas, total / least));
+      if (cta < ranges) {
+        plan.begin = static_cast<uint32_t>(cta) * total / ranges;
+        plan.end = static_cast<uint32_t>(cta + 1) * total / ranges;
+      }
+    }
+  }
+  // the expert of this CTA's first segment
+  const int first_item = plan.end > plan.begin ? plan.begin / units
+                         : plan.chunks && cta < kPair * plan.chunks * plan.cut ? cta / (kPair * plan.chunks)
+                                                                               : plan.cut + cta;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
     const int e = tid * per + i;
-    if (e >= a.E) break;
-    prefix[e] += run;
+    if (i >= per || e >= a.E) continue;
+    const int lo = run + own[i];
+    prefix[e] = lo;
+    if (lo <= first_item && first_item < run + own[i + 1]) first_expert = e;
   }
   if (tid == kThreads - 1) prefix[a.E] = run + mine;   // the last thread ends at the total
   __syncthreads();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, tmem_base_s, 0);
-
-  tok = __shfl_sync(0xffffffffu, tok, 0);   // warp-uniform for the issuing warps
-  const int units = mx_units(a.K);
-  Plan plan;
-  plan.prefix = prefix, plan.cnts = a.counts, plan.offs = a.offsets;
-  plan.E = a.E, plan.n_tiles = a.n_tiles, plan.units = units, plan.max_tok = a.max_tok;
-  plan.items = hdr_ok ? prefix[a.E] : 0;
-  plan.cut = plan.items % static_cast<int>(gridDim.x);
-  // Divided by rows: about one (tile, run of rows) for each CTA.  (With a
-  // single unit nothing is cut along K and there are no partials.)
-  plan.chunks = tok > kSplitTok && units > 1 && plan.cut > 0
-                    ? min(max(static_cast<int>(gridDim.x) / (kPair * plan.cut), 1), tok / 16) : 0;
-  // Divided along K.  A range of u units costs u units' time and its item
-  // units / u parts to add; a part takes tok / 80 of a unit's time (measured
-  // 8 ns a token against 0.6 us), so u is at least the square root of
-  // units * tok / 80.  No range is empty: an item's parts are in consecutive
-  // CTAs.
-  const int total = plan.chunks ? 0 : plan.cut * units;   // the host keeps this far below 2^31
-  const int least = max(1, static_cast<int>(sqrtf(units * tok / 80.f)));
-  const int G = total > 0 ? max(1, min(static_cast<int>(gridDim.x), total / least)) : 0;
-  auto range = [&](int c) { return static_cast<int>(static_cast<long long>(c) * total / G); };
-  plan.begin = blockIdx.x < G ? range(blockIdx.x) : 0;
-  plan.end = blockIdx.x < G ? range(blockIdx.x + 1) : 0;
   const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget / stage);
   const int n_acc = min(kMaxAcc, kSfCol / (kPair * tok));
   ItemRing items{item_full, item_empty, item_slots, 0, 0};
@@ -577,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     }
   } else if (warp == kItemWarp) {
     // ----------------------------------------------------------------- items
-    Walk walk(plan);
+    Walk walk(plan, first_expert);
     int slot = 0, ph = 0;
     for (bool first = true, more = true; more;) {
       if (!first && !__all_sync(0xffffffffu, mbar_wait_backoff(&item_empty[slot], ph ^ 1, a.status))) break;
@@ -650,19 +682,22 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       if (++acc == n_acc) acc = 0, ++use;
       if (whole) continue;
       // a cut item: the CTA that arrives last adds the parts in K order
-      const int i0 = w.item * units;                     // its units are [i0, i0 + units)
-      const int first = static_cast<int>((static_cast<long long>(i0 + 1) * G - 1) / total);
-      const int last = static_cast<int>((static_cast<long long>(i0 + units) * G - 1) / total);
-      __threadfence();
+      int first = w.item * parts, last = first + parts - 1;
+      if (parts == 0) {
+        const uint32_t i0 = w.item * units;               // its units are [i0, i0 + units)
+        first = ((i0 + 1) * ranges - 1) / total;
+        last = ((i0 + units) * ranges - 1) / total;
+      }
       epilogue_all(true);
       if (tid == 32 * kEpiWarp0) {
+        __threadfence();   // the parts stored by all threads before the barrier
         const int done = atomicAdd(a.split_cnt + first, 1) == last - first;
         if (done) atomicExch(a.split_cnt + first, 0);    // zero for the next launch
+        __threadfence();
         last_flag = done;
       }
       epilogue_all(true);
       if (!last_flag) continue;
-      __threadfence();
       // Twelve 16-byte loads in flight: six parts of eight tokens, or twelve
       // parts of four where an item has more (one token's items have ten).
       // Parts past the last and tokens past the rows are loaded again, not added.
