@@ -140,9 +140,8 @@ struct Walk {
   int row0, rows, tile, tiles, u0, u1;
   bool more;
 
-  // e0: the expert of the CTA's first segment
-  __device__ Walk(const Plan& plan, int e0)
-      : p(plan), pos(plan.chunks ? static_cast<int>(blockIdx.x) : plan.begin), item(-1), e(e0) {
+  __device__ explicit Walk(const Plan& plan)
+      : p(plan), pos(plan.chunks ? static_cast<int>(blockIdx.x) : plan.begin), item(-1), e(0) {
     advance();
   }
   __device__ void advance() {
@@ -306,7 +305,7 @@ __device__ __forceinline__ void store_tokens(const MxArgs& a, const uint32_t (&l
 // Eight tokens of a summed item (this lane's weight row `lrow` of tile
 // `tile`), `n` of them valid, at `out`.
 template <bool kGateUp>
-__device__ __forceinline__ void store_columns(const MxArgs& a, const float (&v)[8], uint16_t* out, int tile, int lrow,
+__device__ __forceinline__ void store_columns(const float (&v)[8], uint16_t* out, int ldc, int tile, int lrow,
                                               int n) {
   if (kGateUp) {
     // lanes 0-15 hold gate rows, 16-31 the up rows of the same indices: of
@@ -318,14 +317,50 @@ __device__ __forceinline__ void store_columns(const MxArgs& a, const float (&v)[
       const float other = __shfl_xor_sync(0xffffffffu, up ? v[c] : v[c + 1], 16);
       const float h = silu_mul(up ? other : v[c], up ? v[c + 1] : other);
       const int cc = c + (up ? 1 : 0);
-      if (cc < n && col < a.ldc) out[static_cast<size_t>(cc) * a.ldc + col] = f32_to_bf16_rn(h);
+      if (cc < n && col < ldc) out[static_cast<size_t>(cc) * ldc + col] = f32_to_bf16_rn(h);
     }
   } else {
     const int col = kMxTileRows * tile + lrow;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-      if (c < n && col < a.ldc) out[static_cast<size_t>(c) * a.ldc + col] = f32_to_bf16_rn(v[c]);
+      if (c < n && col < ldc) out[static_cast<size_t>(c) * ldc + col] = f32_to_bf16_rn(v[c]);
   }
+}
+
+// The sum of an item's parts first .. last in K order, to C (this lane's weight
+// row).  Twelve 16-byte loads in flight: six parts of eight tokens, or twelve
+// parts of four where an item has more (one token's items have nine).  Parts
+// past the last and tokens past the rows are loaded again, not added.
+template <bool kGateUp>
+__device__ __forceinline__ void add_parts(const float* partial, int first, int last, int rows, uint16_t* out, int ldc,
+                                       int tile, int lrow) {
+  auto add = [&](auto parts_c, auto quads_c) {
+    constexpr int kParts = decltype(parts_c)::value, kQuads = decltype(quads_c)::value;
+    for (int c0 = 0; c0 < rows; c0 += 4 * kQuads) {
+      float f[8] = {};
+      for (int p0 = first; p0 <= last; p0 += kParts) {
+        float4 x[kParts][kQuads];
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          const int p = min(p0 + i, last);
+          const float* src = partial + static_cast<size_t>(2 * p + (p == first)) * kSlotFloats + c0 * 128;
+#pragma unroll
+          for (int c = 0; c < kQuads; ++c) x[i][c] = ld_cg_f4(src + (c0 + 4 * c < rows ? 512 * c : 0));
+        }
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+          if (p0 + i <= last)
+#pragma unroll
+            for (int c = 0; c < kQuads; ++c) {
+              f[4 * c] += x[i][c].x, f[4 * c + 1] += x[i][c].y;
+              f[4 * c + 2] += x[i][c].z, f[4 * c + 3] += x[i][c].w;
+            }
+      }
+      store_columns<kGateUp>(f, out + static_cast<size_t>(c0) * ldc, ldc, tile, lrow, min(rows - c0, 4 * kQuads));
+    }
+  };
+  if (last - first < 6) add(std::integral_constant<int, 6>{}, std::integral_constant<int, 2>{});
+  else add(std::integral_constant<int, 12>{}, std::integral_constant<int, 1>{});
 }
 
 template <bool kGateUp>
@@ -338,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   __shared__ uint32_t tmem_base_s;
   __shared__ int prefix[kMaxExperts + 1];
   __shared__ int warp_sum[kThreads / 32], warp_max[kThreads / 32];
-  __shared__ int hdr_ok, last_flag, first_expert;
+  __shared__ int hdr_ok, last_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -379,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
   const int per = (a.E + kThreads - 1) / kThreads;
   const int n_pairs = (a.n_tiles + kPair - 1) / kPair;
-  int mine = 0, most = 16, own[kPer + 1];   // items before each of the thread's experts
+  int mine = 0, most = 16, own[kPer];   // items before each of the thread's experts
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid * per + i;
@@ -397,7 +432,6 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       most = max(most, tile_rows(cnt, n_rt));
     }
   }
-  own[kPer] = mine;
   if (tid == kThreads - 1) {
     hdr_ok = h0.x == kMxMagic && h0.y == kMxVersion && static_cast<int>(h0.z) >= a.E &&
              static_cast<int>(h0.w) == a.N && static_cast<int>(h1.x) == a.K && static_cast<int>(h1.y) == (kGateUp ? 1 : 0);
@@ -428,11 +462,21 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   tok = __reduce_max_sync(0xffffffffu, tok);
   const int run = inc - mine + (warp ? __shfl_sync(0xffffffffu, sum, warp - 1) : 0);
 
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = tid * per + i;
+    if (i >= per || e >= a.E) continue;
+    prefix[e] = run + own[i];
+  }
+  if (tid == kThreads - 1) prefix[a.E] = run + mine;   // the last thread ends at the total
+  __syncthreads();
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, tmem_base_s, 0);
+  tok = __shfl_sync(0xffffffffu, tok, 0);
   const int units = mx_units(a.K), ctas = gridDim.x, cta = blockIdx.x;
   Plan plan;
   plan.prefix = prefix, plan.cnts = a.counts, plan.offs = a.offsets;
   plan.E = a.E, plan.n_tiles = a.n_tiles, plan.units = units, plan.max_tok = a.max_tok;
-  plan.items = hdr_ok ? __shfl_sync(0xffffffffu, sum, 31) : 0;
+  plan.items = hdr_ok ? prefix[a.E] : 0;
   plan.cut = plan.items % ctas;
   // Divided by rows: about one (tile, run of rows) for each CTA.  (With a
   // single unit nothing is cut along K and there are no partials.)
@@ -465,21 +509,6 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       }
     }
   }
-  // the expert of this CTA's first segment
-  const int first_item = plan.end > plan.begin ? plan.begin / units
-                         : plan.chunks && cta < kPair * plan.chunks * plan.cut ? cta / (kPair * plan.chunks)
-                                                                               : plan.cut + cta;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = tid * per + i;
-    if (i >= per || e >= a.E) continue;
-    const int lo = run + own[i];
-    prefix[e] = lo;
-    if (lo <= first_item && first_item < run + own[i + 1]) first_expert = e;
-  }
-  if (tid == kThreads - 1) prefix[a.E] = run + mine;   // the last thread ends at the total
-  __syncthreads();
-  const uint32_t tmem_base = __shfl_sync(0xffffffffu, tmem_base_s, 0);
   const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget / stage);
   const int n_acc = min(kMaxAcc, kSfCol / (kPair * tok));
   ItemRing items{item_full, item_empty, item_slots, 0, 0};
@@ -609,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     }
   } else if (warp == kItemWarp) {
     // ----------------------------------------------------------------- items
-    Walk walk(plan, first_expert);
+    Walk walk(plan);
     int slot = 0, ph = 0;
     for (bool first = true, more = true; more;) {
       if (!first && !__all_sync(0xffffffffu, mbar_wait_backoff(&item_empty[slot], ph ^ 1, a.status))) break;
@@ -690,46 +719,19 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       }
       epilogue_all(true);
       if (tid == 32 * kEpiWarp0) {
-        __threadfence();   // the parts stored by all threads before the barrier
-        const int done = atomicAdd(a.split_cnt + first, 1) == last - first;
-        if (done) atomicExch(a.split_cnt + first, 0);    // zero for the next launch
-        __threadfence();
-        last_flag = done;
+        // releases the parts stored by all threads before the barrier, and
+        // acquires the others'
+        int arrived;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                     : "=r"(arrived)
+                     : "l"(a.split_cnt + first)
+                     : "memory");
+        last_flag = arrived == last - first;
       }
       epilogue_all(true);
       if (!last_flag) continue;
-      // Twelve 16-byte loads in flight: six parts of eight tokens, or twelve
-      // parts of four where an item has more (one token's items have ten).
-      // Parts past the last and tokens past the rows are loaded again, not added.
-      auto add = [&](auto parts_c, auto tokens_c) {
-        constexpr int kParts = decltype(parts_c)::value, kQuads = decltype(tokens_c)::value / 4;
-        for (int c0 = 0; c0 < rows; c0 += 4 * kQuads) {
-          float f[8] = {};
-          for (int p0 = first; p0 <= last; p0 += kParts) {
-            float4 x[kParts][kQuads];
-#pragma unroll
-            for (int i = 0; i < kParts; ++i) {
-              const int p = min(p0 + i, last);
-              const float* src =
-                  a.partial + static_cast<size_t>(2 * p + (p == first)) * kSlotFloats + part + c0 * 128;
-#pragma unroll
-              for (int c = 0; c < kQuads; ++c) x[i][c] = ld_cg_f4(src + (c0 + 4 * c < rows ? 512 * c : 0));
-            }
-#pragma unroll
-            for (int i = 0; i < kParts; ++i)
-              if (p0 + i <= last)
-#pragma unroll
-                for (int c = 0; c < kQuads; ++c) {
-                  f[4 * c] += x[i][c].x, f[4 * c + 1] += x[i][c].y;
-                  f[4 * c + 2] += x[i][c].z, f[4 * c + 3] += x[i][c].w;
-                }
-          }
-          store_columns<kGateUp>(a, f, out + static_cast<size_t>(c0) * a.ldc, w.tile + t, lrow,
-                        min(rows - c0, 4 * kQuads));
-        }
-      };
-      if (last - first < 6) add(std::integral_constant<int, 6>{}, std::integral_constant<int, 8>{});
-      else add(std::integral_constant<int, 12>{}, std::integral_constant<int, 4>{});
+      if (tid == 32 * kEpiWarp0) a.split_cnt[first] = 0;   // for the next launch
+      add_parts<kGateUp>(a.partial + part, first, last, rows, out, a.ldc, w.tile + t, lrow);
     }
   }
 
