@@ -414,7 +414,7 @@ int chord_moe_layer(const chord_bf16* x, const float* logits, const float* bias,
  *             increasing j (dweights: FP32), rounded once
  *   *_stride  row strides in elements; rows that are read may overlap
  *             (stride 0: one row for all), rows that are written may not
- *   H         any length; 16-byte accesses where bases, strides and H allow
+ *   H         1 to 2^24; 32-byte accesses where bases, strides and H allow
  *   sorted_token_ids, num_tokens_post_padded, sorted_positions
  *             as chord_moe_align writes them for this M, topk and capacity
  * topk <= 32.  Results are the same from call to call (no atomics).
@@ -444,7 +444,7 @@ int chord_moe_unpermute_backward(const void* dout, const void* y, int dtype, int
  *               infinity or a NaN gets s = 255 and codes 0, and reads as NaN.
  *               x [rows, K] of `dtype`, codes [rows, K/2], scales [rows, K/32]
  *   dequantize  the inverse: out [rows, K] of `dtype`, rounded once
- * K % 32 == 0; codes 16-byte aligned.
+ * K % 32 == 0, K <= 2^24; codes 16-byte aligned.
  */
 int chord_mxfp4_quantize(const void* x, int dtype, int64_t x_stride, int64_t rows, int K, uint8_t* codes,
                          uint8_t* scales, void* stream);
@@ -469,7 +469,8 @@ int chord_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
  *                  (each token is quantised once), or, with sorted_positions
  *                  NULL, row r of x to row r for r < num_tokens_post_padded
  *                  (a previous product's C).  `rows` holds
- *                  chord_mxfp4_rows_bytes(capacity, K) bytes, 16-byte aligned;
+ *                  chord_mxfp4_rows_bytes(capacity, K) bytes, 16-byte aligned,
+ *                  laid out for this capacity, which the product is given too;
  *                  num_tokens_post_padded may be NULL with positions.
  *   workspace      chord_mxfp4_moe_gemm_workspace_bytes() bytes, 16-byte
  *                  aligned, zeroed once when allocated; every call leaves its

@@ -44,6 +44,7 @@ def test_rows_are_checked(L):
     refused(L, ARG, "topk", f(k=33))
     refused(L, ARG, "M=-1", f(M=-1))
     refused(L, ARG, "row length", f(H=0))
+    refused(L, ARG, "row length", f(H=(1 << 24) + 1, xs=1 << 25, os=1 << 25))
     refused(L, ARG, "stride", f(os=63))
     refused(L, ARG, "stride", f(xs=-1))
     refused(L, ARG, "x", f(x=None))
@@ -85,7 +86,8 @@ def test_product_is_checked(L):
     refused(L, ARG, "K=100", f(K=100))
     refused(L, ARG, "epilogue", f(epi=chord.CHORD_EPI_WEIGHTED_ADD))
     refused(L, ARG, "SiLU", f(N=8, epi=chord.CHORD_EPI_SILU_MUL))
-    refused(L, ARG, "too large", f(K=1 << 25))
+    refused(L, ARG, "2^24", f(K=1 << 25))
+    refused(L, ARG, "too large", f(cap=1 << 30, N=1 << 20))
     refused(L, ARG, "null", f(C=None))
     refused(L, ARG, "16-byte", f(w=ctypes.c_void_p(24)))
     refused(L, ARG, "rows", f(rb=100))

@@ -229,6 +229,29 @@ def test_another_stream_and_repeats():
     close(out, xs * ws.sum(1)[:, None], np.abs(xs) * np.abs(ws).sum(1)[:, None], o.k, 2.0 ** -8, "round trip")
 
 
+def test_offsets_beyond_32_bits():
+    """Rows whose element offsets pass 2^31 and byte offsets pass 2^32."""
+    M, H = 70000, 32768
+    assert M * H > 2 ** 31
+    x = torch.zeros((M, H), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = rows(3, H, torch.bfloat16, 1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pos = torch.arange(M - 1, -1, -1, **i32)                 # reversed, then turned back
+    pos[0], pos[M - 1] = M - 1, 0
+    f, ntpp, w = torch.empty(M, **i32), torch.tensor([M], **i32), torch.ones((M, 1), device="cuda")
+    f[pos.long()] = torch.arange(M, **i32)
+    y, back = torch.empty_like(x), torch.empty_like(x)
+    chord.chord_moe_permute(x, pos, f, ntpp, 1, y)
+    assert torch.equal(y[pos[-3:].long()], x[-3:]) and not y[3:M - 3].any()
+    chord.chord_moe_unpermute(y, w, pos, back)
+    assert torch.equal(back, x)
+    dw = torch.empty((M, 1), device="cuda")
+    chord.chord_moe_unpermute_backward(x, y, w, pos, f, ntpp, back, dw)
+    assert torch.equal(back, y)
+    t = f64(x[-3:]) ** 2
+    close(dw[-3:, 0], t.sum(1), t.sum(1), H, 2.0 ** -24, "dweights")
+
+
 def test_in_a_cuda_graph():
     o, H = Order(16, 8, 0, 8, 2, 16, seed=9), 256
     x = rows(o.M, H, torch.bfloat16, 1).contiguous()

@@ -325,6 +325,31 @@ def test_many_rows():
     ex.check(ex.product(True), True)
 
 
+def test_offsets_beyond_32_bits():
+    """x beyond 2^32 elements, the row operand beyond 2^31 bytes: the last rows' product."""
+    M, K, N = 270000, 16384, 16
+    ex = Experts([3], 16, N, K, 29)
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = ex.x
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pos, counts, offsets = torch.arange(M, **i32), torch.tensor([M], **i32), torch.tensor([0, M], **i32)
+    cap = M
+    assert M * K > 2 ** 32 and chord.chord_mxfp4_rows_bytes(cap, K) > 2 ** 31
+    r = torch.empty(chord.chord_mxfp4_rows_bytes(cap, K), dtype=torch.uint8, device="cuda")
+    C = torch.full((cap, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    chord.chord_mxfp4_quantize_rows(x, pos, 1, None, cap, r)
+    chord.chord_mxfp4_moe_gemm(r, ex.pack(False), 1, N, K, counts, offsets, cap, chord.CHORD_EPI_STORE, C, workspace())
+    a, w = values(*ref_quantize(ex.x.double().cpu().numpy())), values(ex.code[0], ex.scale[0])
+    bound = 2.0 ** -8 * np.abs(a @ w.T) + K * 2.0 ** -23 * (np.abs(a) @ np.abs(w).T)
+    assert (np.abs(C[-3:].double().cpu().numpy() - a @ w.T) <= bound).all()
+    assert not C[:-3].any()
+    codes = torch.empty((M, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((M, K // 32), dtype=torch.uint8, device="cuda")
+    chord.chord_mxfp4_quantize(x, codes, scales)
+    chord.chord_mxfp4_dequantize(codes, scales, x)
+    assert np.array_equal(x[-3:].double().cpu().numpy(), a) and not x[:-3].any()
+
+
 def test_stream_and_graph():
     ex = Experts([3, 2, 9], 16, 256, 512, 26)
     packed, rows, ws = ex.pack(False), ex.rows(), torch.zeros_like(workspace())

@@ -20,7 +20,7 @@ int check_rows(int dtype, int M, int topk, int H, size_t capacity) {
   if (!chord::dtype_bytes(dtype)) return fail(CHORD_ERR_INVALID_ARG, "unknown dtype %d", dtype);
   if (M < 0 || topk < 1 || topk > 32) return fail(CHORD_ERR_INVALID_ARG, "bad M=%d or topk=%d (1 <= topk <= 32)", M, topk);
   if (static_cast<long long>(M) * topk > (1LL << 30)) return fail(CHORD_ERR_INVALID_ARG, "M*topk too large");
-  if (H < 1) return fail(CHORD_ERR_INVALID_ARG, "row length %d < 1", H);
+  if (H < 1 || H > (1 << 24)) return fail(CHORD_ERR_INVALID_ARG, "row length %d not in [1, 2^24]", H);
   if (capacity > (1u << 30)) return fail(CHORD_ERR_INVALID_ARG, "%zu rows: too many", capacity);
   return CHORD_OK;
 }
@@ -37,7 +37,8 @@ int check_matrix(const char* name, const void* p, int dtype, long long stride, i
 }
 
 int check_mx(const char* what, int K) {
-  if (K < 1 || K % 32 != 0) return fail(CHORD_ERR_INVALID_ARG, "%s: K=%d must be a positive multiple of 32", what, K);
+  if (K < 1 || K % 32 != 0 || K > (1 << 24))
+    return fail(CHORD_ERR_INVALID_ARG, "%s: K=%d must be a positive multiple of 32 up to 2^24", what, K);
   return CHORD_OK;
 }
 
@@ -188,8 +189,8 @@ int chord_mxfp4_moe_gemm(const void* rows, size_t rows_bytes, const void* packed
     return fail(CHORD_ERR_INVALID_ARG, "SiLU*mul needs N %% 16 == 0 (N=%d)", N);
   if (capacity > (1u << 30)) return fail(CHORD_ERR_INVALID_ARG, "%zu rows: too many", capacity);
   // item and unit counts fit 32 bits with room
-  if (K > (1 << 24) || (capacity / 16 + E_local) * (static_cast<size_t>(N) / 256 + 1) > (1u << 30))
-    return fail(CHORD_ERR_INVALID_ARG, "K=%d or %zu rows x N=%d: too large", K, capacity, N);
+  if ((capacity / 16 + E_local) * (static_cast<size_t>(N) / 256 + 1) > (1u << 30))
+    return fail(CHORD_ERR_INVALID_ARG, "%zu rows x N=%d: too large", capacity, N);
   if (capacity == 0) return CHORD_OK;
   if (!rows || !packed_w || !expert_counts || !expert_offsets || !C) return fail(CHORD_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(rows) || !aligned16(packed_w) || !aligned16(C))

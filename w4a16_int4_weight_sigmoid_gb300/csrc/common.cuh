@@ -296,6 +296,15 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rn(float f) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
+// Multiprocessors of the current device (1 when it cannot be told).
+inline int sm_count() {
+  static int sms[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+  return sms[dev] > 0 ? sms[dev] : 1;
+}
+
 // Raise a kernel's dynamic shared-memory limit once per (kernel, device):
 // the first call must precede any stream capture; later calls make no CUDA
 // call.  Keyed by the kernel itself (a template argument), not its type.

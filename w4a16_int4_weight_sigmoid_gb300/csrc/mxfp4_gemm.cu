@@ -763,16 +763,7 @@ cudaError_t mxfp4_gemm_launch(const uint8_t* rows, const uint8_t* w, int E, int 
   cudaError_t err = gate_up ? ensure_smem_limit<mxfp4_gemm_kernel<true>>(kSmemBytes)
                             : ensure_smem_limit<mxfp4_gemm_kernel<false>>(kSmemBytes);
   if (err != cudaSuccess) return err;
-  static int sms[64] = {0};
-  int dev = 0;
-  err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!sms[dev]) {
-    err = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
-    if (err != cudaSuccess) return err;
-  }
-  return launch_kernel(gate_up ? mxfp4_gemm_kernel<true> : mxfp4_gemm_kernel<false>, dim3(sms[dev] < kMxMaxCtas ? sms[dev] : kMxMaxCtas), dim3(kThreads),
+  return launch_kernel(gate_up ? mxfp4_gemm_kernel<true> : mxfp4_gemm_kernel<false>, dim3(sm_count() < kMxMaxCtas ? sm_count() : kMxMaxCtas), dim3(kThreads),
                        kSmemBytes, st, true, a);
 }
 

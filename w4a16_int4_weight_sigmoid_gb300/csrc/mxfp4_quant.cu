@@ -317,9 +317,7 @@ __global__ void mx_prepack_kernel(const uint8_t* __restrict__ codes, const uint8
 
 template <typename T>
 dim3 grid_for(int columns, long long rows, int waves) {
-  static int sms = 0;
-  if (!sms) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, 0);
-  const long long most = std::max(1LL, static_cast<long long>(waves) * kCtas<T> * sms / columns);
+  const long long most = std::max(1LL, static_cast<long long>(waves) * kCtas<T> * sm_count() / columns);
   return dim3(columns, static_cast<unsigned>(std::min({rows, most, 65535LL})));
 }
 

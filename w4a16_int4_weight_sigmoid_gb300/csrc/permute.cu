@@ -251,14 +251,6 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a,
   }
 }
 
-int sm_count() {
-  static int sms[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  if (!sms[dev]) cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
-  return sms[dev] > 0 ? sms[dev] : 1;
-}
-
 template <int B>
 cudaError_t launch_permute(const RowArgs& a, int elem, cudaStream_t st) {
   const int row_bytes = a.H * elem;
