@@ -108,7 +108,23 @@ struct MxArgs {
 // and 224 rows).  They even out at about 15 units.
 constexpr int kShortTok = 96, kShortUnits = 14;
 inline int largest_tile(int units) { return units <= kShortUnits ? kShortTok : kMaxTok; }
-__device__ __forceinline__ int row_tiles(int cnt, int max_tok) { return (cnt + max_tok - 1) / max_tok; }
+__device__ __forceinline__ int row_tiles(int cnt, int max_tok) {
+  return max_tok == kMaxTok ? (cnt + kMaxTok - 1) / kMaxTok : (cnt + kShortTok - 1) / kShortTok;
+}
+// a / b for 0 <= a < 2^24, 0 < b and a quotient below 2^20 (the correction
+// makes up for a division that is one off): a launch's first instructions are
+// fetched as they run, and an integer division is three times as many.
+__device__ __forceinline__ int small_div(int a, int b) {
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  q -= q * b > a;
+  q += (q + 1) * b <= a;
+  return q;
+}
+__device__ __forceinline__ float approx_sqrt(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // Rows of an expert's row tiles: equal to within the rounding to 16.
 __device__ __forceinline__ int tile_rows(int cnt, int n_rt) {
   return ((n_rt > 1 ? (cnt + n_rt - 1) / n_rt : cnt) + 15) & ~15;
@@ -411,21 +427,21 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
 
   // first item of each expert, and the largest row tile: thread i covers
   // experts [i * per, (i + 1) * per)
-  constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
-  const int per = (a.E + kThreads - 1) / kThreads;
+  const int per = 1 + (a.E > kThreads) + (a.E > 2 * kThreads);
+  static_assert(3 * kThreads >= kMaxExperts, "three experts per thread at most");
   const int n_pairs = (a.n_tiles + kPair - 1) / kPair;
-  int mine = 0, most = 16, own[kPer];   // items before each of the thread's experts
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  int mine = 0, most = 16;
+#pragma unroll 1
+  for (int i = 0; i < per; ++i) {
     const int e = tid * per + i;
-    own[i] = mine;
-    if (i >= per || e >= a.E) continue;
+    if (e >= a.E) break;
     int cnt = ld_ca(a.counts + e);
     const int off = ld_ca(a.offsets + e);
     if (cnt < 0 || off < 0 || off % 8 != 0 || cnt > a.capacity || off > a.capacity - cnt) {
       set_status(a.status, CHORD_ERR_INVALID_ARG);   // not an aligned order of `capacity` rows
       cnt = 0;
     }
+    prefix[e] = mine;
     if (cnt > 0) {
       const int n_rt = cnt <= a.max_tok ? 1 : row_tiles(cnt, a.max_tok);
       mine += n_pairs * n_rt;
@@ -462,11 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   tok = __reduce_max_sync(0xffffffffu, tok);
   const int run = inc - mine + (warp ? __shfl_sync(0xffffffffu, sum, warp - 1) : 0);
 
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+#pragma unroll 1
+  for (int i = 0; i < per; ++i) {
     const int e = tid * per + i;
-    if (i >= per || e >= a.E) continue;
-    prefix[e] = run + own[i];
+    if (e >= a.E) break;
+    prefix[e] += run;
   }
   if (tid == kThreads - 1) prefix[a.E] = run + mine;   // the last thread ends at the total
   __syncthreads();
@@ -480,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   plan.cut = plan.items % ctas;
   // Divided by rows: about one (tile, run of rows) for each CTA.  (With a
   // single unit nothing is cut along K and there are no partials.)
-  plan.chunks = tok > kSplitTok && units > 1 && plan.cut > 0 ? min(max(ctas / (kPair * plan.cut), 1), tok / 16) : 0;
+  plan.chunks = tok > kSplitTok && units > 1 && plan.cut > 0 ? min(max(small_div(ctas, kPair * plan.cut), 1), tok / 16) : 0;
   // Divided along K: where two or more CTAs come to an item, each item into as
   // many equal parts, so that a CTA has one segment to hand over; otherwise
   // all items' units into one range per CTA.  A part of u units costs u units'
@@ -489,16 +505,16 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   // square root of units * tok / 80.  No part is empty, and an item's parts
   // are in consecutive CTAs.
   const int total = plan.chunks ? 0 : plan.cut * units;   // the host keeps this far below 2^31
-  const int least = max(1, static_cast<int>(sqrtf(units * tok / 80.f)));
+  const int least = max(1, static_cast<int>(approx_sqrt(units * tok * (1 / 80.f))));
   int parts = 0, ranges = 0;
   plan.begin = plan.end = 0;
   if (total > 0) {
-    parts = min(ctas / plan.cut, units / least);
+    parts = min(small_div(ctas, plan.cut), small_div(units, least));
     if (parts >= 2) {
-      const int item = cta / parts, part = cta - item * parts;
+      const int item = small_div(cta, parts), part = cta - item * parts;
       if (item < plan.cut) {
-        plan.begin = item * units + part * units / parts;
-        plan.end = item * units + (part + 1) * units / parts;
+        plan.begin = item * units + small_div(part * units, parts);
+        plan.end = item * units + small_div((part + 1) * units, parts);
       }
     } else {
       parts = 0;
