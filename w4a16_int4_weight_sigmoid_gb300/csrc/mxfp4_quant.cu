@@ -19,7 +19,7 @@
 namespace chord {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 // CTAs per SM that the kernels are compiled for, and the grid in such waves,
 // each CTA walking on to its next row.  8192 x 7168 BF16: dequantising took
 // 25.0 us with two waves, 23.9 with four, 34 with a CTA for every row;
@@ -127,13 +127,16 @@ __device__ __forceinline__ uint4 quantize_run(const Run<T>& r, uint32_t& scale) 
 }
 
 // ---------------------------------------------------------------- row-major
-// CTA column: a run of each thread; rows blockIdx.y, + gridDim.y, ..., two at
-// a time so that the second's loads are in flight while the first is worked on.
+// A thread's block g of rows r, r + step, ..., two at a time so that the
+// second's loads are in flight while the first is worked on.  2^cols_log2
+// threads of a CTA lie along the row and the rest on other rows, so short rows
+// leave no threads idle.
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads, kCtas<T>) quantize_kernel(const T* x, long long ldx, long long rows, int K,
                                                             uint8_t* __restrict__ codes,
-                                                            uint8_t* __restrict__ scales) {
-  const int g = blockIdx.x * kThreads + threadIdx.x;
+                                                            uint8_t* __restrict__ scales, int cols_log2) {
+  const int g = (blockIdx.x << cols_log2) + (threadIdx.x & ((1 << cols_log2) - 1)), per = kThreads >> cols_log2;
+  const long long first = static_cast<long long>(blockIdx.y) * per + (threadIdx.x >> cols_log2), step = gridDim.y * per;
   const bool in = g < K / kRun;
   grid_dep_wait();
   grid_dep_launch();
@@ -148,30 +151,31 @@ __global__ void __launch_bounds__(kThreads, kCtas<T>) quantize_kernel(const T* x
       scales[r * (K / kMxBlock) + g] = static_cast<uint8_t>(scale);
     }
   };
-  for (long long r = blockIdx.y; r < rows; r += 2 * gridDim.y) {
+  for (long long r = first; r < rows; r += 2 * step) {
     Run<T> v0{}, v1{};
     load(r, v0);
-    load(r + gridDim.y, v1);
+    load(r + step, v1);
     store(r, v0);
-    store(r + gridDim.y, v1);
+    store(r + step, v1);
   }
 }
 
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads, kCtas<T>) dequantize_kernel(const uint8_t* codes,
                                                               const uint8_t* scales, long long rows,
-                                                              int K, T* __restrict__ out, long long ldo) {
-  const int g = blockIdx.x * kThreads + threadIdx.x;
+                                                              int K, T* __restrict__ out, long long ldo, int cols_log2) {
+  const int g = (blockIdx.x << cols_log2) + (threadIdx.x & ((1 << cols_log2) - 1)), per = kThreads >> cols_log2;
+  const long long first = static_cast<long long>(blockIdx.y) * per + (threadIdx.x >> cols_log2), step = gridDim.y * per;
   grid_dep_wait();
   grid_dep_launch();
   if (g >= K / kRun) return;
   constexpr int kRows = 2;   // rows in flight
-  for (long long r = blockIdx.y; r < rows; r += kRows * gridDim.y) {
+  for (long long r = first; r < rows; r += kRows * step) {
     Chunk<16> q[kRows];
     uint32_t code[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      const long long row = r + static_cast<long long>(j) * gridDim.y;
+      const long long row = r + j * step;
       if (row < rows) {
         load_chunk<16>(codes + row * (K / 2) + 16 * g, q[j]);
         asm volatile("ld.global.u8 %0, [%1];" : "=r"(code[j]) : "l"(scales + row * (K / kMxBlock) + g));
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<T>) dequantize_kernel(const ui
     }
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      const long long row = r + static_cast<long long>(j) * gridDim.y;
+      const long long row = r + j * step;
       if (row >= rows) break;
       // 2^(code - 127): code 0 is subnormal, 255 is NaN
       const float scale =
@@ -220,8 +224,10 @@ __global__ void __launch_bounds__(kThreads, kCtas<T>) dequantize_kernel(const ui
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads, kCtas<T>) quantize_rows_kernel(const T* x, long long ldx, int M, int K,
                                                                  const int32_t* pos, int topk, const int32_t* ntpp,
-                                                                 int rows, uint8_t* __restrict__ out) {
-  const int g = blockIdx.x * kThreads + threadIdx.x, lane = threadIdx.x & 31;
+                                                                 int rows, uint8_t* __restrict__ out, int wpt_log2) {
+  // 2^wpt_log2 warps (1, 2 or 4) of a CTA share a token
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tokens = kWarps >> wpt_log2;
+  const int g = ((blockIdx.x << wpt_log2) + (warp & ((1 << wpt_log2) - 1))) * 32 + lane;
   const int units = mx_units(K);
   uint8_t* out_scales = out + units * mx_rows_padded(rows) * kMxRowBytes;
   const bool in_unit = g < units * (kMxUnitK / kRun), in = g < K / kRun;
@@ -262,11 +268,11 @@ __global__ void __launch_bounds__(kThreads, kCtas<T>) quantize_rows_kernel(const
       }
     }
   };
-  const int step = gridDim.y;
+  const int step = gridDim.y * tokens, t_first = blockIdx.y * tokens + (warp >> wpt_log2);
   Run<T> v0, v1;
-  int p0 = position(blockIdx.y), p1 = position(blockIdx.y + step);
-  uint32_t left0 = load(p0, v0, blockIdx.y);
-  for (int t = blockIdx.y; t < n; t += 2 * step) {
+  int p0 = position(t_first), p1 = position(t_first + step);
+  uint32_t left0 = load(p0, v0, t_first);
+  for (int t = t_first; t < n; t += 2 * step) {
     const int p2 = position(t + 2 * step), p3 = position(t + 3 * step);
     const uint32_t left1 = load(p1, v1, t + step);
     store(p0, left0, v0);
@@ -321,31 +327,41 @@ dim3 grid_for(int columns, long long rows, int waves) {
   return dim3(columns, static_cast<unsigned>(std::min({rows, most, 65535LL})));
 }
 
+// log2 of the threads along a row of K / 32 blocks.
+int row_threads_log2(int K) {
+  int n = 0;
+  while ((1 << n) < kThreads && (1 << n) < K / kRun) ++n;
+  return n;
+}
+
 template <typename T>
 cudaError_t quantize_t(const void* x, long long ldx, long long rows, int K, uint8_t* codes, uint8_t* scales,
                        cudaStream_t st) {
   const bool wide = row_access_bytes(x, ldx, K, sizeof(T), 32) == 32;
+  const int log2 = row_threads_log2(K), cols = 1 << log2, per = kThreads >> log2;
   return launch_kernel(wide ? quantize_kernel<T, true> : quantize_kernel<T, false>,
-                       grid_for<T>((K / kRun + kThreads - 1) / kThreads, rows, kWaves), dim3(kThreads), 0, st, true,
-                       static_cast<const T*>(x), ldx, rows, K, codes, scales);
+                       grid_for<T>((K / kRun + cols - 1) / cols, (rows + per - 1) / per, kWaves), dim3(kThreads), 0,
+                       st, true, static_cast<const T*>(x), ldx, rows, K, codes, scales, log2);
 }
 
 template <typename T>
 cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, long long rows, int K, void* out, long long ldo,
                          cudaStream_t st) {
   const bool wide = row_access_bytes(out, ldo, K, sizeof(T), 32) == 32;
+  const int log2 = row_threads_log2(K), cols = 1 << log2, per = kThreads >> log2;
   return launch_kernel(wide ? dequantize_kernel<T, true> : dequantize_kernel<T, false>,
-                       grid_for<T>((K / kRun + kThreads - 1) / kThreads, rows, kWaves), dim3(kThreads), 0, st, true, codes,
-                       scales, rows, K, static_cast<T*>(out), ldo);
+                       grid_for<T>((K / kRun + cols - 1) / cols, (rows + per - 1) / per, kWaves), dim3(kThreads), 0,
+                       st, true, codes, scales, rows, K, static_cast<T*>(out), ldo, log2);
 }
 
 template <typename T>
 cudaError_t quantize_rows_t(const void* x, long long ldx, int M, int K, const int32_t* pos, int topk,
                             const int32_t* ntpp, int rows, uint8_t* out, cudaStream_t st) {
   const bool wide = row_access_bytes(x, ldx, K, sizeof(T), 32) == 32;
+  const int warps = (mx_units(K) * kMxRowScales + 31) / 32, wpt = warps >= 3 ? 4 : warps, per = kWarps / wpt;
   return launch_kernel(wide ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>,
-                       grid_for<T>((mx_units(K) * (kMxUnitK / kRun) + kThreads - 1) / kThreads, M, kRowWaves), dim3(kThreads), 0,
-                       st, true, static_cast<const T*>(x), ldx, M, K, pos, topk, ntpp, rows, out);
+                       grid_for<T>((warps + wpt - 1) / wpt, (M + per - 1) / per, kRowWaves), dim3(kThreads), 0, st,
+                       true, static_cast<const T*>(x), ldx, M, K, pos, topk, ntpp, rows, out, wpt / 2);
 }
 
 }  // namespace

@@ -41,7 +41,7 @@ struct RowArgs {
   int M, topk, H, rows;     // rows: capacity of the expert order
 };
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 // CTAs per SM that permute is compiled for, and its grid in such waves: 8192
 // rows of 7168 took 48.3 us with one wave, 45.7 with two, 43.6 with four (the
 // CTAs' shares even out) and 49.2 with a CTA for every token.
@@ -73,20 +73,24 @@ __device__ __forceinline__ void zero_padding(const RowArgs& a, int row_bytes, lo
 
 // ----------------------------------------------------------------- permute
 // Copies, so element types do not matter.  A thread moves one access of a
-// token's row to each of its rows; CTAs walk over the tokens, the next one's
-// row and the positions of the one after it in flight.  The CTAs of the last
-// `pad_y` grid rows zero the padding.
+// token's row to each of its rows; 2^wpt_log2 warps (1, 2 or 4) of a CTA
+// share a token, so that short rows do not leave warps idle.  CTAs walk over the
+// tokens, the next one's row and the positions of the one after it in flight.
+// The CTAs of the last `pad_y` grid rows zero the padding.
 template <int B>
 __global__ void __launch_bounds__(kThreads, kCtas) permute_kernel(RowArgs a, int row_bytes, long long x_stride,
-                                                                  long long out_stride, int pad_y) {
+                                                                  long long out_stride, int pad_y, int wpt_log2) {
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31, step = gridDim.y - pad_y;
-  if (static_cast<int>(blockIdx.y) >= step) {
-    zero_padding<B>(a, row_bytes, out_stride, (blockIdx.y - step) * gridDim.x + blockIdx.x, pad_y * gridDim.x);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, token_ctas = gridDim.y - pad_y;
+  if (static_cast<int>(blockIdx.y) >= token_ctas) {
+    zero_padding<B>(a, row_bytes, out_stride, (blockIdx.y - token_ctas) * gridDim.x + blockIdx.x,
+                    pad_y * gridDim.x);
     return;
   }
-  const int c = (blockIdx.x * kThreads + threadIdx.x) * B;
+  const int tokens = kWarps >> wpt_log2, step = token_ctas * tokens;   // tokens per CTA, and at once
+  const int t_first = blockIdx.y * tokens + (warp >> wpt_log2);
+  const int c = (((blockIdx.x << wpt_log2) + (warp & ((1 << wpt_log2) - 1))) * 32 + lane) * B;
   const bool in = c < row_bytes;
   auto position = [&](int t) {
     const int p = t < a.M && lane < a.topk ? ld_ca(a.pos + static_cast<long long>(t) * a.topk + lane) : -1;
@@ -104,9 +108,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) permute_kernel(RowArgs a, int
     }
   };
   Chunk<B> v0, v1;
-  int p0 = position(blockIdx.y), p1 = position(blockIdx.y + step);
-  uint32_t left0 = load(p0, v0, blockIdx.y);
-  for (int t = blockIdx.y; t < a.M; t += 2 * step) {
+  int p0 = position(t_first), p1 = position(t_first + step);
+  uint32_t left0 = load(p0, v0, t_first);
+  for (int t = t_first; t < a.M; t += 2 * step) {
     const int p2 = position(t + 2 * step), p3 = position(t + 3 * step);
     const uint32_t left1 = load(p1, v1, t + step);
     store(p0, left0, v0);
@@ -118,93 +122,88 @@ __global__ void __launch_bounds__(kThreads, kCtas) permute_kernel(RowArgs a, int
 }
 
 // ---------------------------------------------------- weighted sum of rows
-// CTA (t, chunk): VPT accesses per thread of the token's local rows,
-// four rows in flight, added in increasing j.
-template <typename T, int B, int VPT, bool kWeighted>
+// Warp (t, chunk): VPT accesses per lane of the token's local rows, kRows of
+// them in flight, added in increasing j.  A CTA's warps have four tokens (a
+// CTA per token took 12.0 us for 6521 rows of 272 values).
+template <typename T, int B, int VPT, int kRows, bool kWeighted>
 __global__ void __launch_bounds__(kThreads) combine_kernel(RowArgs a) {
-  constexpr int V = B / sizeof(T), kRows = 4;
-  __shared__ int s_pos[kMaxTopk];
-  __shared__ float s_w[kMaxTopk];
-  __shared__ int s_n;
-  const int t = blockIdx.x, tid = threadIdx.x;
+  constexpr int V = B / sizeof(T);
+  const int lane = threadIdx.x & 31, t = blockIdx.x * kWarps + threadIdx.x / 32;
   grid_dep_wait();
   grid_dep_launch();
-  if (tid < 32) {
-    int p = -1;
-    float wj = 1.f;
-    if (tid < a.topk) {
-      const long long o = static_cast<long long>(t) * a.topk + tid;
-      p = ld_ca(a.pos + o);
-      if (kWeighted) wj = ld_ca(a.w + o);
-    }
-    if (p >= a.rows) p = -1;
-    const uint32_t local = __ballot_sync(0xffffffffu, p >= 0);
-    if (p >= 0) {
-      const int k = __popc(local & ((1u << tid) - 1u));
-      s_pos[k] = p;
-      s_w[k] = wj;
-    }
-    if (tid == 0) s_n = __popc(local);
+  if (t >= a.M) return;
+  int p = -1;
+  float w = 1.f;
+  if (lane < a.topk) {
+    const long long o = static_cast<long long>(t) * a.topk + lane;
+    p = ld_ca(a.pos + o);
+    if (kWeighted) w = ld_ca(a.w + o);
   }
-  __syncthreads();
-  const int n = s_n, nv = a.H / V, c0 = blockIdx.y * kThreads * VPT + tid;
+  uint32_t left = __ballot_sync(0xffffffffu, p >= 0 && p < a.rows);
+  const int nv = a.H / V, c0 = blockIdx.y * 32 * VPT + lane;
   float acc[VPT][V];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[i][e] = 0.f;
-  for (int j0 = 0; j0 < n; j0 += kRows) {
+  while (left) {
     Chunk<B> v[kRows][VPT];
+    float wj[kRows];
+    const uint32_t batch = left;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (!left) break;
+      const int j = __ffs(left) - 1;
+      left &= left - 1;
+      const T* src = static_cast<const T*>(a.y) + __shfl_sync(0xffffffffu, p, j) * a.ldy;
+      wj[r] = __shfl_sync(0xffffffffu, w, j);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (c0 + 32 * i < nv) load_chunk<B>(src + V * (c0 + 32 * i), v[r][i]);
+    }
+    const int n = __popc(batch ^ left);
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
-      if (j0 + r < n) {
-        const T* src = static_cast<const T*>(a.y) + s_pos[j0 + r] * a.ldy;
+      if (r < n)
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-          if (c0 + i * kThreads < nv) load_chunk<B>(src + V * (c0 + i * kThreads), v[r][i]);
-      }
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      if (j0 + r < n) {
-        const float wj = s_w[j0 + r];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-          if (c0 + i * kThreads < nv)
+          if (c0 + 32 * i < nv)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
               const float y = chunk_f32<T, B>(v[r][i], e);
-              acc[i][e] = kWeighted ? fmaf(wj, y, acc[i][e]) : acc[i][e] + y;
+              acc[i][e] = kWeighted ? fmaf(wj[r], y, acc[i][e]) : acc[i][e] + y;
             }
-      }
   }
   T* dst = static_cast<T*>(a.out) + t * a.ldo;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
-    if (c0 + i * kThreads < nv) {
+    if (c0 + 32 * i < nv) {
       Chunk<B> o;
       f32_chunk<T, B>(o, acc[i]);
-      store_chunk<B>(dst + V * (c0 + i * kThreads), o);
+      store_chunk<B>(dst + V * (c0 + 32 * i), o);
     }
 }
 
 // ------------------------------------------------- gradient of the weighted sum
-// CTA (t, s) after the padding CTAs: assignments j = s, s + S, ... of token t
-// (S = gridDim.y).  One pass over dout[t] and y[p] gives both dy[p] and the
-// dot product; dout[t] comes from L1 for every j after the first.
-template <typename T, int B>
+// A group of kGroup threads (a CTA, or for short rows a warp) per (t, s) after
+// the padding CTAs: assignments j = s, s + S, ... of token t (S = gridDim.y).
+// One pass over dout[t] and y[p] gives both dy[p] and the dot product; dout[t]
+// comes from L1 for every j after the first.
+template <typename T, int B, int kGroup>
 __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a, int pad_ctas) {
   constexpr int V = B / sizeof(T), kUnroll = B >= 32 ? 2 : 4;
-  __shared__ float s_part[kMaxTopk][kThreads / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ float s_part[kGroup == 32 ? 1 : kMaxTopk][kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x % kGroup;
   grid_dep_wait();
   grid_dep_launch();
   if (static_cast<int>(blockIdx.x) < pad_ctas) {
     if (blockIdx.y == 0)
-      zero_padding<B>(a, a.H * static_cast<int>(sizeof(T)), a.ldo * static_cast<long long>(sizeof(T)),
-                      blockIdx.x, pad_ctas);
+      zero_padding<B>(a, a.H * static_cast<int>(sizeof(T)), a.ldo * static_cast<long long>(sizeof(T)), blockIdx.x,
+                      pad_ctas);
     return;
   }
-  const int t = blockIdx.x - pad_ctas, nv = a.H / V;
+  const int t = (blockIdx.x - pad_ctas) * (kThreads / kGroup) + (kGroup == 32 ? warp : 0), nv = a.H / V;
+  if (kGroup == 32 && t >= a.M) return;
   const T* g = static_cast<const T*>(a.x) + t * a.ldx;
   for (int j = blockIdx.y; j < a.topk; j += gridDim.y) {
     const long long f = static_cast<long long>(t) * a.topk + j;
@@ -214,17 +213,17 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a,
     if (p >= 0 && p < a.rows) {
       const T* y = static_cast<const T*>(a.y) + p * a.ldy;
       T* dy = static_cast<T*>(a.out) + p * a.ldo;
-      for (int c0 = tid; c0 < nv; c0 += kUnroll * kThreads) {
+      for (int c0 = tid; c0 < nv; c0 += kUnroll * kGroup) {
         Chunk<B> vg[kUnroll], vy[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
-          if (c0 + i * kThreads < nv) {
-            load_chunk<B>(g + V * (c0 + i * kThreads), vg[i]);
-            load_chunk<B>(y + V * (c0 + i * kThreads), vy[i]);
+          if (c0 + i * kGroup < nv) {
+            load_chunk<B>(g + V * (c0 + i * kGroup), vg[i]);
+            load_chunk<B>(y + V * (c0 + i * kGroup), vy[i]);
           }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
-          if (c0 + i * kThreads < nv) {
+          if (c0 + i * kGroup < nv) {
             float d[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -234,19 +233,24 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a,
             }
             Chunk<B> o;
             f32_chunk<T, B>(o, d);
-            store_chunk<B>(dy + V * (c0 + i * kThreads), o);
+            store_chunk<B>(dy + V * (c0 + i * kGroup), o);
           }
       }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (lane == 0) s_part[j][warp] = dot;
+    if (kGroup == 32) {
+      if (lane == 0) a.dw[f] = dot;
+    } else if (lane == 0) {
+      s_part[j][warp] = dot;
+    }
   }
+  if (kGroup == 32) return;
   __syncthreads();
   for (int j = blockIdx.y + tid * gridDim.y; j < a.topk; j += kThreads * gridDim.y) {
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) sum += s_part[j][i];
+    for (int i = 0; i < kWarps; ++i) sum += s_part[j][i];
     a.dw[static_cast<long long>(t) * a.topk + j] = sum;
   }
 }
@@ -254,27 +258,29 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a,
 template <int B>
 cudaError_t launch_permute(const RowArgs& a, int elem, cudaStream_t st) {
   const int row_bytes = a.H * elem;
-  const int columns = (row_bytes / B + kThreads - 1) / kThreads;
-  // tokens at once: what is resident; up to a fifth of the CTAs zero padding
+  const int warps = (row_bytes / B + 31) / 32, wpt = warps >= 3 ? 4 : warps;
+  const int columns = (warps + wpt - 1) / wpt;
+  // CTAs for tokens: kWaves of what is resident; up to a fifth more for padding
   const int slots = std::max(1, std::min(kWaves * kCtas * sm_count() / columns, 60000));
-  const int tokens = std::min(a.M, slots);
+  const int tokens = std::min((a.M + kWarps / wpt - 1) / (kWarps / wpt), slots);
   const int runs = (a.rows + kPadRows - 1) / kPadRows;
   const int pad_y = std::max(1, std::min(slots / 5, (runs + columns - 1) / columns));
   return launch_kernel(permute_kernel<B>, dim3(columns, tokens + pad_y), dim3(kThreads), 0, st, true, a, row_bytes,
-                       a.ldx * elem, a.ldo * elem, pad_y);
+                       a.ldx * elem, a.ldo * elem, pad_y, wpt / 2);
 }
 
 template <typename T, int B>
 cudaError_t launch_combine(const RowArgs& a, cudaStream_t st) {
-  const int nv = a.H / (B / static_cast<int>(sizeof(T)));
-  // accesses per thread: many where there are at least four CTAs per SM then
+  const int nv = a.H / (B / static_cast<int>(sizeof(T))), ctas = (a.M + kWarps - 1) / kWarps;
+  // accesses per lane: many, where there are at least four CTAs per SM then;
+  // eight rows in flight with few, four with many
   constexpr int kFew = B >= 16 ? 1 : 4, kMany = 2 * kFew;
-  const int many = (nv + kMany * kThreads - 1) / (kMany * kThreads), few = (nv + kFew * kThreads - 1) / (kFew * kThreads);
-  if (static_cast<long long>(a.M) * many >= 4LL * sm_count())
-    return launch_kernel(a.w ? combine_kernel<T, B, kMany, true> : combine_kernel<T, B, kMany, false>,
-                         dim3(a.M, many), dim3(kThreads), 0, st, true, a);
-  return launch_kernel(a.w ? combine_kernel<T, B, kFew, true> : combine_kernel<T, B, kFew, false>, dim3(a.M, few),
-                       dim3(kThreads), 0, st, true, a);
+  const int many = (nv + 32 * kMany - 1) / (32 * kMany), few = (nv + 32 * kFew - 1) / (32 * kFew);
+  if (static_cast<long long>(ctas) * many >= 4LL * sm_count())
+    return launch_kernel(a.w ? combine_kernel<T, B, kMany, 4, true> : combine_kernel<T, B, kMany, 4, false>,
+                         dim3(ctas, many), dim3(kThreads), 0, st, true, a);
+  return launch_kernel(a.w ? combine_kernel<T, B, kFew, 8, true> : combine_kernel<T, B, kFew, 8, false>,
+                       dim3(ctas, few), dim3(kThreads), 0, st, true, a);
 }
 
 template <typename T, int B>
@@ -282,8 +288,15 @@ cudaError_t launch_unpermute_backward(const RowArgs& a, cudaStream_t st) {
   const int pad = std::min((a.rows + kPadRows - 1) / kPadRows, 2 * sm_count());
   int split = 1;
   while (split < a.topk && static_cast<long long>(a.M) * split < 4LL * sm_count()) split *= 2;
-  return launch_kernel(unpermute_backward_kernel<T, B>, dim3(a.M + pad, std::min(split, a.topk)), dim3(kThreads), 0,
-                       st, true, a, pad);
+  split = std::min(split, a.topk);
+  // a warp per token where its lanes pass over the row at most four times and
+  // the tokens fill the SMs (3296 rows of 117 values: 8.0 us with a CTA each)
+  const int nv = a.H / (B / static_cast<int>(sizeof(T)));
+  if (nv <= 128 && a.M >= 16 * sm_count())
+    return launch_kernel(unpermute_backward_kernel<T, B, 32>, dim3((a.M + kWarps - 1) / kWarps + pad, split),
+                         dim3(kThreads), 0, st, true, a, pad);
+  return launch_kernel(unpermute_backward_kernel<T, B, kThreads>, dim3(a.M + pad, split), dim3(kThreads), 0, st, true,
+                       a, pad);
 }
 
 // Access size shared by all row matrices of the call.
