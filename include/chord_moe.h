@@ -86,10 +86,10 @@ typedef struct chord_tuning {
 /* Description of the last failure on the calling thread ("" if none). */
 const char* chord_last_error_string(void);
 /* Test hook for the device timeout path, not needed in normal use: while
- * enabled, every later launch of the register-MMA GEMM in this process
- * withholds its work items from its consumer warps (the producer issues no
- * copy and hands out no item), so the consumers' barrier waits run out after
- * a short limit: the kernel records CHORD_ERR_TIMEOUT in dev_status and
+ * enabled, every later launch of the register-MMA GEMM and of the MXFP4
+ * product in this process withholds its work items from its consumer warps
+ * (no copy is issued and no item handed out), so the consumers' barrier waits
+ * run out after a short limit: the kernel records CHORD_ERR_TIMEOUT in dev_status and
  * returns, with no copy in flight and the work-queue counters left zero.
  * Nothing is computed.  enable = 0 turns it off.  Returns CHORD_OK. */
 int chord_debug_force_timeout(int enable);

@@ -384,6 +384,24 @@ def test_device_errors():
     assert (C[16:] == 7.0).all() and not (C[:3] == 7.0).all()
 
 
+def test_a_wait_that_runs_out():
+    """With the items withheld every role's wait runs out: the status says so, nothing is
+    written, and the next call on the same workspace is exact."""
+    ex = Experts([3, 20], 16, 256, 512, 30)
+    packed, rows, ws = ex.pack(False), ex.rows(), torch.zeros_like(workspace())
+    want = ex.product(False, packed, rows, ws)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    chord.chord_debug_force_timeout(True)
+    try:
+        C = ex.product(False, packed, rows, ws, status)
+        torch.cuda.synchronize()
+    finally:
+        chord.chord_debug_force_timeout(False)
+    assert status.item() == chord.CHORD_ERR_TIMEOUT and (C == 7.0).all()
+    status.zero_()
+    assert torch.equal(ex.product(False, packed, rows, ws, status), want) and status.item() == 0
+
+
 def test_refusals():
     ex = Experts([3, 2], 16, 128, 256, 28)
     packed, rows, ws = ex.pack(False), ex.rows(), workspace()

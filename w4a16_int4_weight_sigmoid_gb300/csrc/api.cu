@@ -26,6 +26,12 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(CHORD_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Test hook (chord_debug_force_timeout): later small-M GEMM and MXFP4 product
+// launches withhold their work items from the warps that wait for them.
+static std::atomic<int> g_force_timeout{0};
+
+bool force_timeout() { return g_force_timeout.load(std::memory_order_relaxed) != 0; }
+
 }  // namespace chord
 
 using chord::aligned16;
@@ -35,9 +41,6 @@ using chord::valid_block_m;
 
 namespace {
 
-// Test hook (chord_debug_force_timeout): later small-M GEMM launches
-// withhold their work items from the consumer warps.
-std::atomic<int> g_force_timeout{0};
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -174,7 +177,7 @@ extern "C" {
 const char* chord_last_error_string(void) { return chord::g_err; }
 
 int chord_debug_force_timeout(int enable) {
-  g_force_timeout.store(enable ? 1 : 0, std::memory_order_relaxed);
+  chord::g_force_timeout.store(enable ? 1 : 0, std::memory_order_relaxed);
   return CHORD_OK;
 }
 
@@ -407,7 +410,7 @@ static int gemm_impl(const chord_bf16* A, int a_gather, const void* packed_w, in
   g.work = ws.work;
   g.split_cnt = ws.split_cnt;
   g.split_partial = ws.split_partial;
-  g.test_timeout = g_force_timeout.load(std::memory_order_relaxed) ? 1 : 0;
+  g.test_timeout = chord::force_timeout() ? 1 : 0;
   g.epilogue = epilogue;
   g.C = epilogue == CHORD_EPI_WEIGHTED_ADD ? nullptr : static_cast<uint16_t*>(C);
   g.Cf = epilogue == CHORD_EPI_WEIGHTED_ADD ? static_cast<float*>(C) : nullptr;

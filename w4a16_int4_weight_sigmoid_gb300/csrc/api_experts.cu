@@ -203,7 +203,8 @@ int chord_mxfp4_moe_gemm(const void* rows, size_t rows_bytes, const void* packed
   if (!aligned16(workspace)) return fail(CHORD_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   return done(chord::mxfp4_gemm_launch(static_cast<const uint8_t*>(rows), static_cast<const uint8_t*>(packed_w), E_local,
                                        N, K, expert_counts, expert_offsets, static_cast<int>(capacity),
-                                       epilogue == CHORD_EPI_SILU_MUL, C, workspace, dev_status, stream_of(stream)),
+                                       epilogue == CHORD_EPI_SILU_MUL, C, workspace, chord::force_timeout(), dev_status,
+                                       stream_of(stream)),
               "MXFP4 product launch");
 }
 

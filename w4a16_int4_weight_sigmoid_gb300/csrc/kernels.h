@@ -116,7 +116,7 @@ cudaError_t mxfp4_prepack_launch(const uint8_t* codes, const uint8_t* scales, in
                                  uint8_t* out, cudaStream_t st);
 size_t mxfp4_gemm_workspace_bytes();
 cudaError_t mxfp4_gemm_launch(const uint8_t* rows, const uint8_t* w, int E, int N, int K, const int32_t* counts,
-                              const int32_t* offsets, int capacity, bool gate_up, uint16_t* C, void* ws, int* status,
-                              cudaStream_t st);
+                              const int32_t* offsets, int capacity, bool gate_up, uint16_t* C, void* ws,
+                              bool test_timeout, int* status, cudaStream_t st);
 
 }  // namespace chord

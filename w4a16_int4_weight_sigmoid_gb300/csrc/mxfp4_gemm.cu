@@ -7,21 +7,20 @@
 //   * an item is two tiles of 128 weight rows (two MMAs of M = 128 on the same
 //     rows) times up to kMaxTok of an expert's rows (N, a multiple of 16), so
 //     one decoded token costs 16 columns, not 128 rows; one kernel serves
-//     decoding and prefill.  Every SM draws its operands from L2 at about
-//     60 GB/s, which bounds all sizes above a few dozen rows per expert: a
-//     second weight tile on the same rows brings 66 KB for what took 100;
+//     decoding and prefill.  The second weight tile halves the traffic of the
+//     rows (16384 rows of 8 experts: 199 us against 218 with one tile);
 //   * items are dealt whole and in turn, so that CTAs at work at one time
 //     share weights and rows in L2 (a contiguous run of items per CTA spread
 //     the live weights over more than L2: many rows per expert 346 us).  The
 //     items that do not divide evenly among the CTAs (or all, when there are
 //     fewer) come first and are divided further.  With up to kSplitTok rows
-//     per tile, along K: their K units of 256 are cut into ranges of equal
-//     length to within a unit, one per CTA, so one token's few items spread
-//     over all SMs; an item that a range boundary cuts is summed by the CTA
-//     that finishes last, from FP32 partials in workspace, in K order, so
-//     results do not depend on timing.  With more rows adding partials costs
-//     more than the work (8 prefill items in 19 parts each: 110 us), and they
-//     are divided into single weight tiles and runs of rows instead;
+//     per tile, along K: each into equal parts for several CTAs, or all their
+//     K units of 256 into one range per CTA, so one token's few items spread
+//     over all SMs; an item in parts is summed by the CTA that finishes last,
+//     from FP32 partials in workspace, in K order, so results do not depend
+//     on timing.  With more rows adding partials costs more than the work (8
+//     prefill items in 19 parts each: 110 us), and they are divided into
+//     single weight tiles and runs of rows instead;
 //   * per unit one bulk copy brings the pair's weight rows with their scales
 //     (34 KB, contiguous, already swizzled), one or two the rows;
 //   * the rows' scales lie in row order in memory, and a row tile may start at
@@ -41,7 +40,12 @@
 //   * stages and accumulators are laid out for the launch's largest row tile,
 //     which every CTA finds from the counts: decoding has five stages and four
 //     accumulators, a full tile three stages and one accumulator.
-// TMEM: accumulators from column 0, scales from column 480.
+// Measured (kernel alone): 64 tokens on 48 of 384 experts, N 4096, K 7168: 85
+// us, 6.1 TB/s of DRAM, its bound; 8192 tokens: 136 us, DRAM at 5.8 TB/s and
+// exposed epilogues; 16384 rows of 8 experts: 177 us, 5.4 PFLOP/s, bound by
+// the turnaround of three stages (tensor pipe 54 % busy); one token, N 512:
+// 9.2 us, latency.
+// TMEM: accumulators from column 0, scales from column kSfCol.
 // Every mbarrier wait is bounded.  A warp whose wait runs out records
 // CHORD_ERR_TIMEOUT and stops, so the others' waits run out in turn; the CTA
 // drains its own copies and MMAs, frees TMEM and exits.
@@ -94,11 +98,12 @@ struct MxArgs {
   const uint8_t* rows;
   const int32_t* counts;
   const int32_t* offsets;
-  int* split_cnt;        // [kMxMaxCtas], zero between launches
+  int* split_cnt;        // [kMxMaxCtas] parts arrived, zero between launches
   float* partial;        // [2 * kMxMaxCtas][tile of the pair][tokens / 4][128 weight rows][4]
   uint16_t* C;
   int* status;
   int E, N, K, ldc, capacity, n_tiles, max_tok;
+  int test_timeout;      // test of the timeout path: no item is handed out, waits for one are short
   size_t rows_padded;
 };
 
@@ -227,11 +232,12 @@ struct Walk {
 struct ItemRing {
   uint64_t *full, *empty;
   const Seg* slots;
+  uint32_t polls;
   int slot, ph;
   // The next segment: false at the end of the work or on a timeout.  All
   // lanes of the calling warp take it; lane 0 releases the slot.
   __device__ __forceinline__ bool next(Seg& s, int* status) {
-    if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], ph, status))) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[slot], ph, status, polls))) return false;
     const int4* src = reinterpret_cast<const int4*>(&slots[slot]);
     const int4 lo = src[0], hi = src[1];
     s.item = lo.x, s.e = lo.y, s.row0 = lo.z, s.rows = lo.w;
@@ -527,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   }
   const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget / stage);
   const int n_acc = min(kMaxAcc, kSfCol / (kPair * tok));
-  ItemRing items{item_full, item_empty, item_slots, 0, 0};
+  ItemRing items{item_full, item_empty, item_slots, a.test_timeout ? kTestWaitPolls : kWaitPolls, 0, 0};
   Seg w;
 
   if (warp == 0) {
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     // ----------------------------------------------------------------- items
     Walk walk(plan);
     int slot = 0, ph = 0;
-    for (bool first = true, more = true; more;) {
+    for (bool first = true, more = !a.test_timeout; more;) {
       if (!first && !__all_sync(0xffffffffu, mbar_wait_backoff(&item_empty[slot], ph ^ 1, a.status))) break;
       more = walk.more;
       if (lane == 0) {
@@ -766,9 +772,10 @@ size_t mxfp4_gemm_workspace_bytes() {
 }
 
 cudaError_t mxfp4_gemm_launch(const uint8_t* rows, const uint8_t* w, int E, int N, int K, const int32_t* counts,
-                              const int32_t* offsets, int capacity, bool gate_up, uint16_t* C, void* ws, int* status,
-                              cudaStream_t st) {
+                              const int32_t* offsets, int capacity, bool gate_up, uint16_t* C, void* ws,
+                              bool test_timeout, int* status, cudaStream_t st) {
   MxArgs a{};
+  a.test_timeout = test_timeout ? 1 : 0;
   a.w = w, a.rows = rows, a.counts = counts, a.offsets = offsets;
   a.split_cnt = static_cast<int*>(ws);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kMxMaxCtas * sizeof(int));

@@ -9,6 +9,10 @@
 // The maximum is taken on |x| with NaNs above all (16-bit types two to a
 // register), and the scale is a power of two, so x / scale and its rounding
 // to E2M1 are exact operations.
+// Bound by memory.  Measured, 8192 x 7168 BF16: quantise 22.9 us, dequantise
+// 24.0 us (148 MB each: 6.5 and 6.2 TB/s of 6.7 that a copy reaches); rows into
+// expert order on 48 of 384 experts 20.6 us (108 MB), on all of 8 experts, two
+// copies of each token, 29.3 us (179 MB).
 #include <algorithm>
 
 #include "common.cuh"
