@@ -161,6 +161,25 @@ def test_unaligned_outputs_and_broadcast_inputs(name):
     close(out, t.sum(1), np.abs(t).sum(1), o.k, u, "unpermute")
 
 
+@pytest.mark.parametrize("H", [1, 9, 1024, 1030, 4113])
+@pytest.mark.parametrize("name", ["bf16", "fp32"])
+def test_permute_at_every_alignment(name, H):
+    """Rows that begin at each element of 16 bytes, source and destination apart, land
+    whole; the elements between them stay."""
+    dtype, _ = TYPES[name]
+    o = Order(19, 8, 0, 6, 2, 16, seed=H)
+    for off in range(16 // dtype.itemsize):
+        x = rows(o.M, H, dtype, off, H + 13, off)
+        buf = torch.full((o.cap, H + 11), 7.0, dtype=dtype, device="cuda")
+        out = buf.view(-1)[off // 2:off // 2 + (o.cap - 1) * (H + 11) + H].as_strided((o.cap, H), (H + 11, 1))
+        chord.chord_moe_permute(x, o.pos, o.sorted, o.ntpp, o.k, out)
+        ref = torch.full_like(buf, 7.0)
+        view = ref.view(-1)[off // 2:].as_strided((o.cap, H), (H + 11, 1))
+        view[torch.from_numpy(o.pad).cuda()] = 0.0
+        view[torch.from_numpy(o.fill).cuda()] = x[torch.from_numpy(o.f // o.k).long().cuda()]
+        assert torch.equal(buf, ref)
+
+
 def test_gradients_against_differences():
     """L = <g, unpermute(y, w)> and <g, permute(x)>: central differences along random
     directions.  Both maps are linear in the direction, so the difference is exact up

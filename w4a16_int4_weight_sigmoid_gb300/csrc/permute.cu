@@ -11,15 +11,16 @@
 // whatever the number of its experts.  Sums are FP32 in increasing j (the
 // weight gradient: FP32 in a tree fixed by the call's sizes), each result
 // rounded once; no atomics, so a call repeats bit for bit.
-// Measured: permute of 8192 tokens x 7168 BF16 to 48 of 384 experts 43.7 us
+// Measured: permute of 8192 tokens x 7168 BF16 to 48 of 384 experts 43.3 us
 // (239 MB with the zeroed padding: 5.5 TB/s), its weighted sum's gradient
-// 53.5 us (312 MB: 5.8 TB/s), of 6.7 TB/s that a copy reaches; weighted sum of
-// 128 FP32 tokens 5.2 us; 64 tokens permuted 3.5 us, bound by the launch and
-// two dependent loads.
+// 54.1 us (312 MB: 5.8 TB/s), of 6.7 TB/s that a copy reaches; 20 tokens at
+// block 128, 99 % padding, 37 us (6.4 TB/s); weighted sum of 128 FP32 tokens
+// 5.2 us; 64 tokens permuted 3.5 us, bound by the launch and two dependent
+// loads.
 //
 // Rows are moved in accesses of B bytes: 32 where every base, row stride and
 // row length allows it, otherwise the largest power of two they share, down
-// to one element.  All kernels are programmatic launches that touch no memory
+// to one element (permute: 32 or 16, or shifted).  All kernels are programmatic launches that touch no memory
 // before the work ahead of them in the stream has completed.
 #include <algorithm>
 #include <type_traits>
@@ -58,20 +59,34 @@ constexpr int kCtas = 12, kWaves = 4;
 // threads on one row (a warp on a row of its own took 25 us at 64 tokens).
 constexpr int kPadRows = 8;
 
-template <int B>
+// Zeros at any element alignment, by all threads: 16-byte stores between a
+// first and a last part of up to 14 bytes (2-byte stores throughout took 20 us
+// for 5000 rows of 3323 BF16 values).
+__device__ __forceinline__ void zero_bytes(uint8_t* dst, int bytes) {
+  const int head = min(static_cast<int>(-reinterpret_cast<uintptr_t>(dst) & 15u), bytes);
+  const int body = (bytes - head) / 16, tail = bytes - head - 16 * body;
+  const int i = threadIdx.x;
+  if (i < head / 2) reinterpret_cast<uint16_t*>(dst)[i] = 0;
+  for (int c = i; c < body; c += kThreads) reinterpret_cast<uint4*>(dst + head)[c] = make_uint4(0, 0, 0, 0);
+  if (i < tail / 2) reinterpret_cast<uint16_t*>(dst + head + 16 * body)[i] = 0;
+}
+
 __device__ __forceinline__ void zero_padding(const RowArgs& a, int row_bytes, long long out_stride, int b, int nb) {
   const int lane = threadIdx.x & 31, sentinel = a.M * a.topk;
   const int total = ld_ca(a.ntpp);
-  const Chunk<B> z{};
+  // neighbouring rows without a gap are one stretch (their lengths' limit
+  // keeps kPadRows of them within 32 bits)
+  const bool dense = out_stride == row_bytes;
   for (int r0 = b * kPadRows; r0 < a.rows; r0 += nb * kPadRows) {
     // the entry is read before the total is known: entries past the total
     // exist, and are dropped
     const int r = r0 + lane, f = lane < kPadRows && r < a.rows ? ld_ca(a.sorted + r) : 0;
     if (r0 >= total) break;
     uint32_t pad = __ballot_sync(0xffffffffu, lane < kPadRows && r < min(total, a.rows) && f >= sentinel);
-    for (; pad; pad &= pad - 1) {
-      uint8_t* dst = static_cast<uint8_t*>(a.out) + (r0 + __ffs(pad) - 1) * out_stride;
-      for (int c = threadIdx.x * B; c < row_bytes; c += kThreads * B) store_chunk<B>(dst + c, z);
+    while (pad) {
+      const int first = __ffs(pad) - 1, n = dense ? __ffs(~(pad >> first)) - 1 : 1;
+      zero_bytes(static_cast<uint8_t*>(a.out) + (r0 + first) * out_stride, n * row_bytes);
+      pad &= ~(((1u << n) - 1u) << first);
     }
   }
 }
@@ -89,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) permute_kernel(RowArgs a, int
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, token_ctas = gridDim.y - pad_y;
   if (static_cast<int>(blockIdx.y) >= token_ctas) {
-    zero_padding<B>(a, row_bytes, out_stride, (blockIdx.y - token_ctas) * gridDim.x + blockIdx.x,
+    zero_padding(a, row_bytes, out_stride, (blockIdx.y - token_ctas) * gridDim.x + blockIdx.x,
                     pad_y * gridDim.x);
     return;
   }
@@ -123,6 +138,91 @@ __global__ void __launch_bounds__(kThreads, kCtas) permute_kernel(RowArgs a, int
     store(p1, left1, v1);
     p0 = p2;
     p1 = p3;
+  }
+}
+
+// The same for rows that are not all aligned to 16 bytes.  A warp has up to
+// kShiftBytes of a token's row: it stages them in shared memory at the offset
+// that the source has from a 16-byte boundary, and writes each destination
+// with 16-byte stores at that row's own offset, each put together from two
+// staged chunks.  What lies before the first and after the last boundary goes
+// element by element, so that no access leaves the row.  4000 rows of 3323
+// BF16 values to two experts each took 35.6 us in accesses of 2 bytes, of 3324
+// in accesses of 8 bytes 18.6 us; here 17.7 and 17.5, and rows of 3328, which
+// are aligned, 14.2 above.
+constexpr int kShiftBytes = 2048, kShiftCtas = 12;
+__global__ void __launch_bounds__(kThreads, kShiftCtas) permute_shift_kernel(RowArgs a, int row_bytes,
+                                                                             long long x_stride, long long out_stride,
+                                                                             int pad_y, int wpt_log2) {
+  // one chunk of room for the offset and one that is read past the end
+  __shared__ __align__(16) uint8_t s_rows[kWarps][kShiftBytes + 32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, token_ctas = gridDim.y - pad_y;
+  if (static_cast<int>(blockIdx.y) >= token_ctas) {
+    zero_padding(a, row_bytes, out_stride, (blockIdx.y - token_ctas) * gridDim.x + blockIdx.x, pad_y * gridDim.x);
+    return;
+  }
+  uint8_t* stage = s_rows[warp];
+  const int tokens = kWarps >> wpt_log2, step = token_ctas * tokens;
+  const int c = ((blockIdx.x << wpt_log2) + (warp & ((1 << wpt_log2) - 1))) * kShiftBytes;
+  const int bytes = min(kShiftBytes, row_bytes - c);
+  if (bytes <= 0) return;
+  for (int t = blockIdx.y * tokens + (warp >> wpt_log2); t < a.M; t += step) {
+    int p = lane < a.topk ? ld_ca(a.pos + static_cast<long long>(t) * a.topk + lane) : -1;
+    if (p >= a.rows) p = -1;
+    const uint8_t* src = static_cast<const uint8_t*>(a.x) + t * x_stride + c;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15u);
+    {
+      const int head = min((16 - off) & 15, bytes), body = (bytes - head) / 16, tail = bytes - head - 16 * body;
+      Chunk<16> v[kShiftBytes / 512];
+      Chunk<2> h, e;
+#pragma unroll
+      for (int i = 0; i < kShiftBytes / 512; ++i)
+        if (lane + 32 * i < body) load_chunk<16>(src + head + 16 * (lane + 32 * i), v[i]);
+      if (lane < head / 2) load_chunk<2>(src + 2 * lane, h);
+      if (lane < tail / 2) load_chunk<2>(src + head + 16 * body + 2 * lane, e);
+      __syncwarp();   // the last token's chunks are read
+#pragma unroll
+      for (int i = 0; i < kShiftBytes / 512; ++i)
+        if (lane + 32 * i < body) store_chunk<16>(stage + off + head + 16 * (lane + 32 * i), v[i]);
+      if (lane < head / 2) store_chunk<2>(stage + off + 2 * lane, h);
+      if (lane < tail / 2) store_chunk<2>(stage + off + head + 16 * body + 2 * lane, e);
+      __syncwarp();
+    }
+    for (uint32_t left = __ballot_sync(0xffffffffu, p >= 0); left; left &= left - 1) {
+      const long long row = __shfl_sync(0xffffffffu, p, __ffs(left) - 1);
+      uint8_t* dst = static_cast<uint8_t*>(a.out) + row * out_stride + c;
+      const int head = min(static_cast<int>(-reinterpret_cast<uintptr_t>(dst) & 15u), bytes);
+      const int body = (bytes - head) / 16, tail = bytes - head - 16 * body;
+      // destination chunk i starts `words` words and `bits` bits into staged
+      // chunk i + first
+      const int first = (off + head) / 16, words = (off + head) / 4 & 3, bits = (off + head & 3) * 8;
+#pragma unroll
+      for (int i = 0; i < kShiftBytes / 512; ++i) {
+        const int k = lane + 32 * i;
+        if (k >= body) break;
+        const uint4 lo = *reinterpret_cast<const uint4*>(stage + 16 * (first + k));
+        const uint4 hi = *reinterpret_cast<const uint4*>(stage + 16 * (first + k + 1));
+        uint32_t u[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z}, last = hi.w;
+        if (words & 2) {
+          u[0] = u[2], u[1] = u[3], u[2] = u[4], u[3] = u[5], u[4] = u[6], u[5] = last;
+        }
+        if (words & 1) {
+          u[0] = u[1], u[1] = u[2], u[2] = u[3], u[3] = u[4], u[4] = u[5];
+        }
+        Chunk<16> o;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o.w[q] = __funnelshift_r(u[q], u[q + 1], bits);
+        store_chunk<16>(dst + head + 16 * k, o);
+      }
+      const uint8_t* s = stage + off;
+      if (lane < head / 2) reinterpret_cast<uint16_t*>(dst)[lane] = reinterpret_cast<const uint16_t*>(s)[lane];
+      if (lane < tail / 2) {
+        const int q = head + 16 * body + 2 * lane;
+        *reinterpret_cast<uint16_t*>(dst + q) = *reinterpret_cast<const uint16_t*>(s + q);
+      }
+    }
   }
 }
 
@@ -203,75 +303,90 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a,
   grid_dep_launch();
   if (static_cast<int>(blockIdx.x) < pad_ctas) {
     if (blockIdx.y == 0)
-      zero_padding<B>(a, a.H * static_cast<int>(sizeof(T)), a.ldo * static_cast<long long>(sizeof(T)), blockIdx.x,
+      zero_padding(a, a.H * static_cast<int>(sizeof(T)), a.ldo * static_cast<long long>(sizeof(T)), blockIdx.x,
                       pad_ctas);
     return;
   }
   const int t = (blockIdx.x - pad_ctas) * (kThreads / kGroup) + (kGroup == 32 ? warp : 0), nv = a.H / V;
   if (kGroup == 32 && t >= a.M) return;
   const T* g = static_cast<const T*>(a.x) + t * a.ldx;
-  for (int j = blockIdx.y; j < a.topk; j += gridDim.y) {
-    const long long f = static_cast<long long>(t) * a.topk + j;
-    const int p = ld_ca(a.pos + f);
-    const float wj = ld_ca(a.w + f);
+  // lane j holds assignment j: the rows of all are known after one load
+  const long long f = static_cast<long long>(t) * a.topk + lane;
+  const bool mine = lane < a.topk && lane % gridDim.y == blockIdx.y;
+  const int p = mine ? ld_ca(a.pos + f) : -1;
+  const float w = mine ? ld_ca(a.w + f) : 0.f;
+  float dw = 0.f;   // lane j's weight gradient (a warp per token), 0 where not local
+  const uint32_t local = __ballot_sync(0xffffffffu, p >= 0 && p < a.rows);
+  for (uint32_t left = local; left; left &= left - 1) {
+    const int j = __ffs(left) - 1;
+    const long long row = __shfl_sync(0xffffffffu, p, j);
+    const float wj = __shfl_sync(0xffffffffu, w, j);
+    const T* y = static_cast<const T*>(a.y) + row * a.ldy;
+    T* dy = static_cast<T*>(a.out) + row * a.ldo;
     float dot = 0.f;
-    if (p >= 0 && p < a.rows) {
-      const T* y = static_cast<const T*>(a.y) + p * a.ldy;
-      T* dy = static_cast<T*>(a.out) + p * a.ldo;
-      for (int c0 = tid; c0 < nv; c0 += kUnroll * kGroup) {
-        Chunk<B> vg[kUnroll], vy[kUnroll];
+    for (int c0 = tid; c0 < nv; c0 += kUnroll * kGroup) {
+      Chunk<B> vg[kUnroll], vy[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
-          if (c0 + i * kGroup < nv) {
-            load_chunk<B>(g + V * (c0 + i * kGroup), vg[i]);
-            load_chunk<B>(y + V * (c0 + i * kGroup), vy[i]);
+      for (int i = 0; i < kUnroll; ++i)
+        if (c0 + i * kGroup < nv) {
+          load_chunk<B>(g + V * (c0 + i * kGroup), vg[i]);
+          load_chunk<B>(y + V * (c0 + i * kGroup), vy[i]);
+        }
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i)
+        if (c0 + i * kGroup < nv) {
+          float d[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float gv = chunk_f32<T, B>(vg[i], e);
+            dot = fmaf(gv, chunk_f32<T, B>(vy[i], e), dot);
+            d[e] = wj * gv;
           }
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
-          if (c0 + i * kGroup < nv) {
-            float d[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const float gv = chunk_f32<T, B>(vg[i], e);
-              dot = fmaf(gv, chunk_f32<T, B>(vy[i], e), dot);
-              d[e] = wj * gv;
-            }
-            Chunk<B> o;
-            f32_chunk<T, B>(o, d);
-            store_chunk<B>(dy + V * (c0 + i * kGroup), o);
-          }
-      }
+          Chunk<B> o;
+          f32_chunk<T, B>(o, d);
+          store_chunk<B>(dy + V * (c0 + i * kGroup), o);
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (kGroup == 32) {
-      if (lane == 0) a.dw[f] = dot;
+      if (lane == j) dw = dot;
     } else if (lane == 0) {
       s_part[j][warp] = dot;
     }
   }
-  if (kGroup == 32) return;
-  __syncthreads();
-  for (int j = blockIdx.y + tid * gridDim.y; j < a.topk; j += kThreads * gridDim.y) {
-    float sum = 0.f;
+  if (kGroup != 32) {
+    __syncthreads();
+    if (warp) return;
+    if (local >> lane & 1) {
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) sum += s_part[j][i];
-    a.dw[static_cast<long long>(t) * a.topk + j] = sum;
+      for (int i = 0; i < kWarps; ++i) dw += s_part[lane][i];
+    }
   }
+  if (mine) a.dw[f] = dw;
 }
 
-template <int B>
-cudaError_t launch_permute(const RowArgs& a, int elem, cudaStream_t st) {
+// CTAs that cover `rows` rows of the order for their padding: one for each 4
+// KB of them, at most (most of an order's capacity is past its padded total).
+int padding_ctas(int rows, long long row_bytes) {
+  const long long runs = (rows + kPadRows - 1) / kPadRows;
+  return static_cast<int>(std::min(runs, rows * row_bytes / 4096 + 1));
+}
+
+// warp_bytes: what one warp has of a row at a time.
+template <typename Kernel>
+cudaError_t launch_permute(Kernel kernel, int warp_bytes, int ctas, const RowArgs& a, int elem, cudaStream_t st) {
   const int row_bytes = a.H * elem;
-  const int warps = (row_bytes / B + 31) / 32, wpt = warps >= 3 ? 4 : warps;
+  const int warps = (row_bytes + warp_bytes - 1) / warp_bytes, wpt = warps >= 3 ? 4 : warps;
   const int columns = (warps + wpt - 1) / wpt;
-  // CTAs for tokens: kWaves of what is resident; up to a fifth more for padding
-  const int slots = std::max(1, std::min(kWaves * kCtas * sm_count() / columns, 60000));
+  // CTAs for tokens: kWaves of what is resident; for padding a fifth more, or
+  // what few tokens leave over
+  const int slots = std::max(1, std::min(kWaves * ctas * sm_count() / columns, 60000));
   const int tokens = std::min((a.M + kWarps / wpt - 1) / (kWarps / wpt), slots);
-  const int runs = (a.rows + kPadRows - 1) / kPadRows;
-  const int pad_y = std::max(1, std::min(slots / 5, (runs + columns - 1) / columns));
-  return launch_kernel(permute_kernel<B>, dim3(columns, tokens + pad_y), dim3(kThreads), 0, st, true, a, row_bytes,
-                       a.ldx * elem, a.ldo * elem, pad_y, wpt / 2);
+  const int pads = padding_ctas(a.rows, row_bytes);
+  const int pad_y = std::max(1, std::min(std::max(slots / 5, slots - tokens), (pads + columns - 1) / columns));
+  return launch_kernel(kernel, dim3(columns, tokens + pad_y), dim3(kThreads), 0, st, true, a, row_bytes, a.ldx * elem,
+                       a.ldo * elem, pad_y, wpt / 2);
 }
 
 template <typename T, int B>
@@ -290,7 +405,7 @@ cudaError_t launch_combine(const RowArgs& a, cudaStream_t st) {
 
 template <typename T, int B>
 cudaError_t launch_unpermute_backward(const RowArgs& a, cudaStream_t st) {
-  const int pad = std::min((a.rows + kPadRows - 1) / kPadRows, 2 * sm_count());
+  const int pad = std::min(padding_ctas(a.rows, static_cast<long long>(a.H) * sizeof(T)), 8 * sm_count());
   int split = 1;
   while (split < a.topk && static_cast<long long>(a.M) * split < 4LL * sm_count()) split *= 2;
   split = std::min(split, a.topk);
@@ -340,13 +455,10 @@ cudaError_t moe_permute_launch(const void* x, int dtype, long long ldx, const in
   a.x = x, a.ldx = ldx, a.pos = pos, a.sorted = sorted, a.ntpp = ntpp, a.out = out, a.ldo = ldo;
   a.M = M, a.topk = topk, a.H = H, a.rows = rows;
   const int es = static_cast<int>(dtype_bytes(dtype));
-  switch (access_bytes(a, es)) {
-    case 32: return launch_permute<32>(a, es, st);
-    case 16: return launch_permute<16>(a, es, st);
-    case 8: return launch_permute<8>(a, es, st);
-    case 4: return launch_permute<4>(a, es, st);
-    default: return launch_permute<2>(a, es, st);
-  }
+  const int bytes = access_bytes(a, es);
+  if (bytes == 32) return launch_permute(permute_kernel<32>, 32 * 32, kCtas, a, es, st);
+  if (bytes == 16) return launch_permute(permute_kernel<16>, 32 * 16, kCtas, a, es, st);
+  return launch_permute(permute_shift_kernel, kShiftBytes, kShiftCtas, a, es, st);
 }
 
 cudaError_t moe_combine_launch(const void* y, int dtype, long long ldy, const float* w, const int32_t* pos, int M,
