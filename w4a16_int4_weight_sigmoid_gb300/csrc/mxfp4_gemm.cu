@@ -11,16 +11,15 @@
 //     rows (16384 rows of 8 experts: 199 us against 218 with one tile);
 //   * items are dealt whole and in turn, so that CTAs at work at one time
 //     share weights and rows in L2 (a contiguous run of items per CTA spread
-//     the live weights over more than L2: many rows per expert 346 us).  The
-//     items that do not divide evenly among the CTAs (or all, when there are
-//     fewer) come first and are divided further.  With up to kSplitTok rows
-//     per tile, along K: each into equal parts for several CTAs, or all their
-//     K units of 256 into one range per CTA, so one token's few items spread
-//     over all SMs; an item in parts is summed by the CTA that finishes last,
-//     from FP32 partials in workspace, in K order, so results do not depend
-//     on timing.  With more rows adding partials costs more than the work (8
-//     prefill items in 19 parts each: 110 us), and they are divided into
-//     single weight tiles and runs of rows instead;
+//     the live weights over more than L2: many rows per expert 346 us).  Where
+//     what does not divide evenly among the CTAs leaves half of them idle or
+//     more, those items come first and are divided.  With up to kSplitTok rows
+//     per tile, along K into equal parts (one token's few items spread over
+//     all SMs), which the CTA that finishes last sums from FP32 partials in
+//     workspace, in K order, so results do not depend on timing.  With more
+//     rows adding partials costs more than the work (8 prefill items in 19
+//     parts each: 110 us), and they are divided into single weight tiles and
+//     runs of rows instead;
 //   * per unit one bulk copy brings the pair's weight rows with their scales
 //     (34 KB, contiguous, already swizzled), one or two the rows;
 //   * the rows' scales lie in row order in memory, and a row tile may start at
@@ -42,9 +41,9 @@
 //     accumulators, a full tile three stages and one accumulator.
 // Measured (kernel alone): 64 tokens on 48 of 384 experts, N 4096, K 7168: 85
 // us, 6.1 TB/s of DRAM, its bound; 8192 tokens: 136 us, DRAM at 5.8 TB/s and
-// exposed epilogues; 16384 rows of 8 experts: 177 us, 5.4 PFLOP/s, bound by
-// the turnaround of three stages (tensor pipe 54 % busy); one token, N 512:
-// 9.2 us, latency.
+// exposed epilogues; 16384 rows of 8 experts: 177 us, 5.4 PFLOP/s: 54 bytes a
+// cycle into each SM, of about 64 that its port takes (tensor pipe 54 %
+// busy); one token, N 512: 8.7 us, latency.
 // TMEM: accumulators from column 0, scales from column kSfCol.
 // Every mbarrier wait is bounded.  A warp whose wait runs out records
 // CHORD_ERR_TIMEOUT and stops, so the others' waits run out in turn; the CTA
@@ -83,6 +82,7 @@ constexpr int kSmemBytes = kOutOff + kEpiWarps * kOutBytes + 1024;
 constexpr int kMmaWarp0 = 1, kSfWarp = kMmaWarp0 + kPair;
 constexpr int kSfCol = kPair * kMaxTok, kSfCols = 32;   // per tile: SFA at +0 and +8 (alternate units), SFB at +16
 constexpr int kTmemCols = 512;
+constexpr int kSplitUnits = 6, kSplitUnitsHidden = 2;
 constexpr int kSplitTok = 48;          // largest row tile whose items are cut along K
 constexpr int kSlotFloats = kPair * kSplitTok * 128;   // one CTA's part of a cut item
 static_assert(kSplitTok % 16 == 0, "whole runs of rows");
@@ -99,7 +99,7 @@ struct MxArgs {
   const int32_t* counts;
   const int32_t* offsets;
   int* split_cnt;        // [kMxMaxCtas] parts arrived, zero between launches
-  float* partial;        // [2 * kMxMaxCtas][tile of the pair][tokens / 4][128 weight rows][4]
+  float* partial;        // [kMxMaxCtas][tile of the pair][tokens / 4][128 weight rows][4]
   uint16_t* C;
   int* status;
   int E, N, K, ldc, capacity, n_tiles, max_tok;
@@ -135,16 +135,15 @@ __device__ __forceinline__ int tile_rows(int cnt, int n_rt) {
   return ((n_rt > 1 ? (cnt + n_rt - 1) / n_rt : cnt) + 15) & ~15;
 }
 
-// A role's walk over the CTA's segments (an item or a part of one, and a run
-// of its K units): its share of the divided items [0, cut), then its whole
-// items.  Items: experts in order; per expert, weight tile pairs; per pair,
-// row tiles.
+// A CTA's segments: its part of the divided items [0, cut), if it has one,
+// then its whole items.  Items: experts in order; per expert, weight tile
+// pairs; per pair, row tiles.
 struct Plan {
   const int* prefix;                 // shared: first item of each expert
   const int32_t *cnts, *offs;        // rows and first row of each expert (checked where it has items)
   int E, n_tiles, units, max_tok, items, cut;
-  int begin, end;                    // along K: this CTA's units of the divided items
-  int chunks;                        // by rows: runs per single tile (0: along K)
+  int parts;                         // of a divided item: CTA i has part i % parts of item i / parts
+  int chunks;                        // runs of rows per single tile, 0: divided along K
 };
 
 // A segment as the roles read it (two 16-byte words).
@@ -156,50 +155,39 @@ struct alignas(16) Seg {
 // Run by the item warp (the search for the expert is one ballot of 32).
 struct Walk {
   const Plan& p;
-  int pos;                           // next unit, or next (item, tile, run of rows), of the divided items
   int item, e;
   int row0, rows, tile, tiles, u0, u1;
   bool more;
 
-  __device__ explicit Walk(const Plan& plan)
-      : p(plan), pos(plan.chunks ? static_cast<int>(blockIdx.x) : plan.begin), item(-1), e(0) {
+  __device__ explicit Walk(const Plan& plan) : p(plan), item(-1), e(0), u0(0), u1(plan.units) {
+    const int cta = blockIdx.x;
+    if (cta < p.cut * p.parts) {
+      item = cta / p.parts;
+      const int part = cta - item * p.parts;
+      more = true;
+      locate();
+      if (!p.chunks) {
+        u0 = part * p.units / p.parts;
+        u1 = (part + 1) * p.units / p.parts;
+        return;
+      }
+      const int t = part / p.chunks, c = part - t * p.chunks;   // one tile, one run of rows
+      const int run = ((rows + p.chunks - 1) / p.chunks + 15) & ~15;
+      tile += t;
+      tiles -= t;
+      if (tiles > 1) tiles = 1;
+      row0 += c * run;
+      rows = min(run, rows - c * run);
+      if (rows > 0 && tiles > 0) return;
+    }
     advance();
   }
   __device__ void advance() {
-    if (item >= p.cut) {             // whole items, the common case
-      item += gridDim.x;
-      more = item < p.items;
-      if (more) locate();
-      return;
-    }
-    do {
-      int part = -1;
-      u0 = 0;
-      u1 = p.units;
-      if (p.chunks && pos < kPair * p.chunks * p.cut) {
-        item = pos / (kPair * p.chunks);
-        part = pos - item * (kPair * p.chunks);
-        pos += gridDim.x;
-      } else if (!p.chunks && pos < p.end) {
-        item = pos / p.units;
-        u0 = pos - item * p.units;
-        u1 = min(p.units, u0 + p.end - pos);
-        pos += u1 - u0;
-      } else {
-        item = p.cut + static_cast<int>(blockIdx.x);
-      }
-      more = item < p.items;
-      if (!more) return;
-      locate();
-      if (part >= 0) {               // one tile, one run of rows
-        const int t = part / p.chunks, c = part - t * p.chunks;
-        const int run = ((rows + p.chunks - 1) / p.chunks + 15) & ~15;
-        tile += t;
-        tiles = min(1, tiles - t);
-        row0 += c * run;
-        rows = min(run, rows - c * run);
-      }
-    } while (rows <= 0 || tiles <= 0);
+    u0 = 0;
+    u1 = p.units;
+    item = item < p.cut ? p.cut + static_cast<int>(blockIdx.x) : item + static_cast<int>(gridDim.x);
+    more = item < p.items;
+    if (more) locate();
   }
   // The item's expert: the largest e with prefix[e] <= item (items only grow).
   __device__ void locate() {
@@ -365,7 +353,7 @@ __device__ __forceinline__ void add_parts(const float* partial, int first, int l
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
           const int p = min(p0 + i, last);
-          const float* src = partial + static_cast<size_t>(2 * p + (p == first)) * kSlotFloats + c0 * 128;
+          const float* src = partial + static_cast<size_t>(p) * kSlotFloats + c0 * 128;
 #pragma unroll
           for (int c = 0; c < kQuads; ++c) x[i][c] = ld_cg_f4(src + (c0 + 4 * c < rows ? 512 * c : 0));
         }
@@ -500,37 +488,28 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   plan.E = a.E, plan.n_tiles = a.n_tiles, plan.units = units, plan.max_tok = a.max_tok;
   plan.items = hdr_ok ? prefix[a.E] : 0;
   plan.cut = plan.items % ctas;
-  // Divided by rows: about one (tile, run of rows) for each CTA.  (With a
-  // single unit nothing is cut along K and there are no partials.)
-  plan.chunks = tok > kSplitTok && units > 1 && plan.cut > 0 ? min(max(small_div(ctas, kPair * plan.cut), 1), tok / 16) : 0;
-  // Divided along K: where two or more CTAs come to an item, each item into as
-  // many equal parts, so that a CTA has one segment to hand over; otherwise
-  // all items' units into one range per CTA.  A part of u units costs u units'
-  // time and its item units / u parts to add; a part takes tok / 80 of a
-  // unit's time (measured 8 ns a token against 0.6 us), so u is at least the
-  // square root of units * tok / 80.  No part is empty, and an item's parts
-  // are in consecutive CTAs.
-  const int total = plan.chunks ? 0 : plan.cut * units;   // the host keeps this far below 2^31
-  const int least = max(1, static_cast<int>(approx_sqrt(units * tok * (1 / 80.f))));
-  int parts = 0, ranges = 0;
-  plan.begin = plan.end = 0;
-  if (total > 0) {
-    parts = min(small_div(ctas, plan.cut), small_div(units, least));
-    if (parts >= 2) {
-      const int item = small_div(cta, parts), part = cta - item * parts;
-      if (item < plan.cut) {
-        plan.begin = item * units + small_div(part * units, parts);
-        plan.end = item * units + small_div((part + 1) * units, parts);
-      }
-    } else {
-      parts = 0;
-      ranges = max(1, min(ctas, total / least));
-      if (cta < ranges) {
-        plan.begin = static_cast<uint32_t>(cta) * total / ranges;
-        plan.end = static_cast<uint32_t>(cta + 1) * total / ranges;
-      }
-    }
+  // The items that are left over when each CTA has had the same number are
+  // divided where that leaves every CTA one part at most; otherwise they are
+  // dealt like the others (128 items of 28 units on 152 CTAs took 20.3 us, cut
+  // into 152 ranges of K 23.8: fewer CTAs at work draw more each).  A unit
+  // takes about 0.4 us.  Adding up an item's parts takes tok / 80 of a unit
+  // for each (8 ns a token), so a part has at least the square root of units *
+  // tok / 80 units, and about kSplitUnits units' time besides (less where
+  // whole items follow and hide it), which the division has to save: one
+  // token's 32 items of 3 units take 6.6 us undivided and 7.7 divided, of 16
+  // units 11.7 and 9.7.
+  plan.chunks = 0;
+  plan.parts = plan.cut > 0 ? small_div(ctas, plan.cut) : 0;
+  if (tok > kSplitTok) {
+    plan.chunks = min(plan.parts / kPair, tok / 16);
+    plan.parts = kPair * plan.chunks;
+  } else {
+    const int least = max(1, static_cast<int>(approx_sqrt(units * tok * (1 / 80.f))));
+    plan.parts = min(plan.parts, small_div(units, least));
+    const int saved = units - small_div(units + plan.parts - 1, max(plan.parts, 1));
+    if (saved < (plan.items > plan.cut ? kSplitUnitsHidden : kSplitUnits)) plan.parts = 0;
   }
+  if (plan.parts < 2) plan.cut = plan.parts = 0;
   const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget / stage);
   const int n_acc = min(kMaxAcc, kSfCol / (kPair * tok));
   ItemRing items{item_full, item_empty, item_slots, a.test_timeout ? kTestWaitPolls : kWaitPolls, 0, 0};
@@ -680,14 +659,14 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     const int t = (warp - kEpiWarp0) / 4;                // weight tile of the pair
     const uint32_t out_stage = smem0 + kOutOff + (warp - kEpiWarp0) * kOutBytes;
     int acc = 0, use = 0;
-    // A wait that ran out ends a warp; through the segments cut along K, whose
+    // A wait that ran out ends a warp; at a segment cut along K, whose
     // handling has barriers, the epilogue warps end together.
-    int cut_left = plan.end > plan.begin ? (plan.end - 1) / units - plan.begin / units + 1 : 0;
+    bool cut_next = !plan.chunks && static_cast<int>(blockIdx.x) < plan.cut * plan.parts;
     while (true) {
       const bool on = items.next(w, a.status);
       bool ok = on && __all_sync(0xffffffffu, mbar_wait(&tfull[acc], use & 1, a.status));
-      if (cut_left > 0) {
-        --cut_left;
+      if (cut_next) {
+        cut_next = false;
         ok = epilogue_all(ok);
       }
       if (!ok) break;
@@ -697,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       uint16_t* out = a.C + static_cast<size_t>(w.row0) * a.ldc;
       const bool whole = w.u0 == 0 && w.u1 == units;
       const size_t part = static_cast<size_t>(t) * kSplitTok * 128 + 4 * lrow;
-      float* mine_p = a.partial + static_cast<size_t>(2 * blockIdx.x + (w.u0 == 0)) * kSlotFloats + part;
+      float* mine_p = a.partial + static_cast<size_t>(blockIdx.x) * kSlotFloats + part;
       if (whole) {
         // the next 32 tokens' accumulators are on their way while these go out
         uint32_t next[2][16];
@@ -733,12 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
       if (++acc == n_acc) acc = 0, ++use;
       if (whole) continue;
       // a cut item: the CTA that arrives last adds the parts in K order
-      int first = w.item * parts, last = first + parts - 1;
-      if (parts == 0) {
-        const uint32_t i0 = w.item * units;               // its units are [i0, i0 + units)
-        first = ((i0 + 1) * ranges - 1) / total;
-        last = ((i0 + units) * ranges - 1) / total;
-      }
+      const int first = w.item * plan.parts, last = first + plan.parts - 1;
       epilogue_all(true);
       if (tid == 32 * kEpiWarp0) {
         // releases the parts stored by all threads before the barrier, and
@@ -768,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
 }  // namespace
 
 size_t mxfp4_gemm_workspace_bytes() {
-  return kMxMaxCtas * sizeof(int) + 2 * static_cast<size_t>(kMxMaxCtas) * kSlotFloats * sizeof(float);
+  return kMxMaxCtas * sizeof(int) + static_cast<size_t>(kMxMaxCtas) * kSlotFloats * sizeof(float);
 }
 
 cudaError_t mxfp4_gemm_launch(const uint8_t* rows, const uint8_t* w, int E, int N, int K, const int32_t* counts,
