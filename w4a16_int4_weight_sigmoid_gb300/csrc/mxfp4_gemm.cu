@@ -162,17 +162,17 @@ struct Walk {
   __device__ explicit Walk(const Plan& plan) : p(plan), item(-1), e(0), u0(0), u1(plan.units) {
     const int cta = blockIdx.x;
     if (cta < p.cut * p.parts) {
-      item = cta / p.parts;
+      item = small_div(cta, p.parts);
       const int part = cta - item * p.parts;
       more = true;
       locate();
       if (!p.chunks) {
-        u0 = part * p.units / p.parts;
-        u1 = (part + 1) * p.units / p.parts;
+        u0 = small_div(part * p.units, p.parts);
+        u1 = small_div((part + 1) * p.units, p.parts);
         return;
       }
-      const int t = part / p.chunks, c = part - t * p.chunks;   // one tile, one run of rows
-      const int run = ((rows + p.chunks - 1) / p.chunks + 15) & ~15;
+      const int t = part >= p.chunks, c = part - t * p.chunks;   // one tile, one run of rows
+      const int run = (small_div(rows + p.chunks - 1, p.chunks) + 15) & ~15;
       tile += t;
       tiles -= t;
       if (tiles > 1) tiles = 1;
@@ -192,15 +192,15 @@ struct Walk {
   // The item's expert: the largest e with prefix[e] <= item (items only grow).
   __device__ void locate() {
     const int lane = threadIdx.x & 31;
-    while (true) {
-      const int at = e + 1 + lane;
-      const uint32_t past = __ballot_sync(0xffffffffu, at > p.E || p.prefix[at] > item);
-      if (past) {
-        e += __ffs(past) - 1;
-        break;
-      }
-      e += 32;
+    auto past = [&](int at) { return __ballot_sync(0xffffffffu, at > p.E || p.prefix[at] > item); };
+    uint32_t found = past(e + 1 + lane);
+    if (!found) {                    // further on: the 32nd of the experts, then the expert
+      const int block = (p.E + 31) / 32;
+      static_assert(kMaxExperts <= 32 * 32, "two steps of 32");
+      e = block * (__ffs(past(min(block * (lane + 1), p.E))) - 1);
+      found = past(e + 1 + lane);
     }
+    e += __ffs(found) - 1;
     const int cnt = ld_ca(p.cnts + e), local = item - p.prefix[e];
     row0 = ld_ca(p.offs + e);
     rows = cnt;
