@@ -270,6 +270,30 @@ def test_product(case, silu):
     assert torch.equal(C, ex.product(silu))
 
 
+DIVIDED = [
+    ([1] * 200, 8, 128, 2048),                       # K in parts, whole items behind them
+    ([48, 33, 47], 16, 392, 4096),                   # K in parts, the largest row tile for that
+    ([7] * 80, 8, 264, 1792),                        # parts of one unit; an odd number of weight tiles
+    ([90] * 160, 32, 128, 512),                      # rows in runs, whole items behind them
+    ([64] * 77, 16, 128, 512),                       # more than half the CTAs busy: not divided
+    ([300, 50], 16, 392, 7168),                      # rows in runs, unequal row tiles
+    ([0] * 70 + [1] + [0] * 500 + [2] + [0] * 451 + [1], 8, 16, 64),   # 1024 experts, few with rows
+]
+
+
+@pytest.mark.parametrize("case", range(len(DIVIDED)))
+@pytest.mark.parametrize("silu", [False, True])
+def test_product_of_divided_items(case, silu):
+    counts, bm, N, K = DIVIDED[case]
+    N = -(-N // 16) * 16 if silu else N
+    ex = Experts(counts, bm, N, K, 100 + case)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    C = ex.product(silu, status=status)
+    assert status.item() == 0
+    ex.check(C, silu)
+    assert torch.equal(C, ex.product(silu))
+
+
 @pytest.mark.parametrize("name", ["fp16", "fp32"])
 def test_product_of_other_row_types(name):
     ex = Experts([3, 20, 0, 7], 16, 128, 512, 21, TYPES[name])
