@@ -42,7 +42,7 @@
 // Measured (kernel alone): 64 tokens on 48 of 384 experts, N 4096, K 7168: 85
 // us, 6.1 TB/s of DRAM, its bound; 8192 tokens: 136 us, DRAM at 5.8 TB/s and
 // exposed epilogues; 16384 rows of 8 experts: 177 us, 5.4 PFLOP/s: 54 bytes a
-// cycle into each SM, of about 64 that its port takes (tensor pipe 54 %
+// cycle into each SM, of about 64 that its port takes (tensor pipe 56 %
 // busy); one token, N 512: 8.7 us, latency.
 // TMEM: accumulators from column 0, scales from column kSfCol.
 // Every mbarrier wait is bounded.  A warp whose wait runs out records
