@@ -11,11 +11,11 @@
 // whatever the number of its experts.  Sums are FP32 in increasing j (the
 // weight gradient: FP32 in a tree fixed by the call's sizes), each result
 // rounded once; no atomics, so a call repeats bit for bit.
-// Measured: permute of 8192 tokens x 7168 BF16 to 48 of 384 experts 43.3 us
-// (239 MB with the zeroed padding: 5.5 TB/s), its weighted sum's gradient
-// 54.1 us (312 MB: 5.8 TB/s), of 6.7 TB/s that a copy reaches; 20 tokens at
-// block 128, 99 % padding, 37 us (6.4 TB/s); weighted sum of 128 FP32 tokens
-// 5.2 us; 64 tokens permuted 3.5 us, bound by the launch and two dependent
+// Measured: permute of 8192 tokens x 7168 BF16 to 48 of 384 experts 39.3 us
+// (239 MB with the zeroed padding: 6.1 TB/s), its weighted sum's gradient
+// 56 us (312 MB: 5.6 TB/s), of 6.7 TB/s that a copy reaches; 20 tokens at
+// block 128, 99 % padding, 34 us (7.1 TB/s); weighted sum of 128 FP32 tokens
+// 5.2 us; 64 tokens permuted 2.4 us, bound by the launch and two dependent
 // loads.
 //
 // Rows are moved in accesses of B bytes: 32 where every base, row stride and
@@ -55,9 +55,15 @@ constexpr int kCtas = 12, kWaves = 4;
 
 // ------------------------------------------------------------ padding rows
 // Zeros in the padding rows (sorted >= M * topk) of the aligned order: CTA b
-// of nb takes every nb-th run of kPadRows rows below the padded total, all
-// threads on one row (a warp on a row of its own took 25 us at 64 tokens).
-constexpr int kPadRows = 8;
+// of nb takes every nb-th run of rows below the padded total, all threads on
+// one row (a warp on a row of its own took 25 us at 64 tokens).  A run is
+// kPadBytes long, one to eight rows (eight rows of 7168 BF16 values each: one
+// token permuted at block 16 3.2 us against 1.9, 8192 at block 128 43.0
+// against 39.3).
+constexpr int kPadBytes = 8192;
+__host__ __device__ constexpr int pad_run(int row_bytes) {
+  return row_bytes > kPadBytes ? 1 : row_bytes < kPadBytes / 8 ? 8 : kPadBytes / row_bytes;
+}
 
 // Zeros at any element alignment, by all threads: 16-byte stores between a
 // first and a last part of up to 14 bytes (2-byte stores throughout took 20 us
@@ -73,16 +79,19 @@ __device__ __forceinline__ void zero_bytes(uint8_t* dst, int bytes) {
 
 __device__ __forceinline__ void zero_padding(const RowArgs& a, int row_bytes, long long out_stride, int b, int nb) {
   const int lane = threadIdx.x & 31, sentinel = a.M * a.topk;
-  const int total = ld_ca(a.ntpp);
-  // neighbouring rows without a gap are one stretch (their lengths' limit
-  // keeps kPadRows of them within 32 bits)
+  // neighbouring rows without a gap are one stretch (of kPadBytes at
+  // most, or one row)
   const bool dense = out_stride == row_bytes;
-  for (int r0 = b * kPadRows; r0 < a.rows; r0 += nb * kPadRows) {
-    // the entry is read before the total is known: entries past the total
-    // exist, and are dropped
-    const int r = r0 + lane, f = lane < kPadRows && r < a.rows ? ld_ca(a.sorted + r) : 0;
-    if (r0 >= total) break;
-    uint32_t pad = __ballot_sync(0xffffffffu, lane < kPadRows && r < min(total, a.rows) && f >= sentinel);
+  const int run = pad_run(row_bytes);
+  // A run's entries are read ahead, before the total is known and while the run
+  // before is written: entries past the total exist, and are dropped.  (32 rows
+  // of many runs in one load took 0-20 % longer with much padding.)
+  auto entry = [&](int r) { return lane < run && r < a.rows ? ld_ca(a.sorted + r) : 0; };
+  int f = entry(b * run + lane);
+  const int total = min(ld_ca(a.ntpp), a.rows);
+  for (int r0 = b * run; r0 < total; r0 += nb * run) {
+    uint32_t pad = __ballot_sync(0xffffffffu, lane < run && r0 + lane < total && f >= sentinel);
+    f = entry(r0 + nb * run + lane);
     while (pad) {
       const int first = __ffs(pad) - 1, n = dense ? __ffs(~(pad >> first)) - 1 : 1;
       zero_bytes(static_cast<uint8_t*>(a.out) + (r0 + first) * out_stride, n * row_bytes);
@@ -295,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(RowArgs a) {
 // One pass over dout[t] and y[p] gives both dy[p] and the dot product; dout[t]
 // comes from L1 for every j after the first.
 template <typename T, int B, int kGroup>
-__global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a, int pad_ctas) {
+__global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a, int pad_x) {
   // accesses in flight: with short ones more (4000 odd rows of 3323 BF16 values
   // 39.7 us with four, 33.4 with eight; 16 cost short rows up to a third)
   constexpr int V = B / sizeof(T), kUnroll = B >= 32 ? 2 : B >= 8 ? 4 : 8;
@@ -303,13 +312,12 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x % kGroup;
   grid_dep_wait();
   grid_dep_launch();
-  if (static_cast<int>(blockIdx.x) < pad_ctas) {
-    if (blockIdx.y == 0)
-      zero_padding(a, a.H * static_cast<int>(sizeof(T)), a.ldo * static_cast<long long>(sizeof(T)), blockIdx.x,
-                      pad_ctas);
+  if (static_cast<int>(blockIdx.x) < pad_x) {
+    zero_padding(a, a.H * static_cast<int>(sizeof(T)), a.ldo * static_cast<long long>(sizeof(T)),
+                 blockIdx.x * gridDim.y + blockIdx.y, pad_x * gridDim.y);
     return;
   }
-  const int t = (blockIdx.x - pad_ctas) * (kThreads / kGroup) + (kGroup == 32 ? warp : 0), nv = a.H / V;
+  const int t = (blockIdx.x - pad_x) * (kThreads / kGroup) + (kGroup == 32 ? warp : 0), nv = a.H / V;
   if (kGroup == 32 && t >= a.M) return;
   const T* g = static_cast<const T*>(a.x) + t * a.ldx;
   // lane j holds assignment j: the rows of all are known after one load
@@ -368,11 +376,12 @@ __global__ void __launch_bounds__(kThreads) unpermute_backward_kernel(RowArgs a,
   if (mine) a.dw[f] = dw;
 }
 
-// CTAs that cover `rows` rows of the order for their padding: one for each 4
-// KB of them, at most (most of an order's capacity is past its padded total).
-int padding_ctas(int rows, long long row_bytes) {
-  const long long runs = (rows + kPadRows - 1) / kPadRows;
-  return static_cast<int>(std::min(runs, rows * row_bytes / 4096 + 1));
+// CTAs that cover `rows` rows of the order for their padding: one for each
+// run, and for each 4 KB at most (most of an order's capacity is past its
+// padded total).
+int padding_ctas(int rows, int row_bytes) {
+  const int run = pad_run(row_bytes);
+  return static_cast<int>(std::min<long long>((rows + run - 1) / run, static_cast<long long>(rows) * row_bytes / 4096 + 1));
 }
 
 // warp_bytes: what one warp has of a row at a time.
@@ -407,18 +416,19 @@ cudaError_t launch_combine(const RowArgs& a, cudaStream_t st) {
 
 template <typename T, int B>
 cudaError_t launch_unpermute_backward(const RowArgs& a, cudaStream_t st) {
-  const int pad = std::min(padding_ctas(a.rows, static_cast<long long>(a.H) * sizeof(T)), 8 * sm_count());
   int split = 1;
   while (split < a.topk && static_cast<long long>(a.M) * split < 4LL * sm_count()) split *= 2;
   split = std::min(split, a.topk);
+  const int pads = std::min(padding_ctas(a.rows, a.H * static_cast<int>(sizeof(T))), 8 * sm_count());
+  const int pad_x = (pads + split - 1) / split;
   // a warp per token where its lanes pass over the row at most four times and
   // the tokens fill the SMs (3296 rows of 117 values: 8.0 us with a CTA each)
   const int nv = a.H / (B / static_cast<int>(sizeof(T)));
   if (nv <= 128 && a.M >= 16 * sm_count())
-    return launch_kernel(unpermute_backward_kernel<T, B, 32>, dim3((a.M + kWarps - 1) / kWarps + pad, split),
-                         dim3(kThreads), 0, st, true, a, pad);
-  return launch_kernel(unpermute_backward_kernel<T, B, kThreads>, dim3(a.M + pad, split), dim3(kThreads), 0, st, true,
-                       a, pad);
+    return launch_kernel(unpermute_backward_kernel<T, B, 32>, dim3((a.M + kWarps - 1) / kWarps + pad_x, split),
+                         dim3(kThreads), 0, st, true, a, pad_x);
+  return launch_kernel(unpermute_backward_kernel<T, B, kThreads>, dim3(a.M + pad_x, split), dim3(kThreads), 0, st, true,
+                       a, pad_x);
 }
 
 // Access size shared by all row matrices of the call.
