@@ -175,6 +175,14 @@ def _check_operands(A, C, K: int, N: int, epilogue: int, a_rows: int, c_rows: in
         raise ValueError(f"{what}: C holds {C.numel()} values, needs {c_rows} rows of {ncols}")
 
 
+def _check_holds(what: str, **need):
+    """Each tensor given as name=(tensor, values) holds at least that many values: the C ABI
+    writes or reads them through raw pointers.  Raises ValueError before anything runs."""
+    for name, (t, n) in need.items():
+        if isinstance(t, torch.Tensor) and t.numel() < n:
+            raise ValueError(f"{what}: {name} holds {t.numel()} values, needs {n}")
+
+
 # The current stream's handle without building a torch.cuda.Stream object, which
 # takes longer on the host (2.9 us) than the rest of a small call's checks.
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
@@ -242,6 +250,12 @@ def chord_moe_route_align(logits, bias, topk: int, expert_begin: int, E_local: i
                           stream=None):
     """chord_moe_route then chord_moe_align in one call (one launch for small M)."""
     M, E_total = logits.shape
+    n = M * topk
+    blocks = chord_moe_align_capacity(M, topk, E_local, block_m) // max(block_m, 1)
+    _check_holds("chord_moe_route_align", bias=(bias, E_total), topk_weights=(topk_weights, n), topk_ids=(topk_ids, n),
+                 expert_ids=(expert_ids, blocks), num_tokens_post_padded=(num_tokens_post_padded, 1),
+                 expert_counts=(expert_counts, E_local), expert_offsets=(expert_offsets, E_local + 1),
+                 sorted_positions=(sorted_positions, n))
     i32 = torch.int32
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().chord_moe_route_align(
