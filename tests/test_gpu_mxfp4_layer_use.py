@@ -1,0 +1,48 @@
+"""GPU tests of the layer classes as programs use them: other shapes than the layer's,
+batches of changing size, captured graphs, other streams, repeated routing and second
+derivatives."""
+import pytest
+import torch
+
+from w4a16_int4_weight_sigmoid_gb300.layer import MXFP4MoELayer, quantize_mxfp4
+
+from gpu_util import ensure_lib
+
+pytestmark = pytest.mark.gpu
+
+E, K, H, I = 8, 2, 256, 128
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_lib()
+
+
+def randn(*shape, seed=0):
+    return torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def make_layer(seed=0):
+    return MXFP4MoELayer(quantize_mxfp4(randn(E, 2 * I, H, seed=seed) / H ** 0.5),
+                         quantize_mxfp4(randn(E, H, I, seed=seed + 1) / I ** 0.5), E, 0, K)
+
+
+def inputs(M, seed=0):
+    return randn(M, H, seed=10 + seed), randn(M, E, seed=20 + seed), torch.zeros(E, device="cuda")
+
+
+def test_the_layer_refuses_other_shapes():
+    """Rows of another length, and logits of other tokens or experts, are refused before anything runs."""
+    layer = make_layer()
+    x, logits, bias = inputs(12)
+    out = torch.full((12, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    for a in ((x[:, :128], logits, bias), (x[:, :224].contiguous(), logits, bias), (x.reshape(-1), logits, bias),
+              (x, logits[:11], bias), (x, logits[:0], bias), (x[:11], logits, bias), (x[:0], logits, bias),
+              (x, logits[:, :7].contiguous(), bias), (x, logits, bias[:7]), (x, logits, torch.zeros(9, device="cuda"))):
+        with pytest.raises(ValueError):
+            layer.forward(*a, out=out)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all()
+    layer.forward(x, logits, bias, out=out)
+    assert not (out == 7.0).all() and layer.dev_status.item() == 0
+    assert layer.forward(x[:0], logits[:0], bias).shape == (0, H)

@@ -208,6 +208,10 @@ class MXFP4MoELayer:
     def forward(self, x, logits, bias, out=None, stream=None):
         """x [M, H] (BF16, FP16 or FP32), logits FP32 [M, E_total], bias FP32 [E_total] -> out [M, H] BF16."""
         M = x.shape[0]
+        for name, t, shape in (("x", x, (M, self.H)), ("logits", logits, (M, self.E_total)),
+                               ("bias", bias, (self.E_total,))):
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
         if out is None:
             out = torch.empty((M, self.H), dtype=torch.bfloat16, device=self.device)
         if M == 0:
