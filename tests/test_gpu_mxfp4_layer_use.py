@@ -4,7 +4,7 @@ derivatives."""
 import pytest
 import torch
 
-from w4a16_int4_weight_sigmoid_gb300.layer import MXFP4MoELayer, quantize_mxfp4
+from w4a16_int4_weight_sigmoid_gb300.layer import ExpertOrder, MXFP4MoELayer, quantize_mxfp4, unpermute_rows
 
 from gpu_util import ensure_lib
 
@@ -46,3 +46,13 @@ def test_the_layer_refuses_other_shapes():
     layer.forward(x, logits, bias, out=out)
     assert not (out == 7.0).all() and layer.dev_status.item() == 0
     assert layer.forward(x[:0], logits[:0], bias).shape == (0, H)
+
+
+def test_unpermute_takes_the_rows_of_its_order():
+    """Rows of another order would lose assignments without a word."""
+    order = ExpertOrder(12, K, 0, E).route(randn(12, E), torch.zeros(E, device="cuda"))
+    y, w = randn(order.capacity, H), order.topk_weights
+    assert unpermute_rows(y, w, order).shape == (12, H)
+    for bad in (y[:16], torch.cat([y, y[:8]])):
+        with pytest.raises(ValueError, match="rows"):
+            unpermute_rows(bad, w, order)

@@ -152,6 +152,8 @@ def permute_rows(x, order: ExpertOrder):
 def unpermute_rows(y, weights, order: ExpertOrder):
     """The weighted sum of rows y [order.capacity, H] back to tokens [M, H]; differentiable
     in y and in weights FP32 [M, topk]."""
+    if y.shape[0] != order.capacity:
+        raise ValueError(f"y must hold the {order.capacity} rows of its order, got {y.shape[0]}")
     return _Unpermute.apply(y, weights, order)
 
 
