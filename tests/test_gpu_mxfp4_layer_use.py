@@ -56,3 +56,13 @@ def test_unpermute_takes_the_rows_of_its_order():
     for bad in (y[:16], torch.cat([y, y[:8]])):
         with pytest.raises(ValueError, match="rows"):
             unpermute_rows(bad, w, order)
+
+
+def test_the_layer_is_ready_when_made():
+    """Its weights and counters are complete when the constructor returns, whatever the
+    current stream has to do before, so that the first call may be on any stream."""
+    args = [quantize_mxfp4(randn(E, 2 * I, H)), quantize_mxfp4(randn(E, H, I))]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                    # about 10 ms
+    MXFP4MoELayer(*args, E, 0, K)
+    assert torch.cuda.current_stream().query()

@@ -187,6 +187,7 @@ class MXFP4MoELayer:
         self.w2 = self._prepack(q2, s2, False)
         self._ws = torch.zeros(chord.chord_mxfp4_moe_gemm_workspace_bytes(), dtype=torch.uint8, device=self.device)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        torch.cuda.current_stream(self.device).synchronize()   # the first call may be on any stream
         self._M = -1
 
     def _prepack(self, codes, scales, gate_up):
