@@ -66,3 +66,26 @@ def test_the_layer_is_ready_when_made():
     torch.cuda._sleep(20_000_000)                    # about 10 ms
     MXFP4MoELayer(*args, E, 0, K)
     assert torch.cuda.current_stream().query()
+
+
+def test_buffers_are_memory_of_the_stream_they_are_used_on():
+    """Batches of two sizes in turn on a side stream, kept busy, while the current stream
+    allocates and overwrites what the allocator gives it: a call's buffers and output come
+    from its own stream's memory, so nothing that is dropped is handed to the other."""
+    layer = make_layer()
+    batches = [inputs(M, seed=M) for M in (40, 9)]
+    want = [layer.forward(*b) for b in batches]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = []
+    for i in range(6):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(2_000_000)             # about a millisecond ahead of each call
+        got.append(layer.forward(*batches[i % 2], stream=s if i < 3 else s.cuda_stream))
+        for _ in range(8):                            # the sizes of the layer's own buffers and output
+            for t in (layer.h, layer.y, layer._rows, got[-1]):
+                torch.empty_like(t).fill_(1)
+    s.synchronize()
+    for i, out in enumerate(got):
+        assert torch.equal(out, want[i % 2])
+    assert layer.dev_status.item() == 0

@@ -9,6 +9,8 @@ unpermute_rows move rows into it and back with gradients.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -21,6 +23,17 @@ def to_device(a, device="cuda"):
     if a.dtype == np.uint16:
         return torch.from_numpy(a.view(np.int16)).to(device).view(torch.bfloat16)
     return torch.from_numpy(a).to(device)
+
+
+def _on_stream(stream):
+    """A context in which torch allocates and copies on `stream` (a stream, a raw handle, or
+    None: the current one), and calls without a stream run: memory that it frees there is
+    handed out again behind that stream's work only."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.stream(stream)
 
 
 def prepack(q, s, gate_up: bool, stream=None):
@@ -173,8 +186,8 @@ class MXFP4MoELayer:
 
     w13: (codes [E_local, 2I, H/2], scales [E_local, 2I, H/32]), rows 0..I-1 gate and
     I..2I-1 up; w2: (codes [E_local, H, I/2], scales [E_local, H, I/32]), as
-    quantize_mxfp4 gives them, on the device.  Calls share the layer's buffers, so they
-    follow one another on one stream."""
+    quantize_mxfp4 gives them, on the device.  Calls share the product's workspace, so they
+    follow one another; each one's buffers are memory of its own stream."""
 
     def __init__(self, w13, w2, E_total: int, expert_begin: int, topk: int):
         (q13, s13), (q2, s2) = w13, w2
@@ -188,7 +201,7 @@ class MXFP4MoELayer:
         self._ws = torch.zeros(chord.chord_mxfp4_moe_gemm_workspace_bytes(), dtype=torch.uint8, device=self.device)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=self.device)
         torch.cuda.current_stream(self.device).synchronize()   # the first call may be on any stream
-        self._M = -1
+        self._key = None      # (tokens, stream) of the buffers
 
     def _prepack(self, codes, scales, gate_up):
         E, N, K2 = codes.shape
@@ -196,38 +209,44 @@ class MXFP4MoELayer:
         chord.chord_mxfp4_prepack(codes, scales, gate_up, packed)
         return packed
 
+    def _allocate(self, M: int):
+        """(order, row operand, h, y) for M tokens, in the current stream's memory."""
+        order = ExpertOrder(M, self.topk, self.expert_begin, self.E_local, device=self.device)
+        cap, bf16 = order.capacity, dict(dtype=torch.bfloat16, device=self.device)
+        rows = torch.empty(max(chord.chord_mxfp4_rows_bytes(cap, self.H), chord.chord_mxfp4_rows_bytes(cap, self.I)),
+                           dtype=torch.uint8, device=self.device)
+        return order, rows, torch.empty((cap, self.I), **bf16), torch.empty((cap, self.H), **bf16)
+
     def _buffers(self, M: int):
-        if M != self._M:
-            self.order = ExpertOrder(M, self.topk, self.expert_begin, self.E_local, device=self.device)
-            cap = self.order.capacity
-            u8 = dict(dtype=torch.uint8, device=self.device)
-            self._rows = torch.empty(max(chord.chord_mxfp4_rows_bytes(cap, self.H),
-                                         chord.chord_mxfp4_rows_bytes(cap, self.I)), **u8)
-            self.h = torch.empty((cap, self.I), dtype=torch.bfloat16, device=self.device)
-            self.y = torch.empty((cap, self.H), dtype=torch.bfloat16, device=self.device)
-            self._M = M
+        # of one stream only: what is dropped here may still be in use on its own
+        key = (M, chord._stream(None))
+        if key != self._key:
+            self.order, self._rows, self.h, self.y = self._allocate(M)
+            self._key = key
         return self.order
 
     def forward(self, x, logits, bias, out=None, stream=None):
-        """x [M, H] (BF16, FP16 or FP32), logits FP32 [M, E_total], bias FP32 [E_total] -> out [M, H] BF16."""
+        """x [M, H] (BF16, FP16 or FP32), logits FP32 [M, E_total], bias FP32 [E_total] -> out [M, H] BF16.
+        A missing `out` is made on the call's stream."""
         M = x.shape[0]
         for name, t, shape in (("x", x, (M, self.H)), ("logits", logits, (M, self.E_total)),
                                ("bias", bias, (self.E_total,))):
             if t.shape != shape:
                 raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if out is None:
-            out = torch.empty((M, self.H), dtype=torch.bfloat16, device=self.device)
-        if M == 0:
-            return out
-        o = self._buffers(M).route(logits, bias, stream=stream)
-        cap, n = o.capacity, o.num_tokens_post_padded
-        chord.chord_mxfp4_quantize_rows(x, o.sorted_positions, self.topk, n, cap, self._rows, stream=stream)
-        chord.chord_mxfp4_moe_gemm(self._rows, self.w13, self.E_local, 2 * self.I, self.H, o.expert_counts,
-                                   o.expert_offsets, cap, chord.CHORD_EPI_SILU_MUL, self.h, self._ws,
-                                   self.dev_status, stream=stream)
-        chord.chord_mxfp4_quantize_rows(self.h, None, 1, n, cap, self._rows, stream=stream)
-        chord.chord_mxfp4_moe_gemm(self._rows, self.w2, self.E_local, self.H, self.I, o.expert_counts,
-                                   o.expert_offsets, cap, chord.CHORD_EPI_STORE, self.y, self._ws,
-                                   self.dev_status, stream=stream)
-        chord.chord_moe_unpermute(self.y, o.topk_weights, o.sorted_positions, out, stream=stream)
+        with _on_stream(stream):
+            if out is None:
+                out = torch.empty((M, self.H), dtype=torch.bfloat16, device=self.device)
+            if M > 0:
+                self._run(x, logits, bias, out)
         return out
+
+    def _run(self, x, logits, bias, out):
+        o = self._buffers(x.shape[0]).route(logits, bias)
+        cap, n = o.capacity, o.num_tokens_post_padded
+        chord.chord_mxfp4_quantize_rows(x, o.sorted_positions, self.topk, n, cap, self._rows)
+        chord.chord_mxfp4_moe_gemm(self._rows, self.w13, self.E_local, 2 * self.I, self.H, o.expert_counts,
+                                   o.expert_offsets, cap, chord.CHORD_EPI_SILU_MUL, self.h, self._ws, self.dev_status)
+        chord.chord_mxfp4_quantize_rows(self.h, None, 1, n, cap, self._rows)
+        chord.chord_mxfp4_moe_gemm(self._rows, self.w2, self.E_local, self.H, self.I, o.expert_counts,
+                                   o.expert_offsets, cap, chord.CHORD_EPI_STORE, self.y, self._ws, self.dev_status)
+        chord.chord_moe_unpermute(self.y, o.topk_weights, o.sorted_positions, out)
