@@ -89,3 +89,21 @@ def test_buffers_are_memory_of_the_stream_they_are_used_on():
     for i, out in enumerate(got):
         assert torch.equal(out, want[i % 2])
     assert layer.dev_status.item() == 0
+
+
+def test_quantising_strided_weights_on_another_stream():
+    """Rows that have to be copied together first are copied on the call's stream, and what
+    the current stream allocates meanwhile is not theirs."""
+    w = randn(E, H, 2 * I).transpose(1, 2)            # rows of H, not contiguous
+    want = quantize_mxfp4(w.contiguous())
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream, 0):              # 0: the default stream's handle
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(2_000_000)
+        got = quantize_mxfp4(w, stream=stream)
+        for _ in range(8):
+            for t in (w, *got):
+                torch.empty(t.shape, dtype=t.dtype, device="cuda").fill_(1)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -171,11 +171,13 @@ def unpermute_rows(y, weights, order: ExpertOrder):
 
 
 def quantize_mxfp4(w, stream=None):
-    """[..., K] BF16, FP16 or FP32 on the device -> MXFP4 codes uint8 [..., K/2] and scales uint8 [..., K/32]."""
+    """[..., K] BF16, FP16 or FP32 on the device -> MXFP4 codes uint8 [..., K/2] and scales uint8 [..., K/32],
+    made on the call's stream."""
     K = w.shape[-1]
-    codes = torch.empty((*w.shape[:-1], K // 2), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((*w.shape[:-1], K // 32), dtype=torch.uint8, device=w.device)
-    chord.chord_mxfp4_quantize(w.reshape(-1, K), codes, scales, stream=stream)
+    with _on_stream(stream):
+        codes = torch.empty((*w.shape[:-1], K // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((*w.shape[:-1], K // 32), dtype=torch.uint8, device=w.device)
+        chord.chord_mxfp4_quantize(w.reshape(-1, K), codes, scales)
     return codes, scales
 
 
