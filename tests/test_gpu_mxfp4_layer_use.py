@@ -107,3 +107,34 @@ def test_quantising_strided_weights_on_another_stream():
                 torch.empty(t.shape, dtype=t.dtype, device="cuda").fill_(1)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_captured_graphs_keep_their_buffers():
+    """One graph per batch size on one layer, calls of other sizes between, and tensors that
+    take any memory set free: every replay gives what its own batch should, and touches
+    nobody else's memory."""
+    layer = make_layer()
+    sizes = (64, 5, 130, 32)
+    static, fresh, want = {}, {}, {}
+    for M in sizes:
+        static[M], fresh[M] = inputs(M, seed=M), inputs(M, seed=M + 1)
+        want[M] = layer.forward(*fresh[M])
+    graphs, outs, kept, watched = {}, {}, {}, []
+    for M in sizes:
+        graphs[M], outs[M] = torch.cuda.CUDAGraph(), torch.empty((M, H), dtype=torch.bfloat16, device="cuda")
+        with torch.cuda.graph(graphs[M]):
+            layer.forward(*static[M], out=outs[M])
+        kept[M] = [t.data_ptr() for t in (layer.order.sorted_positions, layer._rows, layer.h, layer.y)]
+        layer.forward(*static[32])
+        watched += [torch.full_like(t, 1) for t in (layer._rows, layer.h, layer.y) for _ in range(4)]
+    mine = {t.data_ptr() for t in watched} | {t.data_ptr() for t in (layer._rows, layer.h, layer.y)}
+    for M in sizes:                                   # nothing that lives now is a captured buffer
+        assert not mine & set(kept[M])
+    for M in (32, 64, 5, 130, 64):
+        for a, b in zip(static[M], fresh[M]):
+            a.copy_(b)
+        graphs[M].replay()
+        assert torch.equal(outs[M], want[M])
+        assert torch.equal(layer.forward(*fresh[5]), want[5])
+    assert all((t == 1).all() for t in watched)
+    assert layer.dev_status.item() == 0

@@ -189,7 +189,9 @@ class MXFP4MoELayer:
     w13: (codes [E_local, 2I, H/2], scales [E_local, 2I, H/32]), rows 0..I-1 gate and
     I..2I-1 up; w2: (codes [E_local, H, I/2], scales [E_local, H, I/32]), as
     quantize_mxfp4 gives them, on the device.  Calls share the product's workspace, so they
-    follow one another; each one's buffers are memory of its own stream."""
+    follow one another; each one's buffers are memory of its own stream.  Calls may be
+    captured in CUDA graphs, one per batch size: the buffers of a captured call are kept
+    with the layer, which has to outlive the graph."""
 
     def __init__(self, w13, w2, E_total: int, expert_begin: int, topk: int):
         (q13, s13), (q2, s2) = w13, w2
@@ -204,6 +206,7 @@ class MXFP4MoELayer:
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=self.device)
         torch.cuda.current_stream(self.device).synchronize()   # the first call may be on any stream
         self._key = None      # (tokens, stream) of the buffers
+        self._captured = {}   # buffers that captured graphs use, by (tokens, stream)
 
     def _prepack(self, codes, scales, gate_up):
         E, N, K2 = codes.shape
@@ -222,7 +225,13 @@ class MXFP4MoELayer:
     def _buffers(self, M: int):
         # of one stream only: what is dropped here may still be in use on its own
         key = (M, chord._stream(None))
-        if key != self._key:
+        if torch.cuda.is_current_stream_capturing():
+            # a graph's replays use them as long as it lives: kept, and for captures only
+            if key not in self._captured:
+                self._captured[key] = self._allocate(M)
+            self.order, self._rows, self.h, self.y = self._captured[key]
+            self._key = None
+        elif key != self._key:
             self.order, self._rows, self.h, self.y = self._allocate(M)
             self._key = key
         return self.order
