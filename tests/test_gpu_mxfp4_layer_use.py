@@ -4,7 +4,8 @@ derivatives."""
 import pytest
 import torch
 
-from w4a16_int4_weight_sigmoid_gb300.layer import ExpertOrder, MXFP4MoELayer, quantize_mxfp4, unpermute_rows
+from w4a16_int4_weight_sigmoid_gb300.layer import (ExpertOrder, MXFP4MoELayer, permute_rows, quantize_mxfp4,
+                                                   unpermute_rows)
 
 from gpu_util import ensure_lib
 
@@ -138,3 +139,18 @@ def test_captured_graphs_keep_their_buffers():
         assert torch.equal(layer.forward(*fresh[5]), want[5])
     assert all((t == 1).all() for t in watched)
     assert layer.dev_status.item() == 0
+
+
+def test_second_derivatives_are_refused():
+    """Neither move's gradient is differentiable: a second derivative is an error, not a lost term."""
+    order = ExpertOrder(12, K, 0, E).route(randn(12, E), torch.zeros(E, device="cuda"))
+    x, w = randn(12, H).requires_grad_(), torch.rand((12, K), device="cuda").requires_grad_()
+    rows = permute_rows(x, order)
+    (dx,) = torch.autograd.grad(rows.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        dx.square().sum().backward()
+    y = randn(order.capacity, H).requires_grad_()
+    dy, dw = torch.autograd.grad(unpermute_rows(y, w, order).square().sum(), (y, w), create_graph=True)
+    for g in (dy, dw):
+        with pytest.raises(RuntimeError, match="differentiate twice"):
+            g.sum().backward(retain_graph=True)

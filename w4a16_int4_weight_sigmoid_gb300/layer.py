@@ -13,6 +13,7 @@ import contextlib
 
 import numpy as np
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import chord
 
@@ -131,6 +132,7 @@ class _Permute(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         dout = _unit_columns(dout)
         dx = torch.empty((ctx.order.M, dout.shape[1]), dtype=dout.dtype, device=dout.device)
@@ -148,6 +150,7 @@ class _Unpermute(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         y, weights = ctx.saved_tensors
         o, dout = ctx.order, _unit_columns(dout)
@@ -158,13 +161,14 @@ class _Unpermute(torch.autograd.Function):
 
 
 def permute_rows(x, order: ExpertOrder):
-    """x [M, H] -> rows [order.capacity, H] in expert order, zeros elsewhere; differentiable."""
+    """x [M, H] -> rows [order.capacity, H] in expert order, zeros elsewhere; differentiable once
+    (a second derivative raises)."""
     return _Permute.apply(x, order)
 
 
 def unpermute_rows(y, weights, order: ExpertOrder):
     """The weighted sum of rows y [order.capacity, H] back to tokens [M, H]; differentiable
-    in y and in weights FP32 [M, topk]."""
+    once in y and in weights FP32 [M, topk] (a second derivative raises)."""
     if y.shape[0] != order.capacity:
         raise ValueError(f"y must hold the {order.capacity} rows of its order, got {y.shape[0]}")
     return _Unpermute.apply(y, weights, order)
