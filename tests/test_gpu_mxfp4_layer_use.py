@@ -154,3 +154,45 @@ def test_second_derivatives_are_refused():
     for g in (dy, dw):
         with pytest.raises(RuntimeError, match="differentiate twice"):
             g.sum().backward(retain_graph=True)
+
+
+def test_routing_again_before_backward_is_noticed():
+    """The gradients belong to the routing of their forward; a second route() into the same
+    order makes backward an error.  Forwards of both routings keep their own when each has its order."""
+    x = randn(12, H).requires_grad_()
+    bias = torch.zeros(E, device="cuda")
+    order = ExpertOrder(12, K, 0, E).route(randn(12, E, seed=1), bias)
+    w = torch.rand((12, K), device="cuda").requires_grad_()
+    rows = permute_rows(x, order)
+    order.route(randn(12, E, seed=2), bias)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        rows.sum().backward()
+    out = unpermute_rows(permute_rows(x, order).detach().requires_grad_(), w, order)
+    order.route(randn(12, E, seed=3), bias)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    # weights taken from the order are overwritten as well
+    scale = torch.ones(K, device="cuda", requires_grad=True)
+    weights = order.topk_weights * scale
+    order.route(randn(12, E, seed=4), bias)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        weights.sum().backward()
+    # once more, in order
+    unpermute_rows(permute_rows(x, order), w, order).sum().backward()
+    here = order.sorted_positions.reshape(12, K) >= 0
+    assert torch.allclose(x.grad, (w.detach() * here).sum(1, keepdim=True).expand(12, H))
+
+
+def test_an_order_made_in_inference_mode():
+    """Its tensors carry no versions and cannot be saved; routing it, moving rows and their
+    gradients work all the same."""
+    with torch.inference_mode():
+        order = ExpertOrder(12, K, 0, E).route(randn(12, E), torch.zeros(E, device="cuda"))
+        layer = make_layer()
+        a = layer.forward(*inputs(12))
+    order.route(randn(12, E), torch.zeros(E, device="cuda"))
+    b = layer.forward(*inputs(12))
+    assert torch.equal(a, b)
+    x, w = randn(12, H).requires_grad_(), torch.full((12, K), 0.5, device="cuda", requires_grad=True)
+    unpermute_rows(permute_rows(x, order), w, order).sum().backward()
+    assert (x.grad == 1).all()

@@ -84,7 +84,8 @@ class W4A16MoELayer:
 
 class ExpertOrder:
     """The aligned order of the assignments of M tokens to topk of E_total experts, on
-    one shard (local experts [expert_begin, +E_local)); route() fills it.
+    one shard (local experts [expert_begin, +E_local)); route() fills it, and may fill it
+    anew once the gradients of what used it have been taken (before that, they raise).
 
     topk_weights [M, topk] FP32 and topk_ids [M, topk]; sorted_token_ids [capacity],
     sorted_positions [M * topk], num_tokens_post_padded [1], expert_counts [E_local]
@@ -113,6 +114,11 @@ class ExpertOrder:
                                     self.topk_weights, self.topk_ids, self.sorted_token_ids, self.expert_ids,
                                     self.num_tokens_post_padded, self.expert_counts, self.expert_offsets,
                                     self.sorted_positions, self._ws, stream=stream)
+        # written through raw pointers: autograd is told, as of any write in place
+        torch.autograd.graph.increment_version(
+            [t for t in (self.topk_weights, self.topk_ids, self.sorted_token_ids, self.sorted_positions,
+                         self.expert_ids, self.num_tokens_post_padded, self.expert_counts, self.expert_offsets)
+             if not t.is_inference()])
         return self
 
 
@@ -121,10 +127,18 @@ def _unit_columns(g):
     return g if g.stride(1) == 1 or g.shape[1] == 1 else g.contiguous()
 
 
+# The maps are saved like any tensor, so that a backward after route() has filled the order
+# anew is an error instead of the gradient of another routing.
+def _save(ctx, *tensors):
+    copy = not torch.is_inference_mode_enabled()   # tensors made in that mode cannot be saved
+    ctx.save_for_backward(*(t.clone() if copy and t.is_inference() else t for t in tensors))
+
+
 class _Permute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, order):
-        ctx.order = order
+        ctx.M, ctx.topk = order.M, order.topk
+        _save(ctx, order.sorted_positions)
         # rows past the padded total are not written by the call: zeros
         out = torch.zeros((order.capacity, x.shape[1]), dtype=x.dtype, device=x.device)
         chord.chord_moe_permute(x, order.sorted_positions, order.sorted_token_ids, order.num_tokens_post_padded,
@@ -134,17 +148,17 @@ class _Permute(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
+        positions, = ctx.saved_tensors
         dout = _unit_columns(dout)
-        dx = torch.empty((ctx.order.M, dout.shape[1]), dtype=dout.dtype, device=dout.device)
-        chord.chord_moe_permute_backward(dout, ctx.order.sorted_positions, ctx.order.topk, dx)
+        dx = torch.empty((ctx.M, dout.shape[1]), dtype=dout.dtype, device=dout.device)
+        chord.chord_moe_permute_backward(dout, positions, ctx.topk, dx)
         return dx, None
 
 
 class _Unpermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, order):
-        ctx.order = order
-        ctx.save_for_backward(y, weights)
+        _save(ctx, y, weights, order.sorted_positions, order.sorted_token_ids, order.num_tokens_post_padded)
         out = torch.empty((order.M, y.shape[1]), dtype=y.dtype, device=y.device)
         chord.chord_moe_unpermute(y, weights, order.sorted_positions, out)
         return out
@@ -152,11 +166,10 @@ class _Unpermute(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        y, weights = ctx.saved_tensors
-        o, dout = ctx.order, _unit_columns(dout)
+        y, weights, positions, token_ids, total = ctx.saved_tensors
+        dout = _unit_columns(dout)
         dy, dw = torch.zeros_like(y, memory_format=torch.contiguous_format), torch.empty_like(weights)
-        chord.chord_moe_unpermute_backward(dout, y, weights, o.sorted_positions, o.sorted_token_ids,
-                                           o.num_tokens_post_padded, dy, dw)
+        chord.chord_moe_unpermute_backward(dout, y, weights, positions, token_ids, total, dy, dw)
         return dy, dw, None
 
 
