@@ -196,3 +196,15 @@ def test_an_order_made_in_inference_mode():
     x, w = randn(12, H).requires_grad_(), torch.full((12, K), 0.5, device="cuda", requires_grad=True)
     unpermute_rows(permute_rows(x, order), w, order).sum().backward()
     assert (x.grad == 1).all()
+
+
+def test_an_order_of_no_tokens():
+    """A rank without tokens routes, moves and differentiates nothing."""
+    order = ExpertOrder(0, K, 0, E).route(torch.empty((0, E), device="cuda"), torch.zeros(E, device="cuda"))
+    assert order.num_tokens_post_padded.item() == 0
+    assert not order.expert_counts.any() and not order.expert_offsets.any()
+    x = torch.empty((0, H), device="cuda", requires_grad=True)
+    w = torch.empty((0, K), device="cuda", requires_grad=True)
+    out = unpermute_rows(permute_rows(x, order), w, order)
+    out.sum().backward()
+    assert out.shape == (0, H) and x.grad.shape == (0, H) and w.grad.shape == (0, K)

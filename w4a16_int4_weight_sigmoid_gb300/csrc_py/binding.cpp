@@ -49,7 +49,8 @@ struct Rows {
   Rows(PyObject* o, const char* name) {
     const at::Tensor& t = tensor(o, name);
     dtype = dtype_code(t, name);
-    if (t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1))
+    // (strides mean nothing without elements)
+    if (t.dim() != 2 || (t.size(0) > 0 && t.size(1) > 1 && t.stride(1) != 1))
       raise(PyExc_ValueError, "%s must be a matrix of rows with unit column stride", name);
     p = t.data_ptr();
     n = t.size(0);

@@ -110,6 +110,11 @@ class ExpertOrder:
         """Top-k routing of logits [M, E_total] and the order, on the device."""
         if logits.dim() != 2 or logits.shape[0] != self.M:
             raise ValueError(f"logits must be [{self.M}, E_total] for this order, got {list(logits.shape)}")
+        if self.M == 0:   # arrays without elements have no address to give
+            with _on_stream(stream):
+                for t in (self.num_tokens_post_padded, self.expert_counts, self.expert_offsets):
+                    t.zero_()
+            return self
         chord.chord_moe_route_align(logits, bias, self.topk, self.expert_begin, self.E_local, self.block_m,
                                     self.topk_weights, self.topk_ids, self.sorted_token_ids, self.expert_ids,
                                     self.num_tokens_post_padded, self.expert_counts, self.expert_offsets,
