@@ -208,3 +208,21 @@ def test_an_order_of_no_tokens():
     out = unpermute_rows(permute_rows(x, order), w, order)
     out.sum().backward()
     assert out.shape == (0, H) and x.grad.shape == (0, H) and w.grad.shape == (0, K)
+
+
+def test_an_order_dropped_while_its_stream_is_busy():
+    """Its memory is handed out again only when the stream that routes it is done."""
+    logits, bias = randn(1000, E), torch.zeros(E, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    order = ExpertOrder(1000, K, 0, E)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)               # about 50 ms
+    order.route(logits, bias, stream=s)
+    at = {order.sorted_token_ids.data_ptr(), order.sorted_positions.data_ptr(), order.topk_ids.data_ptr()}
+    sizes = [order.sorted_token_ids.numel(), order.sorted_positions.numel(), order.topk_ids.numel()]
+    del order
+    new = [torch.empty(n, dtype=torch.int32, device="cuda") for n in sizes for _ in range(4)]
+    assert not s.query()                              # it was busy all the while
+    assert not at & {t.data_ptr() for t in new}
+    s.synchronize()

@@ -105,11 +105,22 @@ class ExpertOrder:
         self.expert_offsets = torch.empty(E_local + 1, **i32)
         nbytes = chord.chord_moe_align_workspace_bytes(M, topk, E_local)
         self._ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        self._streams = {None}   # streams that its memory may be in use on
+
+    def _arrays(self):
+        return (self.topk_weights, self.topk_ids, self.sorted_token_ids, self.sorted_positions, self.expert_ids,
+                self.num_tokens_post_padded, self.expert_counts, self.expert_offsets)
 
     def route(self, logits, bias, stream=None):
-        """Top-k routing of logits [M, E_total] and the order, on the device."""
+        """Top-k routing of logits [M, E_total] and the order, on the device.  The order's memory
+        is of the stream that was current when it was made: a call on another `stream` follows
+        that one's work, and with a raw handle the order is kept until the call has run."""
         if logits.dim() != 2 or logits.shape[0] != self.M:
             raise ValueError(f"logits must be [{self.M}, E_total] for this order, got {list(logits.shape)}")
+        if stream not in self._streams and isinstance(stream, torch.cuda.Stream):
+            for t in (*self._arrays(), *([] if self._ws is None else [self._ws])):
+                t.record_stream(stream)
+            self._streams.add(stream)
         if self.M == 0:   # arrays without elements have no address to give
             with _on_stream(stream):
                 for t in (self.num_tokens_post_padded, self.expert_counts, self.expert_offsets):
@@ -120,10 +131,7 @@ class ExpertOrder:
                                     self.num_tokens_post_padded, self.expert_counts, self.expert_offsets,
                                     self.sorted_positions, self._ws, stream=stream)
         # written through raw pointers: autograd is told, as of any write in place
-        torch.autograd.graph.increment_version(
-            [t for t in (self.topk_weights, self.topk_ids, self.sorted_token_ids, self.sorted_positions,
-                         self.expert_ids, self.num_tokens_post_padded, self.expert_counts, self.expert_offsets)
-             if not t.is_inference()])
+        torch.autograd.graph.increment_version([t for t in self._arrays() if not t.is_inference()])
         return self
 
 
