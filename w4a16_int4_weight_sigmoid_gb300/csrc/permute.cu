@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, kShiftCtas) permute_shift_kernel(Row
 // ---------------------------------------------------- weighted sum of rows
 // Warp (t, chunk): VPT accesses per lane of the token's local rows, kRows of
 // them in flight, added in increasing j.  A CTA's warps have four tokens (a
-// CTA per token took 12.0 us for 6521 rows of 272 values).
+// CTA per token took 12.0 us for 6521 rows of 272 values).  Chunks lie along the
+// grid's y, which ends at 65535, and its z.
 template <typename T, int B, int VPT, int kRows, bool kWeighted>
 __global__ void __launch_bounds__(kThreads) combine_kernel(RowArgs a) {
   constexpr int V = B / sizeof(T);
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(RowArgs a) {
     if (kWeighted) w = ld_ca(a.w + o);
   }
   uint32_t left = __ballot_sync(0xffffffffu, p >= 0 && p < a.rows);
-  const int nv = a.H / V, c0 = blockIdx.y * 32 * VPT + lane;
+  const int nv = a.H / V, c0 = (blockIdx.z * gridDim.y + blockIdx.y) * 32 * VPT + lane;
   float acc[VPT][V];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
@@ -407,11 +408,15 @@ cudaError_t launch_combine(const RowArgs& a, cudaStream_t st) {
   // eight rows in flight with few, four with many
   constexpr int kFew = B >= 16 ? 1 : 4, kMany = 2 * kFew;
   const int many = (nv + 32 * kMany - 1) / (32 * kMany), few = (nv + 32 * kFew - 1) / (32 * kFew);
+  auto grid = [&](int chunks) {
+    const int z = (chunks + 65534) / 65535;
+    return dim3(ctas, (chunks + z - 1) / z, z);
+  };
   if (static_cast<long long>(ctas) * many >= 4LL * sm_count())
     return launch_kernel(a.w ? combine_kernel<T, B, kMany, 4, true> : combine_kernel<T, B, kMany, 4, false>,
-                         dim3(ctas, many), dim3(kThreads), 0, st, true, a);
+                         grid(many), dim3(kThreads), 0, st, true, a);
   return launch_kernel(a.w ? combine_kernel<T, B, kFew, 8, true> : combine_kernel<T, B, kFew, 8, false>,
-                       dim3(ctas, few), dim3(kThreads), 0, st, true, a);
+                       grid(few), dim3(kThreads), 0, st, true, a);
 }
 
 template <typename T, int B>
