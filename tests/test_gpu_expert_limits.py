@@ -1,12 +1,14 @@
 """GPU tests of the rows in expert order and of the MXFP4 product at the ends of their
 ranges: the longest rows, gates far below zero, orders that are none, and launches whose
 CTAs walk many items.  Bounds as derived in test_gpu_expert_rows.py and test_gpu_mxfp4.py."""
+import numpy as np
 import pytest
 import torch
 
 from w4a16_int4_weight_sigmoid_gb300 import chord
 
 from gpu_util import ensure_lib
+from test_gpu_mxfp4 import LEVELS, Experts
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +53,38 @@ def test_the_longest_rows(name, H, off):
     assert torch.equal(dy[1], x[0] / 2) and torch.equal(dy[0], x[0] / 4)
     # integer terms whose partial sums stay far below 2^24: exact too
     assert torch.equal(dw[0].double(), (x.double() * y.double()).sum(1).flip(0))
+
+
+# ------------------------------------------------------- gates far below zero
+def encode(v):
+    """The code and the scale code that hold v exactly."""
+    for e in range(-4, 7):
+        if abs(v) / 2.0 ** e in LEVELS:
+            return int(np.nonzero(LEVELS == abs(v) / 2.0 ** e)[0][0]) | (8 if v < 0 else 0), 127 + e
+    raise ValueError(v)
+
+
+@pytest.mark.parametrize("K", [256, 4096])            # whole items, and items divided along K
+def test_gates_far_below_zero(K):
+    """silu(g) u with g from -82 to -100 and u = 6 * 2^120: small factors, ordinary results.
+
+    g and u are exact.  Of silu's own value, in units of it: exp(-|g|) from the fast
+    exponential within 2 + 1.173 |g| last places (CUDA's documented bound), the product with
+    g and the sum 1 + t half a place each, the fast quotient two, u's product a half: (6 + 1.173
+    |g|) 2^-23.  Below FP32's normal range roundings are of 2^-150 instead: one of exp(-|g|),
+    two of silu.  And BF16's rounding."""
+    third = [-6, -4, -3, -2, -1.5, -1, -0.5, 0, 0.5, 1, 2, 3, 4, 6, 8, 12]
+    n = len(third)
+    ex = Experts([1, 3], 8, 2 * n, K, 40)
+    ex.x.zero_()
+    ex.x[:, [5, 37, 69]] = 1.0                         # three blocks, so three terms of a gate
+    ex.code[:], ex.scale[:] = 0, 127
+    for i, v in enumerate(third):
+        for block, term in enumerate((-64, -24, -v)):
+            ex.code[:, i, 32 * block + 5], ex.scale[:, i, block] = encode(term)
+    ex.code[:, n:, 5], ex.scale[:, n:, 0] = 7, 127 + 120
+    g, u = -88.0 - np.array(third), LEVELS[7] * 2.0 ** 120
+    C = ex.product(True).double().cpu().numpy()[ex.pos]
+    silu = g / (1 + np.exp(-g))
+    rel = 2.0 ** -8 + (6 + 1.173 * np.abs(g)) * 2.0 ** -23 + 2.0 ** -150 * (1 / np.exp(g) + 2 / np.abs(silu))
+    assert (np.abs(C - silu * u) <= rel * np.abs(silu * u)).all(), C[0] / (silu * u)

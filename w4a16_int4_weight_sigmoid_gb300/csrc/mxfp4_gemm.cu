@@ -251,8 +251,11 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
   return r != 0;
 }
 
+// With the exponential of -|g|, whose value and divisor stay within range: the
+// divisor 1 + exp(-g) is past 2^126, where __fdividef gives 0, for g below -87.3.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  return __fdividef(g, 1.0f + __expf(-g)) * u;
+  const float t = __expf(-fabsf(g));
+  return __fdividef(g < 0.f ? g * t : g, 1.0f + t) * u;
 }
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   uint32_t r;
