@@ -478,8 +478,11 @@ int chord_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
  *                  After a call that recorded CHORD_ERR_TIMEOUT zero it again.
  *   dev_status     device int for errors found on the device (may be NULL):
  *                  a weights header that does not match the call, counts and
- *                  offsets that are no aligned order of `capacity` rows (such
- *                  an expert is skipped), a bounded wait that ran out
+ *                  offsets that are no aligned order of `capacity` rows (an
+ *                  expert whose rows are misaligned or past the capacity is
+ *                  skipped; where an expert's rows reach past
+ *                  expert_offsets[e + 1], or offsets descend, nothing is
+ *                  computed), a bounded wait that ran out
  * Counts are read on the device, so the call never waits for the host.
  * Results are the same from call to call.  E_local <= 1024.
  */

@@ -88,3 +88,58 @@ def test_gates_far_below_zero(K):
     silu = g / (1 + np.exp(-g))
     rel = 2.0 ** -8 + (6 + 1.173 * np.abs(g)) * 2.0 ** -23 + 2.0 ** -150 * (1 / np.exp(g) + 2 / np.abs(silu))
     assert (np.abs(C - silu * u) <= rel * np.abs(silu * u)).all(), C[0] / (silu * u)
+
+
+# --------------------------------------------------------- orders that are none
+@pytest.mark.parametrize("counts,offsets,written", [
+    ([3, 20, 5], [0, 16, 32, 48], [False] * 3),               # 16 + 20 ends past 32: the next expert's rows
+    ([17, 5, 5], [0, 0, 32, 48], [False] * 3),                # two experts at one place
+    ([3, 5, 5], [0, 32, 16, 48], [False] * 3),                # descending
+    ([3, 5, 5], [32, 16, 0, 48], [False] * 3),
+    ([3, 5, 5], [0, 16, 32, -8], [False] * 3),
+    ([3, 0, 5], [0, 1 << 20, 0, 48], [False] * 3),            # up and down again
+    ([3, -5, 5], [0, 32, 16, 48], [False] * 3),
+    ([3, 5, 40], [0, 16, 32, 48], [True, True, False]),       # the last expert past the end of the order
+    ([3, 5, 5], [0, 20, 32, 48], [True, False, True]),        # not a multiple of 8
+    ([3, -5, 5], [0, 16, 32, 48], [True, False, True]),
+    ([3, 2 ** 31 - 1, 5], [0, 16, 32, 48], [True, False, True]),
+])
+def test_counts_and_offsets_that_are_no_order(counts, offsets, written):
+    """An expert whose rows are misaligned or past the capacity is skipped; experts whose rows
+    overlap, and offsets that descend, stop the launch.  So the rows of all experts together
+    stay within the capacity, as the host assumes."""
+    ex = Experts([3, 5, 5], 16, 128, 256, 41)
+    good = ex.product(False)
+    packed, rows = ex.pack(False), ex.rows()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    C, status = torch.full_like(good, 7.0), i32([0])
+    ws = torch.zeros(chord.chord_mxfp4_moe_gemm_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    chord.chord_mxfp4_moe_gemm(rows, packed, 3, 128, 256, i32(counts), i32(offsets), ex.cap, chord.CHORD_EPI_STORE, C,
+                               ws, status)
+    assert status.item() == chord.CHORD_ERR_INVALID_ARG
+    touched = (C != 7.0).any(1).cpu()
+    for e, w in enumerate(written):
+        if w and offsets[e] == 16 * e:                        # an expert in its own place: its own values
+            at = slice(offsets[e], offsets[e] + counts[e])
+            assert torch.equal(C[at], good[at])
+    expect = torch.zeros(ex.cap, dtype=torch.bool)
+    for e, w in enumerate(written):
+        if w:
+            expect[offsets[e]:offsets[e] + counts[e]] = True
+    assert torch.equal(touched, expect)
+    # the counters are zero: a good call on the same workspace is right
+    status.zero_()
+    assert torch.equal(ex.product(False, packed, rows, ws, status), good) and status.item() == 0
+
+
+def test_many_experts_of_all_rows():
+    """1024 experts that each claim the whole capacity, each of them within it."""
+    n, cap, N, K = 1024, 256, 8, 32
+    ex = Experts([cap], 16, N, K, 42)
+    ex.code, ex.scale = ex.code.repeat(n, 0), ex.scale.repeat(n, 0)
+    ex.E = n
+    ex.d_counts = torch.full((n,), cap, dtype=torch.int32, device="cuda")
+    ex.d_offsets = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    ex.d_offsets[n] = cap
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert (ex.product(False, status=status) == 7.0).all() and status.item() == chord.CHORD_ERR_INVALID_ARG

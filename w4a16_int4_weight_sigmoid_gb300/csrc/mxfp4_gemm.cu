@@ -67,6 +67,7 @@ constexpr int kThreads = 32 * (kItemWarp + 1);
 constexpr int kItemSlots = 8;
 constexpr int kItemReaders = 1 + kPair + 1 + kEpiWarps;   // copies, MMAs, scales, epilogue
 constexpr int kMaxExperts = 1024;
+constexpr int kNoOrder = 1 << 16;      // for the largest row tile: the experts' rows overlap
 // stage: weight tiles with their scales | rows
 constexpr int kBOff = kPair * kMxUnitBytes;
 __host__ __device__ constexpr int stage_bytes(int tok) { return kBOff + tok * kMxRowBytes; }
@@ -433,9 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
     const int e = tid * per + i;
     if (e >= a.E) break;
     int cnt = ld_ca(a.counts + e);
-    const int off = ld_ca(a.offsets + e);
-    if (cnt < 0 || off < 0 || off % 8 != 0 || cnt > a.capacity || off > a.capacity - cnt) {
+    const int off = ld_ca(a.offsets + e), next = ld_ca(a.offsets + e + 1);
+    const bool alone = cnt >= 0 && off >= 0 && off % 8 == 0 && cnt <= a.capacity && off <= a.capacity - cnt;
+    // Experts that end before the next one begins have disjoint rows, so that
+    // the items number at most what the host has checked.
+    if (!alone || off + cnt > next) {
       set_status(a.status, CHORD_ERR_INVALID_ARG);   // not an aligned order of `capacity` rows
+      if (alone || off > next) most = kNoOrder;
       cnt = 0;
     }
     prefix[e] = mine;
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   Plan plan;
   plan.prefix = prefix, plan.cnts = a.counts, plan.offs = a.offsets;
   plan.E = a.E, plan.n_tiles = a.n_tiles, plan.units = units, plan.max_tok = a.max_tok;
-  plan.items = hdr_ok ? prefix[a.E] : 0;
+  plan.items = hdr_ok && tok <= kMaxTok ? prefix[a.E] : 0;
   plan.cut = plan.items % ctas;
   // The items that are left over when each CTA has had the same number are
   // divided where that leaves every CTA one part at most; otherwise they are
