@@ -468,7 +468,7 @@ int chord_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t 
  *                  row operand: token t to its rows sorted_positions[t, :]
  *                  (each token is quantised once), or, with sorted_positions
  *                  NULL, row r of x to row r for r < num_tokens_post_padded
- *                  (a previous product's C).  `rows` holds
+ *                  (a previous product's C; topk is not read).  `rows` holds
  *                  chord_mxfp4_rows_bytes(capacity, K) bytes, 16-byte aligned,
  *                  laid out for this capacity, which the product is given too;
  *                  num_tokens_post_padded may be NULL with positions.

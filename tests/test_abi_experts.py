@@ -106,3 +106,14 @@ def test_extension_is_built_and_refuses_host_tensors(L):
         chord.chord_mxfp4_quantize([1, 2], i, i)
     with pytest.raises(ValueError, match="CUDA"):
         chord.chord_mxfp4_dequantize(i, i, t)
+
+
+def test_rows_without_positions_have_no_topk(L):
+    """topk is not read when row r of x is row r of the order; the other checks hold."""
+    f = lambda k, M=1 << 27, cap=0, pos=None, total=P: L.chord_mxfp4_quantize_rows(P, 0, 64, M, 64, pos, k, total, cap,
+                                                                                   P, 1 << 40, None)
+    assert f(0) == 0 and f(33) == 0 and f(16) == 0
+    refused(L, ARG, "topk", f(0, pos=P))
+    refused(L, ARG, "M*topk", f(16, pos=P))
+    refused(L, ARG, "M=-1", f(0, M=-1))
+    refused(L, ARG, "null", f(0, M=4, cap=64, total=None))

@@ -138,6 +138,7 @@ size_t chord_mxfp4_rows_bytes(size_t capacity, int K) {
 int chord_mxfp4_quantize_rows(const void* x, int dtype, int64_t x_stride, int M, int K,
                               const int32_t* sorted_positions, int topk, const int32_t* num_tokens_post_padded,
                               size_t capacity, void* rows, size_t rows_bytes, void* stream) {
+  if (!sorted_positions) topk = 1;   // row r of x is row r of the order
   int rc = check_rows(dtype, M, topk, K, capacity);
   if (rc) return rc;
   if ((rc = check_mx("quantize_rows", K))) return rc;
