@@ -23,6 +23,7 @@ int fail(int code, const char* fmt, ...) {
 }
 
 int cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();   // reported here: not to be taken for the next call's
   return fail(CHORD_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
