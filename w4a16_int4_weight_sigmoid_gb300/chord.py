@@ -175,10 +175,10 @@ def _check_operands(A, C, K: int, N: int, epilogue: int, a_rows: int, c_rows: in
         raise ValueError(f"{what}: C holds {C.numel()} values, needs {c_rows} rows of {ncols}")
 
 
-def _check_holds(what: str, **need):
-    """Each tensor given as name=(tensor, values) holds at least that many values: the C ABI
+def _check_holds(what: str, *need):
+    """Each tensor given as (name, tensor, values) holds at least that many values: the C ABI
     writes or reads them through raw pointers.  Raises ValueError before anything runs."""
-    for name, (t, n) in need.items():
+    for name, t, n in need:
         if isinstance(t, torch.Tensor) and t.numel() < n:
             raise ValueError(f"{what}: {name} holds {t.numel()} values, needs {n}")
 
@@ -251,11 +251,14 @@ def chord_moe_route_align(logits, bias, topk: int, expert_begin: int, E_local: i
     """chord_moe_route then chord_moe_align in one call (one launch for small M)."""
     M, E_total = logits.shape
     n = M * topk
-    blocks = chord_moe_align_capacity(M, topk, E_local, block_m) // max(block_m, 1)
-    _check_holds("chord_moe_route_align", bias=(bias, E_total), topk_weights=(topk_weights, n), topk_ids=(topk_ids, n),
-                 expert_ids=(expert_ids, blocks), num_tokens_post_padded=(num_tokens_post_padded, 1),
-                 expert_counts=(expert_counts, E_local), expert_offsets=(expert_offsets, E_local + 1),
-                 sorted_positions=(sorted_positions, n))
+    _check_holds("chord_moe_route_align", ("bias", bias, E_total), ("topk_weights", topk_weights, n),
+                 ("topk_ids", topk_ids, n), ("num_tokens_post_padded", num_tokens_post_padded, 1),
+                 ("expert_counts", expert_counts, E_local), ("expert_offsets", expert_offsets, E_local + 1),
+                 ("sorted_positions", sorted_positions, n))
+    if isinstance(expert_ids, torch.Tensor) and expert_ids.numel() * block_m < sorted_token_ids.numel():
+        # fewer blocks than sorted_token_ids has room for: as many as M tokens can fill will do
+        blocks = chord_moe_align_capacity(M, topk, E_local, block_m) // max(block_m, 1)
+        _check_holds("chord_moe_route_align", ("expert_ids", expert_ids, blocks))
     i32 = torch.int32
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().chord_moe_route_align(

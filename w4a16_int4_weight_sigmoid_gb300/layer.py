@@ -105,11 +105,17 @@ class ExpertOrder:
         self.expert_offsets = torch.empty(E_local + 1, **i32)
         nbytes = chord.chord_moe_align_workspace_bytes(M, topk, E_local)
         self._ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        self._arrays = (self.topk_weights, self.topk_ids, self.sorted_token_ids, self.sorted_positions,
+                        self.expert_ids, self.num_tokens_post_padded, self.expert_counts, self.expert_offsets)
+        # tensors made in inference mode have no versions, and cannot be saved outside it
+        self._versioned = () if self.topk_weights.is_inference() else self._arrays
         self._streams = {None}   # streams that its memory may be in use on
 
-    def _arrays(self):
-        return (self.topk_weights, self.topk_ids, self.sorted_token_ids, self.sorted_positions, self.expert_ids,
-                self.num_tokens_post_padded, self.expert_counts, self.expert_offsets)
+    def _saved(self, *arrays):
+        """Arrays of the order as a backward pass can keep them."""
+        if self._versioned or torch.is_inference_mode_enabled():
+            return arrays
+        return [t.clone() for t in arrays]
 
     def route(self, logits, bias, stream=None):
         """Top-k routing of logits [M, E_total] and the order, on the device.  The order's memory
@@ -118,7 +124,7 @@ class ExpertOrder:
         if logits.dim() != 2 or logits.shape[0] != self.M:
             raise ValueError(f"logits must be [{self.M}, E_total] for this order, got {list(logits.shape)}")
         if stream not in self._streams and isinstance(stream, torch.cuda.Stream):
-            for t in (*self._arrays(), *([] if self._ws is None else [self._ws])):
+            for t in (*self._arrays, *([] if self._ws is None else [self._ws])):
                 t.record_stream(stream)
             self._streams.add(stream)
         if self.M == 0:   # arrays without elements have no address to give
@@ -131,7 +137,7 @@ class ExpertOrder:
                                     self.num_tokens_post_padded, self.expert_counts, self.expert_offsets,
                                     self.sorted_positions, self._ws, stream=stream)
         # written through raw pointers: autograd is told, as of any write in place
-        torch.autograd.graph.increment_version([t for t in self._arrays() if not t.is_inference()])
+        torch.autograd.graph.increment_version(self._versioned)
         return self
 
 
@@ -140,18 +146,20 @@ def _unit_columns(g):
     return g if g.stride(1) == 1 or g.shape[1] == 1 else g.contiguous()
 
 
+def _once(backward):
+    """once_differentiable, but only where a graph of the gradient is asked for: its wrapping
+    takes the host 2 us a call."""
+    checked = once_differentiable(backward)
+    return lambda ctx, *grads: (checked if torch.is_grad_enabled() else backward)(ctx, *grads)
+
+
 # The maps are saved like any tensor, so that a backward after route() has filled the order
 # anew is an error instead of the gradient of another routing.
-def _save(ctx, *tensors):
-    copy = not torch.is_inference_mode_enabled()   # tensors made in that mode cannot be saved
-    ctx.save_for_backward(*(t.clone() if copy and t.is_inference() else t for t in tensors))
-
-
 class _Permute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, order):
         ctx.M, ctx.topk = order.M, order.topk
-        _save(ctx, order.sorted_positions)
+        ctx.save_for_backward(*order._saved(order.sorted_positions))
         # rows past the padded total are not written by the call: zeros
         out = torch.zeros((order.capacity, x.shape[1]), dtype=x.dtype, device=x.device)
         chord.chord_moe_permute(x, order.sorted_positions, order.sorted_token_ids, order.num_tokens_post_padded,
@@ -159,7 +167,7 @@ class _Permute(torch.autograd.Function):
         return out
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dout):
         positions, = ctx.saved_tensors
         dout = _unit_columns(dout)
@@ -171,13 +179,14 @@ class _Permute(torch.autograd.Function):
 class _Unpermute(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, order):
-        _save(ctx, y, weights, order.sorted_positions, order.sorted_token_ids, order.num_tokens_post_padded)
+        ctx.save_for_backward(y, weights, *order._saved(order.sorted_positions, order.sorted_token_ids,
+                                                       order.num_tokens_post_padded))
         out = torch.empty((order.M, y.shape[1]), dtype=y.dtype, device=y.device)
         chord.chord_moe_unpermute(y, weights, order.sorted_positions, out)
         return out
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dout):
         y, weights, positions, token_ids, total = ctx.saved_tensors
         dout = _unit_columns(dout)
