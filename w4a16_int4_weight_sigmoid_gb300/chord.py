@@ -209,8 +209,8 @@ def chord_version() -> int:
 
 
 def chord_debug_force_timeout(enable: bool) -> None:
-    """Test hook: later register-MMA GEMM launches withhold their work items,
-    so their consumers' waits run out (CHORD_ERR_TIMEOUT, nothing computed)."""
+    """Test hook: later launches of the register-MMA GEMM and of the MXFP4 product withhold
+    their work items, so their consumers' waits run out (CHORD_ERR_TIMEOUT, nothing computed)."""
     _check(lib().chord_debug_force_timeout(int(bool(enable))))
 
 

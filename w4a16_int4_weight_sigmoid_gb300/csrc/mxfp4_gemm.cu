@@ -38,9 +38,11 @@
 //     1600 cycles, as long as a short item's work);
 //   * stages and accumulators are laid out for the launch's largest row tile,
 //     which every CTA finds from the counts: decoding has five stages and four
-//     accumulators, a full tile three stages and one accumulator.
+//     accumulators, a full tile three stages and one accumulator.  One expert
+//     with many rows so sets the layout for the small items too, and keeps them
+//     from being divided along K.
 // Measured (kernel alone): 64 tokens on 48 of 384 experts, N 4096, K 7168: 85
-// us, 6.1 TB/s of DRAM, its bound; 8192 tokens: 136 us, DRAM at 5.8 TB/s and
+// us, 6.1 TB/s of DRAM, its bound; 8192 tokens: 137 us, DRAM at 5.8 TB/s and
 // exposed epilogues; 16384 rows of 8 experts: 177 us, 5.4 PFLOP/s: 54 bytes a
 // cycle into each SM, of about 64 that its port takes (tensor pipe 56 %
 // busy); one token, N 512: 8.7 us, latency.
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) mxfp4_gemm_kernel(MxArgs a) {
   __syncthreads();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, tmem_base_s, 0);
   tok = __shfl_sync(0xffffffffu, tok, 0);
-  const int units = mx_units(a.K), ctas = gridDim.x, cta = blockIdx.x;
+  const int units = mx_units(a.K), ctas = gridDim.x;
   Plan plan;
   plan.prefix = prefix, plan.cnts = a.counts, plan.offs = a.offsets;
   plan.E = a.E, plan.n_tiles = a.n_tiles, plan.units = units, plan.max_tok = a.max_tok;
