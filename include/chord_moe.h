@@ -498,6 +498,45 @@ int chord_mxfp4_moe_gemm(const void* rows, size_t rows_bytes, const void* packed
                          const int32_t* expert_counts, const int32_t* expert_offsets, size_t capacity, int epilogue,
                          chord_bf16* C, void* workspace, size_t ws_bytes, int* dev_status, void* stream);
 
+/* ------------------------------------- the experts' product in 16 bits
+ * For callers that train the experts between chord_moe_permute and
+ * chord_moe_unpermute, or decode with 16-bit weights.  Expert e's rows are the
+ * expert_counts[e] rows from expert_offsets[e] on: any number of rows, none
+ * too, from any row on, an expert's last before the next one's first
+ * (chord_moe_align's order is one; padding is not needed).
+ *   gemm    out[r, n] = sum_k x[r, k] w[e, n, k]                  transpose_w 0
+ *           out[r, k] = sum_n x[r, n] w[e, n, k]                  transpose_w 1
+ *           (the second is the gradient of the first one's x, with dout for x)
+ *   wgrad   dw[e, n, k] = sum over e's rows of dout[r, n] x[r, k]; zeros for
+ *           an expert without rows
+ * x, w, out and dout are BF16 or FP16 (`dtype`), products are summed in FP32
+ * and rounded once; dw is of `dtype` or FP32 (`dw_dtype`), contiguous.  Rows
+ * of out that are no expert's are not written, and rows that are no expert's
+ * reach no result, whatever they hold.
+ *   N, K       multiples of 8 (16-byte accesses), up to 2^20
+ *   *_stride   in elements, multiples of 8; rows do not overlap.  Bases are
+ *              16-byte aligned
+ *   capacity   rows of x, dout and out
+ *   workspace  chord_expert_gemm_workspace_bytes() bytes, 16-byte aligned,
+ *              zeroed once when allocated; every call leaves its counters
+ *              zero.  Calls that may overlap need their own.  After a call
+ *              that recorded CHORD_ERR_TIMEOUT zero it again.
+ *   dev_status device int for errors found on the device (may be NULL):
+ *              CHORD_ERR_INVALID_ARG where counts and offsets are no such
+ *              order of `capacity` rows (nothing is computed then), a bounded
+ *              wait that ran out
+ * Counts are read on the device, so the call never waits for the host.
+ * Results are the same from call to call.  E_local <= 1024.
+ */
+size_t chord_expert_gemm_workspace_bytes(void);
+int chord_expert_gemm(const void* x, int dtype, int64_t x_stride, const void* w, int64_t w_stride,
+                      int64_t w_expert_stride, int E_local, int N, int K, int transpose_w,
+                      const int32_t* expert_counts, const int32_t* expert_offsets, size_t capacity, void* out,
+                      int64_t out_stride, void* workspace, size_t ws_bytes, int* dev_status, void* stream);
+int chord_expert_wgrad(const void* dout, const void* x, int dtype, int64_t dout_stride, int64_t x_stride, int E_local,
+                       int N, int K, const int32_t* expert_counts, const int32_t* expert_offsets, size_t capacity,
+                       void* dw, int dw_dtype, void* workspace, size_t ws_bytes, int* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,134 @@
+"""The experts' product in 16 bits and its weights' gradient.
+
+Operands are small integers, so that every product and every partial sum is
+exact in FP32 whatever the order of the sum, and the result is the exact sum
+rounded once: compared bit for bit with the 64-bit product.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+LEFT = 77.0          # what rows that are not written hold
+
+
+def order(counts, gaps=None):
+    """Counts and offsets of experts whose rows follow one another after `gaps` rows each."""
+    gaps = gaps or [0] * len(counts)
+    offsets, at = [], 0
+    for c, g in zip(counts, gaps):
+        at += g
+        offsets.append(at)
+        at += c
+    i32 = dict(dtype=torch.int32, device="cuda")
+    return torch.tensor(counts, **i32), torch.tensor(offsets + [at], **i32), at
+
+
+def integers(g, *shape, dtype, most=2):
+    return torch.randint(-most, most + 1, shape, generator=g, device="cuda").to(dtype)
+
+
+def rows_of(counts, offsets):
+    """A mask of the rows that are an expert's."""
+    c, o = counts.tolist(), offsets.tolist()
+    return [(e, slice(o[e], o[e] + c[e])) for e in range(len(c)) if c[e]]
+
+
+def workspace():
+    from w4a16_int4_weight_sigmoid_gb300 import chord
+    return torch.zeros(chord.chord_expert_gemm_workspace_bytes(), dtype=torch.uint8, device="cuda")
+
+
+def product(x, w, counts, offsets, transpose, out=None):
+    from w4a16_int4_weight_sigmoid_gb300 import chord
+    E, N, K = w.shape
+    if out is None:
+        out = torch.full((x.shape[0], K if transpose else N), LEFT, dtype=x.dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    chord.chord_expert_gemm(x, w, counts, offsets, out, workspace(), transpose, status)
+    assert status.item() == 0
+    return out
+
+
+def expected_product(x, w, counts, offsets, transpose):
+    E, N, K = w.shape
+    out = torch.full((x.shape[0], K if transpose else N), LEFT, dtype=x.dtype, device="cuda")
+    for e, at in rows_of(counts, offsets):
+        out[at] = (x[at].double() @ (w[e].double() if transpose else w[e].double().T)).to(x.dtype)
+    return out
+
+
+def check_product(counts, K, N, transpose, dtype, gaps=None, extra=0, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    c, o, rows = order(counts, gaps)
+    inner = N if transpose else K
+    x = torch.full((rows + extra, inner), float("nan"), dtype=dtype, device="cuda")
+    for _, at in rows_of(c, o):
+        x[at] = integers(g, at.stop - at.start, inner, dtype=dtype)
+    w = integers(g, len(counts), N, K, dtype=dtype)
+    got = product(x, w, c, o, transpose)
+    assert torch.equal(got, expected_product(x, w, c, o, transpose))
+
+
+SHAPES = [
+    ([5], 64, 64),                        # one box of the contraction
+    ([1], 8, 8),                          # the smallest
+    ([32], 64, 256),                      # a whole tile
+    ([33, 0, 1], 72, 264),                # tiles end behind the tensors' edges
+    ([256, 257, 31], 200, 520),           # one and two row tiles
+    ([0, 0, 3, 0, 700], 640, 328),        # more boxes than stages
+    ([2000], 136, 600),                   # eight row tiles
+    ([2305, 7], 72, 1032),                # groups of row tiles
+    ([1] * 40, 256, 512),                 # decoding
+]
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("counts,K,N", SHAPES)
+def test_product(counts, K, N, transpose, dtype):
+    check_product(counts, K, N, transpose, dtype)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_product_rows_between_experts_are_left(transpose):
+    check_product([17, 0, 260, 1], 128, 264, transpose, BF16, gaps=[3, 7, 1, 64], extra=9)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_product_many_experts(transpose):
+    check_product([i % 3 for i in range(1024)], 64, 72, transpose, BF16)
+
+
+def wgrad(dout, x, counts, offsets, out_dtype):
+    from w4a16_int4_weight_sigmoid_gb300 import chord
+    dw = torch.full((counts.numel(), dout.shape[1], x.shape[1]), LEFT, dtype=out_dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    chord.chord_expert_wgrad(dout, x, counts, offsets, dw, workspace(), status)
+    assert status.item() == 0
+    return dw
+
+
+def check_wgrad(counts, K, N, dtype, out_dtype, gaps=None, extra=0, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    c, o, rows = order(counts, gaps)
+    dout = torch.full((rows + extra, N), float("nan"), dtype=dtype, device="cuda")
+    x = torch.full((rows + extra, K), float("nan"), dtype=dtype, device="cuda")
+    want = torch.zeros((len(counts), N, K), dtype=out_dtype, device="cuda")
+    for e, at in rows_of(c, o):
+        n = at.stop - at.start
+        dout[at], x[at] = integers(g, n, N, dtype=dtype), integers(g, n, K, dtype=dtype)
+        want[e] = (dout[at].double().T @ x[at].double()).to(out_dtype)
+    assert torch.equal(wgrad(dout, x, c, o, out_dtype), want)
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [(BF16, BF16), (FP16, FP16), (BF16, FP32), (FP16, FP32)])
+@pytest.mark.parametrize("counts,K,N", SHAPES)
+def test_weight_gradient(counts, K, N, dtype, out_dtype):
+    check_wgrad(counts, K, N, dtype, out_dtype)
+
+
+@pytest.mark.parametrize("count", [1, 15, 16, 17, 63, 64, 65, 80, 127, 128])
+def test_weight_gradient_ends_inside_a_box(count):
+    check_wgrad([count, 3, count], 136, 264, BF16, FP32, gaps=[1, 2, 0], extra=5)

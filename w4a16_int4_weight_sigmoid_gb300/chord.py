@@ -97,6 +97,9 @@ _SIGS = {
     "chord_mxfp4_prepack": (_I, [_P, _P, _I, _I, _I, _I, _P, _Z, _P]),
     "chord_mxfp4_moe_gemm_workspace_bytes": (_Z, []),
     "chord_mxfp4_moe_gemm": (_I, [_P, _Z, _P, _I, _I, _I, _P, _P, _Z, _I, _P, _P, _Z, _P, _P]),
+    "chord_expert_gemm_workspace_bytes": (_Z, []),
+    "chord_expert_gemm": (_I, [_P, _I, _L, _P, _L, _L, _I, _I, _I, _I, _P, _P, _Z, _P, _L, _P, _Z, _P, _P]),
+    "chord_expert_wgrad": (_I, [_P, _P, _I, _L, _L, _I, _I, _I, _P, _P, _Z, _P, _I, _P, _Z, _P, _P]),
 }
 
 _lib = None
@@ -511,5 +514,30 @@ def chord_mxfp4_moe_gemm(rows, packed_w, E_local: int, N: int, K: int, expert_co
     rc = (_ext_module or _ext()).moe_gemm(rows, packed_w, E_local, N, K, expert_counts, expert_offsets, capacity,
                                           epilogue, C, workspace, dev_status,
                                           None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+
+# --------------------------------------- the experts' product in 16 bits
+
+def chord_expert_gemm_workspace_bytes() -> int:
+    return lib().chord_expert_gemm_workspace_bytes()
+
+
+def chord_expert_gemm(x, w, expert_counts, expert_offsets, out, workspace, transpose_w: bool = False, dev_status=None,
+                      stream=None):
+    """out[r] = w[e] @ x[r] (transpose_w: w[e].T @ x[r]) for every expert e's rows r.  x and out are rows in expert
+    order, w [E, N, K], all BF16 or FP16; workspace: uint8 tensor of chord_expert_gemm_workspace_bytes() bytes,
+    zeroed once when allocated."""
+    rc = (_ext_module or _ext()).expert_gemm(x, w, expert_counts, expert_offsets, out, workspace, int(transpose_w),
+                                             dev_status, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def chord_expert_wgrad(dout, x, expert_counts, expert_offsets, dw, workspace, dev_status=None, stream=None):
+    """dw[e] = dout[rows of e].T @ x[rows of e], zeros for an expert without rows.  dout [capacity, N] and
+    x [capacity, K] of one type (BF16, FP16), dw contiguous [E, N, K] of that type or FP32."""
+    rc = (_ext_module or _ext()).expert_wgrad(dout, x, expert_counts, expert_offsets, dw, workspace, dev_status,
+                                              None if stream is None else _stream(stream))
     if rc:
         _check(rc)

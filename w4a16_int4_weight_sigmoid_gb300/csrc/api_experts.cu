@@ -42,6 +42,34 @@ int check_mx(const char* what, int K) {
   return CHORD_OK;
 }
 
+// The sizes and buffers that the 16-bit products share.
+int check_product(int dtype, int E, int N, int K, const int32_t* counts, const int32_t* offsets, size_t capacity,
+                  const void* ws, size_t ws_bytes) {
+  if (dtype != CHORD_DTYPE_BF16 && dtype != CHORD_DTYPE_FP16)
+    return fail(CHORD_ERR_INVALID_ARG, "dtype %d: the experts' 16-bit product takes BF16 and FP16", dtype);
+  if (E < 1 || E > 1024) return fail(CHORD_ERR_INVALID_ARG, "E_local=%d not in [1, 1024]", E);
+  if (N < 8 || N % 8 != 0 || N > (1 << 20) || K < 8 || K % 8 != 0 || K > (1 << 20))
+    return fail(CHORD_ERR_INVALID_ARG, "N=%d and K=%d must be positive multiples of 8 up to 2^20", N, K);
+  if (capacity > (1u << 30)) return fail(CHORD_ERR_INVALID_ARG, "%zu rows: too many", capacity);
+  if (!counts || !offsets) return fail(CHORD_ERR_INVALID_ARG, "null pointer: expert_counts or expert_offsets");
+  const size_t need = chord::expert_gemm_workspace_bytes();
+  if (!ws || ws_bytes < need)
+    return fail(CHORD_ERR_WORKSPACE_TOO_SMALL, "expert product workspace %zu < required %zu", ws_bytes, need);
+  if (!aligned16(ws)) return fail(CHORD_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  return CHORD_OK;
+}
+// A matrix that the products read or write in 16-byte parts, rows disjoint
+// (the stride of a single row means nothing).
+int check_rows16(const char* name, const void* p, int64_t& stride, int width, size_t rows) {
+  if (rows == 1) stride = width;
+  if (!p) return fail(CHORD_ERR_INVALID_ARG, "null pointer: %s", name);
+  if (!aligned16(p)) return fail(CHORD_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (stride < width || stride % 8 != 0 || stride > (1LL << 36))
+    return fail(CHORD_ERR_INVALID_ARG, "%s: row stride %lld must be a multiple of 8 from %d to 2^36", name,
+                (long long)stride, width);
+  return CHORD_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -207,6 +235,60 @@ int chord_mxfp4_moe_gemm(const void* rows, size_t rows_bytes, const void* packed
                                        epilogue == CHORD_EPI_SILU_MUL, C, workspace, chord::force_timeout(), dev_status,
                                        stream_of(stream)),
               "MXFP4 product launch");
+}
+
+size_t chord_expert_gemm_workspace_bytes(void) { return chord::expert_gemm_workspace_bytes(); }
+
+int chord_expert_gemm(const void* x, int dtype, int64_t x_stride, const void* w, int64_t w_stride,
+                      int64_t w_expert_stride, int E_local, int N, int K, int transpose_w,
+                      const int32_t* expert_counts, const int32_t* expert_offsets, size_t capacity, void* out,
+                      int64_t out_stride, void* workspace, size_t ws_bytes, int* dev_status, void* stream) {
+  int rc = check_product(dtype, E_local, N, K, expert_counts, expert_offsets, capacity, workspace, ws_bytes);
+  if (rc) return rc;
+  // item counts fit 32 bits with room
+  if ((capacity / 256 + E_local) * static_cast<size_t>((transpose_w ? K : N) / 256 + 1) > (1u << 30))
+    return fail(CHORD_ERR_INVALID_ARG, "%zu rows x N=%d, K=%d: too large", capacity, N, K);
+  if (capacity == 0) return CHORD_OK;
+  if ((rc = check_rows16("x", x, x_stride, transpose_w ? N : K, capacity))) return rc;
+  if ((rc = check_rows16("w", w, w_stride, K, N))) return rc;
+  if ((rc = check_rows16("out", out, out_stride, transpose_w ? K : N, capacity))) return rc;
+  if (E_local == 1) w_expert_stride = w_stride * N;   // not used
+  if (w_expert_stride < 8 || w_expert_stride % 8 != 0 || w_expert_stride > (1LL << 38))
+    return fail(CHORD_ERR_INVALID_ARG, "w: expert stride %lld must be a multiple of 8 from 8 to 2^38",
+                (long long)w_expert_stride);
+  chord::ExpertGemm g{};
+  g.x = x, g.ldx = x_stride, g.w = w, g.ldw = w_stride, g.expert_stride = w_expert_stride;
+  g.f16 = dtype == CHORD_DTYPE_FP16, g.transposed = transpose_w != 0;
+  g.counts = expert_counts, g.offsets = expert_offsets;
+  g.E = E_local, g.N = N, g.K = K, g.capacity = static_cast<int>(capacity);
+  g.out = out, g.ldo = out_stride, g.ws = workspace, g.test_timeout = chord::force_timeout(), g.status = dev_status;
+  return done(chord::expert_gemm_launch(g, stream_of(stream)), "expert product launch");
+}
+
+int chord_expert_wgrad(const void* dout, const void* x, int dtype, int64_t dout_stride, int64_t x_stride, int E_local,
+                       int N, int K, const int32_t* expert_counts, const int32_t* expert_offsets, size_t capacity,
+                       void* dw, int dw_dtype, void* workspace, size_t ws_bytes, int* dev_status, void* stream) {
+  int rc = check_product(dtype, E_local, N, K, expert_counts, expert_offsets, capacity, workspace, ws_bytes);
+  if (rc) return rc;
+  if (dw_dtype != dtype && dw_dtype != CHORD_DTYPE_FP32)
+    return fail(CHORD_ERR_INVALID_ARG, "dw_dtype %d must be dtype or FP32", dw_dtype);
+  const size_t tiles = (static_cast<size_t>(N) / 256 + 1) * (K / 256 + 1);
+  if (tiles * E_local > (1u << 30)) return fail(CHORD_ERR_INVALID_ARG, "%d experts x N=%d, K=%d: too large", E_local, N, K);
+  if (!dw) return fail(CHORD_ERR_INVALID_ARG, "null pointer: dw");
+  if (!aligned16(dw)) return fail(CHORD_ERR_INVALID_ARG, "dw must be 16-byte aligned");
+  if (capacity == 0)
+    return done(cudaMemsetAsync(dw, 0, static_cast<size_t>(E_local) * N * K * chord::dtype_bytes(dw_dtype),
+                                stream_of(stream)),
+                "weight gradient of no rows");
+  if ((rc = check_rows16("dout", dout, dout_stride, N, capacity))) return rc;
+  if ((rc = check_rows16("x", x, x_stride, K, capacity))) return rc;
+  chord::ExpertWgrad g{};
+  g.dout = dout, g.ldd = dout_stride, g.x = x, g.ldx = x_stride;
+  g.f16 = dtype == CHORD_DTYPE_FP16, g.f32 = dw_dtype == CHORD_DTYPE_FP32;
+  g.counts = expert_counts, g.offsets = expert_offsets;
+  g.E = E_local, g.N = N, g.K = K, g.capacity = static_cast<int>(capacity);
+  g.dw = dw, g.ws = workspace, g.test_timeout = chord::force_timeout(), g.status = dev_status;
+  return done(chord::expert_wgrad_launch(g, stream_of(stream)), "weight gradient launch");
 }
 
 }  // extern "C"

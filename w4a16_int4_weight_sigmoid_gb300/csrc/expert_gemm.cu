@@ -1,0 +1,633 @@
+// The experts' product in 16 bits and its gradients, on pairs of SMs:
+//   product      out[r, n] = sum_k x[r, k] W[e(r), n, k]
+//   transposed   out[r, k] = sum_n x[r, n] W[e(r), n, k]     (the rows' gradient)
+//   gradient     dW[e, n, k] = sum_{r of e} dout[r, n] x[r, k]
+// over rows in expert order: expert e's rows are counts[e] rows from
+// offsets[e] on, of any number, read on the device.
+//
+// Design on sm_103a (one persistent CTA per SM, two to a cluster):
+//   * the MMA is M = 256 over the pair (cta_group::2).  M is the weights' side
+//     (product: 256 weight rows times up to 256 of an expert's rows, a
+//     multiple of 32; gradient: 256 x 256 of an expert's dW), so an expert of
+//     few rows costs 32 columns, not 256 rows;
+//   * each CTA loads half of A and half of B per 64 of the contraction, 32 KB
+//     at most for 512 cycles of MMA; one CTA alone would need 48;
+//   * the transposed product reads the same weights with their M index
+//     contiguous, and the gradient reads both operands so: only the TMA boxes
+//     and the descriptors differ;
+//   * an item is one output tile; clusters take items in turn, so that those
+//     at work at one time share weights and rows in L2;
+//   * one warp per CTA loads, one (of the leading CTA) issues MMAs, one decodes
+//     items for the others, eight store finished tiles from one accumulator
+//     while the next is filled;
+//   * product tiles have weights in lanes and rows in columns: stmatrix.trans
+//     turns them so that rows are stored 16 bytes per lane.  Gradient tiles
+//     leave by TMA, which stops at the edges of dW;
+//   * the gradient's contraction ends inside a box of 64 rows.  What lies
+//     behind an expert's last row may be anything (another expert's, NaN), so
+//     a warp of each CTA zeroes up to 15 rows of both operands in shared
+//     memory before the MMAs of a last box run; MMAs that would see no row at
+//     all are left out.
+// Rows of a product's B that are not the expert's give columns that are not
+// stored, so they need no zeroing.
+// Every mbarrier wait is bounded; see mxfp4_gemm.cu.
+#include "common.cuh"
+#include "kernels.h"
+#include "pair.cuh"
+
+namespace chord {
+namespace {
+
+enum Mode { kProduct, kTransposed, kGradient };
+
+constexpr int kMaxTok = 256;           // largest row tile (columns of the accumulator)
+constexpr int kTileM = 256;            // of the pair
+constexpr int kStageK = 64;
+constexpr int kABytes = 128 * kStageK * 2;
+constexpr int kBlockBytes = 64 * kStageK * 2;      // 64 contiguous M or N values x 64 of the contraction
+constexpr int kMaxStages = 10, kMaxAcc = 8;
+__host__ __device__ constexpr int stage_bytes(int tok) { return kABytes + tok / 2 * kStageK * 2; }
+constexpr int kStageBudget = 6 * stage_bytes(kMaxTok);
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kItemWarp = 2, kZeroWarp = 3;
+constexpr int kItemSlots = 8;
+constexpr int kMaxExperts = 1024;
+constexpr int kTmemCols = 512;
+constexpr int kGroupTiles = 8;         // row tiles that are taken together
+// An epilogue warp's staging: product 32 tokens x 32 weights (rows of 80
+// bytes spread over the banks); gradient 32 rows of 128 bytes.
+constexpr int kOutPitch = 80;
+template <Mode kMode>
+constexpr int kOutBytes = kMode == kGradient ? 32 * 128 : 32 * kOutPitch;
+template <Mode kMode>
+constexpr int kSmemBytes = kStageBudget + kEpiWarps * kOutBytes<kMode> + 1024;
+static_assert(kMaxStages * stage_bytes(32) <= kStageBudget, "stage budget");
+static_assert(kSmemBytes<kProduct> + (kMaxExperts + 1) * 4 + 2048 <= 232448, "shared memory budget");
+static_assert(kSmemBytes<kGradient> + 1536 <= 232448, "shared memory budget");
+static_assert(3 * kThreads >= kMaxExperts, "three experts per thread at most");
+
+struct Args {
+  const int32_t* counts;
+  const int32_t* offsets;
+  uint16_t* out;         // product
+  long long ldo;
+  int* status;
+  int E, capacity;
+  int m, k;              // product: weights' side of the output, contraction; gradient: N, K
+  int m_tiles, n_tiles;  // tiles of 256
+  int f32;               // gradient: dW in FP32
+  int test_timeout;      // test of the timeout path: no item is handed out, waits for one are short
+};
+// The product's B boxes (rows of x) have the height of half a row tile: one
+// map for each multiple of 16.
+struct Maps {
+  CUtensorMap a, b[8], out;
+};
+
+struct alignas(16) Seg {
+  int e, row0, rows, m0;   // expert; its rows of this item (gradient: all of them); first weight row
+  int n0, cols;            // gradient: first column of dW; columns of the accumulator
+  int stages, valid;       // of 64 of the contraction
+};
+
+__device__ __forceinline__ int up32(int v) { return (v + 31) & ~31; }
+__device__ __forceinline__ int row_tiles(int cnt) { return (cnt + kMaxTok - 1) / kMaxTok; }
+// Rows of an expert's row tiles: equal to within the rounding to 32.
+__device__ __forceinline__ int tile_rows(int cnt, int n) { return up32(n > 1 ? (cnt + n - 1) / n : cnt); }
+
+// The items in the order in which they are dealt.
+//   product: experts in order; per expert groups of kGroupTiles row tiles; per
+//   group the weight tiles; per weight tile the group's row tiles
+//   gradient: experts in order; per expert tiles of N, per tile tiles of K
+template <Mode kMode>
+__device__ __forceinline__ Seg decode(const Args& a, const int* prefix, int item, int& e) {
+  const int lane = threadIdx.x & 31;
+  Seg s{};
+  s.valid = 1;
+  if constexpr (kMode == kGradient) {
+    const int per = a.m_tiles * a.n_tiles;
+    e = item / per;
+    const int local = item - e * per, mt = local / a.n_tiles;
+    s.m0 = mt * kTileM;
+    s.n0 = (local - mt * a.n_tiles) * kMaxTok;
+    s.cols = min(kMaxTok, up32(a.k - s.n0));
+    s.row0 = ld_ca(a.offsets + e);
+    s.rows = ld_ca(a.counts + e);
+    s.stages = (s.rows + kStageK - 1) / kStageK;
+  } else {
+    // the largest e with prefix[e] <= item (items only grow)
+    auto past = [&](int at) { return __ballot_sync(0xffffffffu, at > a.E || prefix[at] > item); };
+    uint32_t found = past(e + 1 + lane);
+    if (!found) {                      // further on: the 32nd of the experts, then the expert
+      const int block = (a.E + 31) / 32;
+      static_assert(kMaxExperts <= 32 * 32, "two steps of 32");
+      e = block * (__ffs(past(min(block * (lane + 1), a.E))) - 1);
+      found = past(e + 1 + lane);
+    }
+    e += __ffs(found) - 1;
+    const int cnt = ld_ca(a.counts + e);
+    int local = item - prefix[e], rt = 0;
+    s.row0 = ld_ca(a.offsets + e);
+    s.rows = cnt;
+    if (cnt > kMaxTok) {
+      const int n = row_tiles(cnt), per = tile_rows(cnt, n);
+      const int group = local / (kGroupTiles * a.m_tiles);
+      local -= group * kGroupTiles * a.m_tiles;
+      const int width = min(kGroupTiles, n - group * kGroupTiles);
+      const int mt = local / width;
+      rt = group * kGroupTiles + local - mt * width;
+      local = mt;
+      s.row0 += rt * per;
+      s.rows = min(per, cnt - rt * per);
+    }
+    s.m0 = local * kTileM;
+    s.cols = up32(s.rows);
+    s.stages = (a.k + kStageK - 1) / kStageK;
+  }
+  s.e = e;
+  return s;
+}
+
+struct ItemRing {
+  uint64_t *full, *empty;
+  const Seg* slots;
+  uint32_t polls;
+  int slot, ph;
+  // The next item: false at the end of the work or on a timeout.  All lanes
+  // of the calling warp take it; lane 0 releases the slot.
+  __device__ __forceinline__ bool next(Seg& s, bool& ok, int* status) {
+    ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], ph, status, polls));
+    if (!ok) return false;
+    const int4* src = reinterpret_cast<const int4*>(&slots[slot]);
+    const int4 lo = src[0], hi = src[1];
+    s.e = lo.x, s.row0 = lo.y, s.rows = lo.z, s.m0 = lo.w;
+    s.n0 = hi.x, s.cols = hi.y, s.stages = hi.z, s.valid = hi.w;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[slot]);
+    if (++slot == kItemSlots) slot = 0, ph ^= 1;
+    return s.valid != 0;
+  }
+};
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (kF16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four 8 x 8 matrices of 16-bit values, transposed (as in mxfp4_gemm.cu).
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r0), "r"(r1),
+               "r"(r2), "r"(r3)
+               : "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Up to 32 rows of a finished product tile: this warp's accumulators of its 32
+// weights (lo: 0-15 of the lane quarter, hi: 16-31), `n` rows at `out`, from
+// column `col0` on.
+template <bool kF16>
+__device__ __forceinline__ void store_rows(const Args& a, const uint32_t (&lo)[16], const uint32_t (&hi)[16],
+                                           uint16_t* out, uint32_t stage_s, int col0, int lane, int n) {
+  // lane 8 i + c: row c of its group of 8, weights 8 (i & 1) on
+  const uint32_t dst = stage_s + ((lane & 7) + 8 * (lane >> 4)) * kOutPitch + ((lane >> 3) & 1) * 16;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {   // rows 16 p .. 16 p + 15
+    uint32_t l[4], h[4];          // [group of 8 rows][weights 0-7, 8-15]
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * p + 2 * i;
+      l[i] = pack2<kF16>(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
+      h[i] = pack2<kF16>(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1]));
+    }
+    stmatrix_x4_trans(dst + 16 * p * kOutPitch, l[0], l[1], l[2], l[3]);
+    stmatrix_x4_trans(dst + 16 * p * kOutPitch + 32, h[0], h[1], h[2], h[3]);
+  }
+  __syncwarp();
+  const int part = lane & 3, col = col0 + 8 * part;   // four lanes per row
+  uint4 v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[j].x), "=r"(v[j].y), "=r"(v[j].z), "=r"(v[j].w)
+                 : "r"(stage_s + ((lane >> 2) + 8 * j) * kOutPitch + 16 * part)
+                 : "memory");
+  if (col < a.m) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = (lane >> 2) + 8 * j;
+      if (row < n) *reinterpret_cast<uint4*>(out + row * a.ldo + col) = v[j];
+    }
+  }
+  __syncwarp();
+}
+
+template <Mode kMode, bool kF16>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    expert_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
+  constexpr bool kGrad = kMode == kGradient;
+  constexpr bool kMnA = kMode != kProduct, kMnB = kGrad;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages];
+  __shared__ __align__(8) uint64_t tfull[kMaxAcc], tempty[kMaxAcc], done_bar;
+  __shared__ __align__(8) uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+  __shared__ Seg item_slots[kItemSlots];
+  __shared__ uint32_t tmem_base_s;
+  __shared__ int prefix[kGrad ? 1 : kMaxExperts + 1];
+  __shared__ int warp_sum[kThreads / 32], warp_max[kThreads / 32];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+
+  if (tid == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&full[s], 2);              // of the leading CTA: each CTA's bytes, or its zeroing warp
+      mbar_init(&empty[s], 1);
+      mbar_init(&tail[s], 1);
+    }
+    for (int b = 0; b < kMaxAcc; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * kEpiWarps);   // of the leading CTA
+    }
+    mbar_init(&done_bar, 1);
+    for (int q = 0; q < kItemSlots; ++q) {
+      mbar_init(&item_full[q], 1);
+      mbar_init(&item_empty[q], 1 + (rank == 0 ? 1 : 0) + (kGrad ? 1 : 0) + kEpiWarps);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(&tmem_base_s, kTmemCols);
+  // programmatic launch: nothing above touches global memory
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // The order is checked, and for a product the first item of each expert and
+  // the largest row tile are found: thread i covers experts [i * per, (i + 1) * per).
+  const int per = 1 + (a.E > kThreads) + (a.E > 2 * kThreads);
+  int mine = 0, most = 32, bad = 0;
+#pragma unroll 1
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    if (e >= a.E) break;
+    int cnt = ld_ca(a.counts + e);
+    const int off = ld_ca(a.offsets + e), next = ld_ca(a.offsets + e + 1);
+    // Experts that end before the next one begins have disjoint rows.
+    if (cnt < 0 || off < 0 || cnt > a.capacity || off > a.capacity - cnt || off + cnt > next) bad = 1, cnt = 0;
+    if constexpr (!kGrad) {
+      prefix[e] = mine;
+      if (cnt > 0) {
+        const int n = row_tiles(cnt);
+        mine += a.m_tiles * n;
+        most = max(most, tile_rows(cnt, n));
+      }
+    }
+  }
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  most = __reduce_max_sync(0xffffffffu, bad ? 1 << 16 : most);
+  if (lane == 31) {
+    warp_sum[warp] = inc;
+    warp_max[warp] = most;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int sum = lane < kThreads / 32 ? warp_sum[lane] : 0;
+  int tok = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? warp_max[lane] : 0);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += t;
+  }
+  const int run = inc - mine + (warp ? __shfl_sync(0xffffffffu, sum, warp - 1) : 0);
+  if constexpr (!kGrad) {
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+      const int e = tid * per + i;
+      if (e >= a.E) break;
+      prefix[e] += run;
+    }
+    if (tid == kThreads - 1) prefix[a.E] = run + mine;   // the last thread ends at the total
+  }
+  const bool order_ok = tok < 1 << 16;   // else nothing is computed
+  if (!order_ok && tid == 0) set_status(a.status, CHORD_ERR_INVALID_ARG);
+  cluster_sync();                        // also: the peer's barriers are there
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, tmem_base_s, 0);
+  if (kGrad) tok = kMaxTok;
+  tok = order_ok ? tok : 32;
+  const int items = !order_ok ? 0 : kGrad ? a.E * a.m_tiles * a.n_tiles : prefix[a.E];
+  const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget / stage);
+  const int n_acc = min(kMaxAcc, kTmemCols / tok);
+  ItemRing ring{item_full, item_empty, item_slots, a.test_timeout ? kTestWaitPolls : kWaitPolls, 0, 0};
+  Seg w;
+  bool ok = true;
+
+  if (warp == 0) {
+    // ----------------------------------------------------------------- loads
+    // The whole warp runs the loop, one elected lane issues.  Both CTAs' bytes
+    // count on the leading CTA's barrier; a gradient's last box completes on
+    // this CTA's own, for the zeroing warp.
+    const uint32_t full0 = cluster_addr(&full[0], 0);
+    int it = 0, st = 0, ph = 0;
+    while (ring.next(w, ok, a.status)) {
+      const int half = w.cols >> 1;
+      const CUtensorMap* mb = &maps.b[kGrad ? 0 : (half >> 4) - 1];
+      const uint32_t bytes = kABytes + (kGrad ? 2 * kBlockBytes : half * kStageK * 2);
+      const int m = w.m0 + 128 * static_cast<int>(rank);
+      const int n = kGrad ? w.n0 + half * static_cast<int>(rank) : w.row0 + half * static_cast<int>(rank);
+      for (int u = 0; u < w.stages; ++u, ++it) {
+        if (it >= n_stages && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, a.status)))) break;
+        const uint32_t dst = smem0 + st * stage;
+        const int k0 = u * kStageK;
+        uint32_t bar = full0 + 8 * st;
+        if (kGrad && w.rows - k0 < kStageK && ((w.rows - k0) & 15)) {
+          bar = smem_u32(&tail[st]);
+          mbar_arrive_expect_tx_elect(&tail[st], bytes);
+        } else {
+          mbar_arrive_expect_tx_cluster_elect(bar, bytes);
+        }
+        if constexpr (kMode == kProduct) {
+          tma_pair_3d_elect(dst, &maps.a, k0, m, w.e, bar);
+          tma_pair_2d_elect(dst + kABytes, mb, k0, n, bar);
+        } else if constexpr (kMode == kTransposed) {
+          tma_pair_3d_elect(dst, &maps.a, m, k0, w.e, bar);
+          tma_pair_3d_elect(dst + kBlockBytes, &maps.a, m + 64, k0, w.e, bar);
+          tma_pair_2d_elect(dst + kABytes, mb, k0, n, bar);
+        } else {
+          const int row = w.row0 + k0;
+          tma_pair_2d_elect(dst, &maps.a, m, row, bar);
+          tma_pair_2d_elect(dst + kBlockBytes, &maps.a, m + 64, row, bar);
+          tma_pair_2d_elect(dst + kABytes, mb, n, row, bar);
+          tma_pair_2d_elect(dst + kABytes + kBlockBytes, mb, n + 64, row, bar);
+        }
+        if (++st == n_stages) st = 0, ph ^= 1;
+      }
+      if (!ok) break;
+    }
+    // Every copy lands before a CTA can exit: the leading CTA waits for both
+    // CTAs' bytes (the cluster barrier below holds the other).
+    if (rank == 0)
+      for (int j = max(0, it - n_stages); j < it; ++j)
+        ok = mbar_wait(&full[j % n_stages], (j / n_stages) & 1, a.status) && ok;
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------------------------ MMAs
+    int st = 0, ph = 0, acc = 0, use = 0;
+    bool issued = false;
+    while (ring.next(w, ok, a.status)) {
+      const uint32_t d = tmem_base + acc * tok;
+      const uint32_t idesc = idesc_pair(!kF16, kMnA, kMnB, w.cols);
+      uint32_t accumulate = 0;
+      if (use >= 1) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], (use - 1) & 1, a.status));
+      tc_fence_after();
+      for (int u = 0; ok && u < w.stages; ++u) {
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&full[st], ph, a.status));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sa = smem0 + st * stage, sb = sa + kABytes;
+        const uint64_t da = kMnA ? sw128_mnmajor_desc(sa, kBlockBytes) : sw128_kmajor_desc(sa);
+        const uint64_t db = kMnB ? sw128_mnmajor_desc(sb, kBlockBytes) : sw128_kmajor_desc(sb);
+        // 16 of the contraction: 32 bytes on in a row, or 16 rows of 128 bytes
+        constexpr int kStepA = kMnA ? 128 : 2, kStepB = kMnB ? 128 : 2;
+        const int steps = kGrad ? (min(w.rows - u * kStageK, kStageK) + 15) / 16 : 4;
+        if (!kGrad || steps == 4) {
+          tc_pair_mma4_elect<kStepA, kStepB>(d, da, db, idesc, accumulate);
+        } else {
+          for (int i = 0; i < steps; ++i)
+            tc_pair_mma_elect(d, da + i * kStepA, db + i * kStepB, idesc, accumulate | (i > 0));
+        }
+        tc_pair_commit_elect(&empty[st]);
+        accumulate = 1;
+        issued = true;
+        if (++st == n_stages) st = 0, ph ^= 1;
+      }
+      if (!ok) break;
+      tc_pair_commit_elect(&tfull[acc]);
+      if (++acc == n_acc) acc = 0, ++use;
+    }
+    // all issued MMAs complete before TMEM can be freed
+    if (issued) {
+      tc_commit_pair_local_elect(&done_bar);
+      ok = mbar_wait(&done_bar, 0, a.status) && ok;
+    }
+  } else if (warp == kItemWarp) {
+    // ----------------------------------------------------------------- items
+    int slot = 0, ph = 0, e = 0;
+    int item = a.test_timeout ? -1 : cluster;
+    for (bool first = true, more = item >= 0; more;) {
+      more = item < items;
+      Seg s{};
+      if (more) s = decode<kMode>(a, prefix, item, e);
+      if (!first && !(ok = __all_sync(0xffffffffu, mbar_wait_backoff(&item_empty[slot], ph ^ 1, a.status)))) break;
+      if (lane == 0) {
+        item_slots[slot] = s;
+        mbar_arrive(&item_full[slot]);   // release: the item is visible to the waiters
+      }
+      item += clusters;
+      if (++slot == kItemSlots) slot = 0, ph ^= 1, first = false;
+    }
+  } else if (kGrad && warp == kZeroWarp) {
+    // ------------------------------------------- rows behind an expert's last
+    const uint32_t full0 = cluster_addr(&full[0], 0);
+    int st = 0;
+    uint32_t tail_ph = 0;                // a slot's phase turns when it holds a last box
+    while (ring.next(w, ok, a.status)) {
+      st = (st + w.stages) % n_stages;
+      const int last = w.rows % kStageK;
+      if (!(last & 15)) continue;
+      const int at = (st ? st : n_stages) - 1;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&tail[at], (tail_ph >> at) & 1, a.status)))) break;
+      tail_ph ^= 1u << at;
+      // rows last .. next multiple of 16 of the four blocks of 64 values
+      const uint32_t base = smem0 + at * stage + (lane & 7) * 16;
+      const int end = (last + 15) & ~15;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        for (int r = last + (lane >> 3); r < end; r += 4)
+          st_shared_v4(base + b * kBlockBytes + r * 128, 0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(full0 + 8 * at);
+    }
+  } else if (warp >= kEpiWarp0) {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3, t = (warp - kEpiWarp0) / 4;   // TMEM lane quarter; which of the column chunks
+    const uint32_t out_stage = smem0 + kStageBudget + (warp - kEpiWarp0) * kOutBytes<kMode>;
+    const uint32_t tempty0 = cluster_addr(&tempty[0], 0);
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    int acc = 0, use = 0;
+    while (ring.next(w, ok, a.status)) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], use & 1, a.status)))) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + acc * tok + lanes;
+      const int m = w.m0 + 128 * static_cast<int>(rank) + 32 * q;
+      if constexpr (!kGrad) {
+        // the next 32 rows' accumulators are on their way while these go out
+        uint32_t next[2][16];
+        auto load = [&](int c0) {
+          tmem_ld_16x256b_x4(taddr + c0, next[0]);
+          tmem_ld_16x256b_x4(taddr + c0 + (16u << 16), next[1]);
+        };
+        uint16_t* out = a.out + w.row0 * a.ldo;
+        if (32 * t < w.rows) load(32 * t);
+#pragma unroll 1
+        for (int c0 = 32 * t; c0 < w.rows; c0 += 64) {
+          tmem_ld_wait();
+          uint32_t v[2][16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[0][i] = next[0][i], v[1][i] = next[1][i];
+          if (c0 + 64 < w.rows) load(c0 + 64);
+          store_rows<kF16>(a, v[0], v[1], out + c0 * a.ldo, out_stage, m, lane, w.rows - c0);
+        }
+      } else {
+        // chunks of 128 bytes of dW's rows, 16-byte parts swizzled with the row
+        const int width = a.f32 ? 32 : 64;
+        const uint32_t dst = out_stage + lane * 128;
+#pragma unroll 1
+        for (int c0 = width * t; c0 < w.cols; c0 += 2 * width) {
+          uint32_t v[2][32];
+          if (w.rows > 0) {
+            tmem_ld_32x32b_x32(taddr + c0, v[0]);
+            if (!a.f32 && c0 + 32 < w.cols) tmem_ld_32x32b_x32(taddr + c0 + 32, v[1]);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0;
+          }
+          if (lane == 0) bulk_wait_read();   // the last store has read its staging
+          __syncwarp();
+          if (a.f32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_v4(dst + ((j ^ (lane & 7)) << 4), v[0][4 * j], v[0][4 * j + 1], v[0][4 * j + 2],
+                           v[0][4 * j + 3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t* x = &v[j / 4][8 * (j & 3)];
+              uint32_t p[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) p[i] = pack2<kF16>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+              st_shared_v4(dst + ((j ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && m < a.m && w.n0 + c0 < a.k) {
+            tma_store_3d(&maps.out, out_stage, w.n0 + c0, m, w.e);
+            bulk_commit_group();
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
+      if (++acc == n_acc) acc = 0, ++use;
+    }
+    if (kGrad && lane == 0) bulk_wait_all();
+  }
+  // A wait that ran out: copies that the other CTA, which may have stopped
+  // elsewhere, does not account for have landed by then.
+  if (!ok)
+    for (int i = 0; i < 1 << 14; ++i) __nanosleep(64);
+
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// A map of [experts][rows][cols] (rows and experts at the given strides, in
+// elements; experts 0: two dimensions) in boxes of 128 bytes by `height` rows,
+// 128-byte swizzle.
+bool encode(CUtensorMap* map, const void* p, bool f16, bool f32, long long cols, long long rows, long long ld,
+            int experts, long long expert_stride, int height) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int size = f32 ? 4 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(experts)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * size, static_cast<cuuint64_t>(expert_stride) * size};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(height), 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUtensorMapDataType type = f32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return fn(map, type, experts ? 3 : 2, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Mode kMode, bool kF16>
+cudaError_t launch(const Maps& maps, const Args& a, cudaStream_t st) {
+  cudaError_t err = ensure_smem_limit<expert_gemm_kernel<kMode, kF16>>(kSmemBytes<kMode>);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(expert_gemm_kernel<kMode, kF16>, dim3(sm_count() < 2 ? 2 : sm_count() & ~1), dim3(kThreads), kSmemBytes<kMode>, st,
+                       true, maps, a);
+}
+
+}  // namespace
+
+size_t expert_gemm_workspace_bytes() { return 256; }
+
+cudaError_t expert_gemm_launch(const ExpertGemm& g, cudaStream_t st) {
+  Args a{};
+  a.counts = g.counts, a.offsets = g.offsets, a.status = g.status;
+  a.E = g.E, a.capacity = g.capacity, a.test_timeout = g.test_timeout ? 1 : 0;
+  a.out = static_cast<uint16_t*>(g.out), a.ldo = g.ldo;
+  a.m = g.transposed ? g.K : g.N, a.k = g.transposed ? g.N : g.K;
+  a.m_tiles = (a.m + kTileM - 1) / kTileM;
+  Maps maps{};
+  if (!encode(&maps.a, g.w, g.f16, false, g.K, g.N, g.ldw, g.E, g.expert_stride, g.transposed ? kStageK : 128))
+    return cudaErrorInvalidValue;
+  for (int i = 0; i < 8; ++i)
+    if (!encode(&maps.b[i], g.x, g.f16, false, a.k, g.capacity, g.ldx, 0, 0, 16 * (i + 1)))
+      return cudaErrorInvalidValue;
+  if (g.transposed) return g.f16 ? launch<kTransposed, true>(maps, a, st) : launch<kTransposed, false>(maps, a, st);
+  return g.f16 ? launch<kProduct, true>(maps, a, st) : launch<kProduct, false>(maps, a, st);
+}
+
+cudaError_t expert_wgrad_launch(const ExpertWgrad& g, cudaStream_t st) {
+  Args a{};
+  a.counts = g.counts, a.offsets = g.offsets, a.status = g.status;
+  a.E = g.E, a.capacity = g.capacity, a.test_timeout = g.test_timeout ? 1 : 0;
+  a.m = g.N, a.k = g.K, a.f32 = g.f32 ? 1 : 0;
+  a.m_tiles = (g.N + kTileM - 1) / kTileM;
+  a.n_tiles = (g.K + kMaxTok - 1) / kMaxTok;
+  Maps maps{};
+  if (!encode(&maps.a, g.dout, g.f16, false, g.N, g.capacity, g.ldd, 0, 0, kStageK) ||
+      !encode(&maps.b[0], g.x, g.f16, false, g.K, g.capacity, g.ldx, 0, 0, kStageK) ||
+      !encode(&maps.out, g.dw, g.f16, g.f32, g.K, g.N, g.K, g.E, static_cast<long long>(g.N) * g.K, 32))
+    return cudaErrorInvalidValue;
+  return g.f16 ? launch<kGradient, true>(maps, a, st) : launch<kGradient, false>(maps, a, st);
+}
+
+}  // namespace chord

@@ -119,4 +119,38 @@ cudaError_t mxfp4_gemm_launch(const uint8_t* rows, const uint8_t* w, int E, int 
                               const int32_t* offsets, int capacity, bool gate_up, uint16_t* C, void* ws,
                               bool test_timeout, int* status, cudaStream_t st);
 
+// The experts' product in 16 bits (FP16 where f16, else BF16) and its weights'
+// gradient; ld*: row strides in elements.
+struct ExpertGemm {
+  const void* x;
+  long long ldx;
+  const void* w;         // [E, N, K], rows and experts at these strides
+  long long ldw, expert_stride;
+  bool f16, transposed;
+  const int32_t* counts;
+  const int32_t* offsets;
+  int E, N, K, capacity;
+  void* out;
+  long long ldo;
+  void* ws;
+  bool test_timeout;
+  int* status;
+};
+struct ExpertWgrad {
+  const void* dout;
+  const void* x;
+  long long ldd, ldx;
+  bool f16, f32;         // operands; dW in FP32
+  const int32_t* counts;
+  const int32_t* offsets;
+  int E, N, K, capacity;
+  void* dw;              // contiguous [E, N, K]
+  void* ws;
+  bool test_timeout;
+  int* status;
+};
+size_t expert_gemm_workspace_bytes();
+cudaError_t expert_gemm_launch(const ExpertGemm& g, cudaStream_t st);
+cudaError_t expert_wgrad_launch(const ExpertWgrad& g, cudaStream_t st);
+
 }  // namespace chord

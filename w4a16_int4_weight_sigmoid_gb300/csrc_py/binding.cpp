@@ -191,6 +191,53 @@ int moe_gemm(PyObject* const* a) {
                               static_cast<chord_bf16*>(C.data_ptr()), ws, numel(a[10]), status, stream(a[12]));
 }
 
+// Tensors that a kernel launched now may use: on the current device.
+template <typename... O>
+void here(O... objects) {
+  const int device = c10::cuda::current_device();
+  for (PyObject* o : {objects...})
+    if (o != Py_None && THPVariable_Check(o) && THPVariable_Unpack(o).get_device() != device)
+      raise(PyExc_ValueError, "all tensors must be on the current device (cuda:%d)", device);
+}
+
+int expert_gemm(PyObject* const* a) {
+  const Rows x(a[0], "x"), out(a[4], "out");
+  const at::Tensor& w = tensor(a[1], "w");
+  const bool transpose = integer(a[6]) != 0;
+  if (dtype_code(w, "w") != x.dtype || out.dtype != x.dtype) raise(PyExc_TypeError, "x, w and out must be of one type");
+  if (w.dim() != 3 || (w.size(2) > 1 && w.stride(2) != 1))
+    raise(PyExc_ValueError, "w must be [experts, N, K] with unit stride along K");
+  const int64_t E = w.size(0), N = w.size(1), K = w.size(2);
+  if (x.h != (transpose ? N : K) || out.h != (transpose ? K : N) || out.n != x.n)
+    raise(PyExc_ValueError, "x [%lld, %lld] and out [%lld, %lld] do not fit w [%lld, %lld, %lld]", (long long)x.n,
+          (long long)x.h, (long long)out.n, (long long)out.h, (long long)E, (long long)N, (long long)K);
+  void* ws = bytes(a[5], -1, "workspace");
+  int* status = a[7] == Py_None ? nullptr : ints(a[7], 1, "dev_status");
+  const int32_t *counts = ints(a[2], E, "expert_counts"), *offsets = ints(a[3], E + 1, "expert_offsets");
+  here(a[0], a[1], a[2], a[3], a[4], a[5], a[7]);
+  return chord_expert_gemm(x.p, x.dtype, x.stride, w.data_ptr(), N > 1 ? w.stride(1) : K,
+                           E > 1 ? w.stride(0) : N * K, narrow(E, "experts"), narrow(N, "N"), narrow(K, "K"), transpose,
+                           counts, offsets, x.n, out.p, out.stride, ws, numel(a[5]), status, stream(a[8]));
+}
+
+int expert_wgrad(PyObject* const* a) {
+  const Rows dout(a[0], "dout"), x(a[1], "x");
+  if (x.dtype != dout.dtype) raise(PyExc_TypeError, "x is of another type");
+  if (x.n != dout.n) raise(PyExc_ValueError, "x has %lld rows, need %lld", (long long)x.n, (long long)dout.n);
+  const at::Tensor& dw = tensor(a[4], "dw");
+  const int out = dtype_code(dw, "dw");
+  if (dw.dim() != 3 || dw.size(1) != dout.h || dw.size(2) != x.h || !dw.is_contiguous())
+    raise(PyExc_ValueError, "dw must be contiguous [experts, %lld, %lld]", (long long)dout.h, (long long)x.h);
+  const int64_t E = dw.size(0);
+  void* ws = bytes(a[5], -1, "workspace");
+  int* status = a[6] == Py_None ? nullptr : ints(a[6], 1, "dev_status");
+  const int32_t *counts = ints(a[2], E, "expert_counts"), *offsets = ints(a[3], E + 1, "expert_offsets");
+  here(a[0], a[1], a[2], a[3], a[4], a[5], a[6]);
+  return chord_expert_wgrad(dout.p, x.p, x.dtype, dout.stride, x.stride, narrow(E, "experts"), narrow(dout.h, "N"),
+                            narrow(x.h, "K"), counts, offsets, x.n, dw.data_ptr(), out, ws, numel(a[5]), status,
+                            stream(a[7]));
+}
+
 template <int (*kCall)(PyObject* const*), int kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != kArgs) {
@@ -221,6 +268,8 @@ PyMethodDef kMethods[] = {
     method<dequantize, 4>("dequantize"),
     method<quantize_rows, 7>("quantize_rows"),
     method<moe_gemm, 13>("moe_gemm"),
+    method<expert_gemm, 9>("expert_gemm"),
+    method<expert_wgrad, 8>("expert_wgrad"),
     {nullptr, nullptr, 0, nullptr},
 };
 
