@@ -392,8 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (use >= 1) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], (use - 1) & 1, a.status));
       tc_fence_after();
       for (int u = 0; ok && u < w.stages; ++u) {
-        ok = __all_sync(0xffffffffu, mbar_wait_cluster(&full[st], ph, a.status));
-        if (!ok) break;
+        // (a last box was written by threads of the other CTA too)
+        ok = kGrad && w.rows - u * kStageK < kStageK ? mbar_wait_cluster(&full[st], ph, a.status)
+                                                      : mbar_wait(&full[st], ph, a.status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
         const uint32_t sa = smem0 + st * stage, sb = sa + kABytes;
         const uint64_t da = kMnA ? sw128_mnmajor_desc(sa, kBlockBytes) : sw128_kmajor_desc(sa);
