@@ -537,6 +537,62 @@ int chord_expert_wgrad(const void* dout, const void* x, int dtype, int64_t dout_
                        int N, int K, const int32_t* expert_counts, const int32_t* expert_offsets, size_t capacity,
                        void* dw, int dw_dtype, void* workspace, size_t ws_bytes, int* dev_status, void* stream);
 
+/* ------------------------------------------------------ rows in 8 bits
+ * Microscaled 8-bit floating point (OCP Microscaling Formats v1.0, MXFP8 with
+ * E4M3 values), for activations that a backward pass reads again: 32
+ * consecutive values of a row share a scale 2^(s - 127) (E8M0, one byte).
+ *   quantize    s = the smallest from 0 on with amax <= 448 * 2^(s - 127), so
+ *               that nothing saturates; code = x / scale rounded to the
+ *               nearest E4M3 value, ties to even (at s = 247, whose 256 is
+ *               past FP32, to at most 240).  A block that holds an infinity or
+ *               a NaN gets s = 255 and codes 0, and reads as NaN.
+ *               x [rows, K] of `dtype`, codes [rows, K], scales [rows, K/32]
+ *   dequantize  the inverse: out [rows, K] of `dtype`, rounded once (FP16: to
+ *               at most 65504)
+ *   permute     dequantize of token rows [M, K] into the aligned expert order
+ *               of chord_moe_align: out[p(t,j)] = row t, padding rows become
+ *               zeros, rows at or past num_tokens_post_padded are not written
+ * K % 32 == 0, K <= 2^24; codes 16-byte aligned.
+ */
+int chord_mxfp8_quantize(const void* x, int dtype, int64_t x_stride, int64_t rows, int K, uint8_t* codes,
+                         uint8_t* scales, void* stream);
+int chord_mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, void* out, int dtype,
+                           int64_t out_stride, void* stream);
+int chord_mxfp8_permute(const uint8_t* codes, const uint8_t* scales, const int32_t* sorted_token_ids,
+                        const int32_t* num_tokens_post_padded, int M, int topk, int K, size_t capacity, void* out,
+                        int dtype, int64_t out_stride, void* stream);
+
+/* --------------------------------------- the gated activation in training
+ * Between an expert's two products, over rows in the aligned expert order,
+ * with the routing weight w of the row's assignment (t, j) on it, so that the
+ * second product's rows are summed to tokens without weights:
+ *   forward   h[r, i] = w silu(gu[r, i]) gu[r, I + i]
+ *   backward  dgu[r, i]     = w dh[r, i] gu[r, I + i] silu'(gu[r, i])
+ *             dgu[r, I + i] = w dh[r, i] silu(gu[r, i])
+ *             dweights[t, j] = sum_i dh[r, i] silu(gu[r, i]) gu[r, I + i],
+ *             0 for an assignment without a row here
+ *             h as in the forward pass, where asked for (h not NULL)
+ * Padding rows become zeros and none of their values reaches a result; rows
+ * at or past num_tokens_post_padded are not written.
+ *   dtype     chord_dtype of gu, h, dh and dgu; sums are FP32, rounded once
+ *   codes, scales
+ *             forward: gu [capacity, 2I] in 8 bits as chord_mxfp8_quantize
+ *             holds it (padding rows as zeros; the rows of h are of gu itself),
+ *             both NULL for none.  backward: read in the place of gu, which is
+ *             NULL then.  I % 32 == 0 and codes 16-byte aligned with them, any
+ *             I without
+ *   *_stride  row strides in elements, as for chord_moe_permute
+ * Results are the same from call to call.  topk <= 32.
+ */
+int chord_swiglu(const void* gu, int dtype, int64_t gu_stride, const float* topk_weights,
+                 const int32_t* sorted_token_ids, const int32_t* num_tokens_post_padded, int M, int topk, int I,
+                 size_t capacity, void* h, int64_t h_stride, uint8_t* codes, uint8_t* scales, void* stream);
+int chord_swiglu_backward(const void* dh, int dtype, int64_t dh_stride, const void* gu, int64_t gu_stride,
+                          const uint8_t* codes, const uint8_t* scales, const float* topk_weights,
+                          const int32_t* sorted_positions, const int32_t* sorted_token_ids,
+                          const int32_t* num_tokens_post_padded, int M, int topk, int I, size_t capacity, void* dgu,
+                          int64_t dgu_stride, float* dweights, void* h, int64_t h_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

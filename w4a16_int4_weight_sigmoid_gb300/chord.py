@@ -99,6 +99,12 @@ _SIGS = {
     "chord_mxfp4_moe_gemm": (_I, [_P, _Z, _P, _I, _I, _I, _P, _P, _Z, _I, _P, _P, _Z, _P, _P]),
     "chord_expert_gemm_workspace_bytes": (_Z, []),
     "chord_expert_gemm": (_I, [_P, _I, _L, _P, _L, _L, _I, _I, _I, _I, _P, _P, _Z, _P, _L, _P, _Z, _P, _P]),
+    "chord_mxfp8_quantize": (_I, [_P, _I, _L, _L, _I, _P, _P, _P]),
+    "chord_mxfp8_dequantize": (_I, [_P, _P, _L, _I, _P, _I, _L, _P]),
+    "chord_mxfp8_permute": (_I, [_P, _P, _P, _P, _I, _I, _I, _Z, _P, _I, _L, _P]),
+    "chord_swiglu": (_I, [_P, _I, _L, _P, _P, _P, _I, _I, _I, _Z, _P, _L, _P, _P, _P]),
+    "chord_swiglu_backward": (_I, [_P, _I, _L, _P, _L, _P, _P, _P, _P, _P, _P, _I, _I, _I, _Z, _P, _L, _P, _P, _L,
+                                   _P]),
     "chord_expert_wgrad": (_I, [_P, _P, _I, _L, _L, _I, _I, _I, _P, _P, _Z, _P, _I, _P, _Z, _P, _P]),
 }
 
@@ -539,5 +545,53 @@ def chord_expert_wgrad(dout, x, expert_counts, expert_offsets, dw, workspace, de
     x [capacity, K] of one type (BF16, FP16), dw contiguous [E, N, K] of that type or FP32."""
     rc = (_ext_module or _ext()).expert_wgrad(dout, x, expert_counts, expert_offsets, dw, workspace, dev_status,
                                               None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+# ------------------------------- rows in 8 bits, and the gated activation
+
+def chord_mxfp8_quantize(x, codes, scales, stream=None):
+    """x [rows, K] (BF16, FP16, FP32) -> codes uint8 [rows, K], scales uint8 [rows, K/32]."""
+    rc = (_ext_module or _ext()).mxfp8_quantize(x, codes, scales, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def chord_mxfp8_dequantize(codes, scales, out, stream=None):
+    """The values of codes and scales, out [rows, K] (BF16, FP16, FP32)."""
+    rc = (_ext_module or _ext()).mxfp8_dequantize(codes, scales, out, None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def chord_mxfp8_permute(codes, scales, sorted_positions, sorted_token_ids, num_tokens_post_padded, topk: int, out,
+                        stream=None):
+    """The values of token rows codes [M, K] and scales into the aligned expert order, out [capacity, K];
+    padding rows become zeros.  (Of sorted_positions [M * topk] only the size is used.)"""
+    rc = (_ext_module or _ext()).mxfp8_permute(codes, scales, sorted_positions, sorted_token_ids,
+                                               num_tokens_post_padded, topk, out,
+                                               None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def chord_swiglu(gu, topk_weights, sorted_token_ids, num_tokens_post_padded, h, codes=None, scales=None, stream=None):
+    """h[r] = w silu(gu[r, :I]) gu[r, I:] with the routing weight w of row r's assignment, padding rows zeros.
+    gu [capacity, 2I], topk_weights FP32 [M, topk], h [capacity, I] of gu's type.  With codes uint8
+    [capacity, 2I] and scales uint8 [capacity, 2I/32], gu is held there in 8 bits."""
+    rc = (_ext_module or _ext()).swiglu(gu, topk_weights, sorted_token_ids, num_tokens_post_padded, h, codes, scales,
+                                        None if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def chord_swiglu_backward(dh, gu, codes, scales, topk_weights, sorted_positions, sorted_token_ids,
+                          num_tokens_post_padded, dgu, dweights, h=None, stream=None):
+    """The gradients of chord_swiglu: dgu [capacity, 2I] and dweights FP32 [M, topk] from dh [capacity, I] and gu, or
+    (gu None) its codes and scales; h [capacity, I]: the forward pass's rows again, of what gu or its codes hold."""
+    rc = (_ext_module or _ext()).swiglu_backward(dh, gu, codes, scales, topk_weights, sorted_positions,
+                                                 sorted_token_ids, num_tokens_post_padded, dgu, dweights, h,
+                                                 None if stream is None else _stream(stream))
     if rc:
         _check(rc)

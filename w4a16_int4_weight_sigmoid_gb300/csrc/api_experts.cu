@@ -42,6 +42,12 @@ int check_mx(const char* what, int K) {
   return CHORD_OK;
 }
 
+int check_codes(const uint8_t* codes, const uint8_t* scales) {
+  if (!codes || !scales) return fail(CHORD_ERR_INVALID_ARG, "null pointer: codes or scales");
+  if (!aligned16(codes)) return fail(CHORD_ERR_INVALID_ARG, "codes must be 16-byte aligned");
+  return CHORD_OK;
+}
+
 // The sizes and buffers that the 16-bit products share.
 int check_product(int dtype, int E, int N, int K, const int32_t* counts, const int32_t* offsets, size_t capacity,
                   const void* ws, size_t ws_bytes) {
@@ -289,6 +295,95 @@ int chord_expert_wgrad(const void* dout, const void* x, int dtype, int64_t dout_
   g.E = E_local, g.N = N, g.K = K, g.capacity = static_cast<int>(capacity);
   g.dw = dw, g.ws = workspace, g.test_timeout = chord::force_timeout(), g.status = dev_status;
   return done(chord::expert_wgrad_launch(g, stream_of(stream)), "weight gradient launch");
+}
+
+int chord_mxfp8_quantize(const void* x, int dtype, int64_t x_stride, int64_t rows, int K, uint8_t* codes,
+                         uint8_t* scales, void* stream) {
+  if (!chord::dtype_bytes(dtype)) return fail(CHORD_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (rows < 0) return fail(CHORD_ERR_INVALID_ARG, "rows < 0");
+  int rc = check_mx("quantize", K);
+  if (rc || rows == 0) return rc;
+  if ((rc = check_matrix("x", x, dtype, x_stride, K, false))) return rc;
+  if ((rc = check_codes(codes, scales))) return rc;
+  return done(chord::mxfp8_quantize_launch(x, dtype, x_stride, rows, K, codes, scales, stream_of(stream)),
+              "quantize launch");
+}
+
+int chord_mxfp8_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, void* out, int dtype,
+                           int64_t out_stride, void* stream) {
+  if (!chord::dtype_bytes(dtype)) return fail(CHORD_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (rows < 0) return fail(CHORD_ERR_INVALID_ARG, "rows < 0");
+  int rc = check_mx("dequantize", K);
+  if (rc || rows == 0) return rc;
+  if ((rc = check_matrix("out", out, dtype, out_stride, K, true))) return rc;
+  if ((rc = check_codes(codes, scales))) return rc;
+  return done(chord::mxfp8_dequantize_launch(codes, scales, rows, K, out, dtype, out_stride, stream_of(stream)),
+              "dequantize launch");
+}
+
+int chord_mxfp8_permute(const uint8_t* codes, const uint8_t* scales, const int32_t* sorted_token_ids,
+                        const int32_t* num_tokens_post_padded, int M, int topk, int K, size_t capacity, void* out,
+                        int dtype, int64_t out_stride, void* stream) {
+  int rc = check_rows(dtype, M, topk, K, capacity);
+  if (rc) return rc;
+  if ((rc = check_mx("permute", K))) return rc;
+  if (M == 0 || capacity == 0) return CHORD_OK;
+  if ((rc = check_matrix("out", out, dtype, out_stride, K, true))) return rc;
+  if ((rc = check_codes(codes, scales))) return rc;
+  if (!sorted_token_ids || !num_tokens_post_padded) return fail(CHORD_ERR_INVALID_ARG, "null pointer");
+  return done(chord::mxfp8_permute_launch(codes, scales, K, sorted_token_ids, num_tokens_post_padded, M, topk,
+                                          static_cast<int>(capacity), out, dtype, out_stride, stream_of(stream)),
+              "permute launch");
+}
+
+int chord_swiglu(const void* gu, int dtype, int64_t gu_stride, const float* topk_weights,
+                 const int32_t* sorted_token_ids, const int32_t* num_tokens_post_padded, int M, int topk, int I,
+                 size_t capacity, void* h, int64_t h_stride, uint8_t* codes, uint8_t* scales, void* stream) {
+  int rc = check_rows(dtype, M, topk, I, capacity);
+  if (rc) return rc;
+  if (I > (1 << 23)) return fail(CHORD_ERR_INVALID_ARG, "I=%d > 2^23", I);
+  const bool keep = codes || scales;
+  if (keep && (rc = check_mx("swiglu in 8 bits", I))) return rc;
+  if (M == 0 || capacity == 0) return CHORD_OK;
+  if ((rc = check_matrix("gu", gu, dtype, gu_stride, 2 * I, false))) return rc;
+  if ((rc = check_matrix("h", h, dtype, h_stride, I, true))) return rc;
+  if (keep && (rc = check_codes(codes, scales))) return rc;
+  if (!topk_weights || !sorted_token_ids || !num_tokens_post_padded) return fail(CHORD_ERR_INVALID_ARG, "null pointer");
+  chord::Swiglu s{};
+  s.gu = gu, s.w = topk_weights, s.sorted = sorted_token_ids, s.ntpp = num_tokens_post_padded;
+  s.h = h, s.codes = codes, s.scales = scales, s.ldg = gu_stride, s.ldh = h_stride;
+  s.rows = static_cast<int>(capacity), s.I = I, s.assignments = M * topk;
+  return done(chord::swiglu_launch(s, dtype, false, stream_of(stream)), "swiglu launch");
+}
+
+int chord_swiglu_backward(const void* dh, int dtype, int64_t dh_stride, const void* gu, int64_t gu_stride,
+                          const uint8_t* codes, const uint8_t* scales, const float* topk_weights,
+                          const int32_t* sorted_positions, const int32_t* sorted_token_ids,
+                          const int32_t* num_tokens_post_padded, int M, int topk, int I, size_t capacity, void* dgu,
+                          int64_t dgu_stride, float* dweights, void* h, int64_t h_stride, void* stream) {
+  int rc = check_rows(dtype, M, topk, I, capacity);
+  if (rc) return rc;
+  if (I > (1 << 23)) return fail(CHORD_ERR_INVALID_ARG, "I=%d > 2^23", I);
+  const bool keep = codes || scales;
+  if (keep && gu) return fail(CHORD_ERR_INVALID_ARG, "gu and its codes: one of them");
+  if (keep && (rc = check_mx("swiglu in 8 bits", I))) return rc;
+  if (M == 0) return CHORD_OK;
+  if (!dweights) return fail(CHORD_ERR_INVALID_ARG, "null pointer: dweights");
+  if (capacity == 0)
+    return done(cudaMemsetAsync(dweights, 0, sizeof(float) * M * topk, stream_of(stream)), "gradient of no rows");
+  if ((rc = check_matrix("dh", dh, dtype, dh_stride, I, false))) return rc;
+  if (keep ? (rc = check_codes(codes, scales)) : (rc = check_matrix("gu", gu, dtype, gu_stride, 2 * I, false))) return rc;
+  if ((rc = check_matrix("dgu", dgu, dtype, dgu_stride, 2 * I, true))) return rc;
+  if (h && (rc = check_matrix("h", h, dtype, h_stride, I, true))) return rc;
+  if (!topk_weights || !sorted_positions || !sorted_token_ids || !num_tokens_post_padded)
+    return fail(CHORD_ERR_INVALID_ARG, "null pointer");
+  chord::Swiglu s{};
+  s.gu = gu, s.dh = dh, s.w = topk_weights, s.sorted = sorted_token_ids, s.ntpp = num_tokens_post_padded;
+  s.pos = sorted_positions, s.h = h, s.dgu = dgu, s.dw = dweights;
+  s.codes = const_cast<uint8_t*>(codes), s.scales = const_cast<uint8_t*>(scales);   // (read only)
+  s.ldg = gu_stride, s.ldh = h_stride, s.ldd = dh_stride, s.ldo = dgu_stride;
+  s.rows = static_cast<int>(capacity), s.I = I, s.assignments = M * topk;
+  return done(chord::swiglu_launch(s, dtype, true, stream_of(stream)), "swiglu backward launch");
 }
 
 }  // extern "C"

@@ -153,4 +153,32 @@ size_t expert_gemm_workspace_bytes();
 cudaError_t expert_gemm_launch(const ExpertGemm& g, cudaStream_t st);
 cudaError_t expert_wgrad_launch(const ExpertWgrad& g, cudaStream_t st);
 
+// Rows in 8 bits (MXFP8): codes and scales of rows, and back; token rows into
+// the expert order.
+cudaError_t mxfp8_quantize_launch(const void* x, int dtype, long long ldx, long long rows, int K, uint8_t* codes,
+                                  uint8_t* scales, cudaStream_t st);
+cudaError_t mxfp8_dequantize_launch(const uint8_t* codes, const uint8_t* scales, long long rows, int K, void* out,
+                                    int dtype, long long ldo, cudaStream_t st);
+cudaError_t mxfp8_permute_launch(const uint8_t* codes, const uint8_t* scales, int K, const int32_t* sorted,
+                                 const int32_t* ntpp, int M, int topk, int rows, void* out, int dtype, long long ldo,
+                                 cudaStream_t st);
+
+// The gated activation and its gradient; see csrc/swiglu.cu.
+struct Swiglu {
+  const void* gu;
+  const void* dh;
+  const float* w;
+  const int32_t* sorted;
+  const int32_t* ntpp;
+  const int32_t* pos;
+  void* h;
+  void* dgu;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* dw;
+  long long ldg, ldh, ldd, ldo;
+  int rows, I, assignments;
+};
+cudaError_t swiglu_launch(const Swiglu& s, int dtype, bool backward, cudaStream_t st);
+
 }  // namespace chord

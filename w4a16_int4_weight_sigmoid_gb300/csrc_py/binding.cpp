@@ -238,6 +238,83 @@ int expert_wgrad(PyObject* const* a) {
                             stream(a[7]));
 }
 
+int mxfp8_quantize(PyObject* const* a) {
+  const Rows x(a[0], "x");
+  uint8_t *codes = bytes(a[1], x.n * x.h, "codes"), *scales = bytes(a[2], x.n * x.h / 32, "scales");
+  here(a[0], a[1], a[2]);
+  return chord_mxfp8_quantize(x.p, x.dtype, x.stride, x.n, narrow(x.h, "K"), codes, scales, stream(a[3]));
+}
+
+int mxfp8_dequantize(PyObject* const* a) {
+  const Rows out(a[2], "out");
+  const uint8_t *codes = bytes(a[0], out.n * out.h, "codes"), *scales = bytes(a[1], out.n * out.h / 32, "scales");
+  here(a[0], a[1], a[2]);
+  return chord_mxfp8_dequantize(codes, scales, out.n, narrow(out.h, "K"), out.p, out.dtype, out.stride, stream(a[3]));
+}
+
+int mxfp8_permute(PyObject* const* a) {
+  const Rows out(a[6], "out");
+  const int k = narrow(integer(a[5]), "topk");
+  const at::Tensor& pos = tensor(a[2], "sorted_positions");
+  if (k < 1 || pos.numel() % k != 0) raise(PyExc_ValueError, "sorted_positions does not hold topk=%d values a token", k);
+  const int64_t M = pos.numel() / k;
+  const uint8_t *codes = bytes(a[0], M * out.h, "codes"), *scales = bytes(a[1], M * out.h / 32, "scales");
+  const int32_t *sorted = ints(a[3], out.n, "sorted_token_ids"), *total = ints(a[4], 1, "num_tokens_post_padded");
+  here(a[0], a[1], a[3], a[4], a[6]);
+  return chord_mxfp8_permute(codes, scales, sorted, total, narrow(M, "tokens"), k, narrow(out.h, "K"), out.n, out.p,
+                             out.dtype, out.stride, stream(a[7]));
+}
+
+// The codes and scales of [rows, cols], or NULL for None.
+void kept(PyObject* c, PyObject* s, int64_t rows, int64_t cols, uint8_t*& codes, uint8_t*& scales) {
+  codes = c == Py_None ? nullptr : bytes(c, rows * cols, "codes");
+  scales = s == Py_None ? nullptr : bytes(s, rows * cols / 32, "scales");
+}
+
+int swiglu(PyObject* const* a) {
+  int64_t M, k;
+  const Rows gu(a[0], "gu"), h(a[4], "h");
+  const float* w = weights(a[1], M, k);
+  if (h.dtype != gu.dtype) raise(PyExc_TypeError, "h is of another type");
+  if (gu.h != 2 * h.h || gu.n != h.n)
+    raise(PyExc_ValueError, "gu [%lld, %lld] must be [%lld, %lld] for this h", (long long)gu.n, (long long)gu.h,
+          (long long)h.n, 2 * (long long)h.h);
+  uint8_t *codes, *scales;
+  kept(a[5], a[6], gu.n, gu.h, codes, scales);
+  const int32_t *sorted = ints(a[2], gu.n, "sorted_token_ids"), *total = ints(a[3], 1, "num_tokens_post_padded");
+  here(a[0], a[1], a[2], a[3], a[4], a[5], a[6]);
+  return chord_swiglu(gu.p, gu.dtype, gu.stride, w, sorted, total, narrow(M, "tokens"), narrow(k, "topk"),
+                      narrow(h.h, "I"), gu.n, h.p, h.stride, codes, scales, stream(a[7]));
+}
+
+int swiglu_backward(PyObject* const* a) {
+  int64_t M, k;
+  const Rows dh(a[0], "dh"), dgu(a[8], "dgu");
+  const float* w = weights(a[4], M, k);
+  if (dgu.dtype != dh.dtype) raise(PyExc_TypeError, "dgu is of another type");
+  if (dgu.h != 2 * dh.h || dgu.n != dh.n)
+    raise(PyExc_ValueError, "dgu must be [%lld, %lld]", (long long)dh.n, 2 * (long long)dh.h);
+  void *gu = nullptr, *h = nullptr;
+  int64_t gu_stride = 0, h_stride = 0;
+  if (a[1] != Py_None) {
+    const Rows r(a[1], "gu", dgu, dh.n);
+    gu = r.p, gu_stride = r.stride;
+  }
+  if (a[10] != Py_None) {
+    const Rows r(a[10], "h", dh, dh.n);
+    h = r.p, h_stride = r.stride;
+  }
+  uint8_t *codes, *scales;
+  kept(a[2], a[3], dh.n, dgu.h, codes, scales);
+  const int32_t *pos = ints(a[5], M * k, "sorted_positions"), *sorted = ints(a[6], dh.n, "sorted_token_ids");
+  const int32_t* total = ints(a[7], 1, "num_tokens_post_padded");
+  float* dw = values<float>(a[9], at::kFloat, M * k, "dweights");
+  here(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10]);
+  return chord_swiglu_backward(dh.p, dh.dtype, dh.stride, gu, gu_stride, codes, scales, w, pos, sorted, total,
+                               narrow(M, "tokens"), narrow(k, "topk"), narrow(dh.h, "I"), dh.n, dgu.p, dgu.stride, dw,
+                               h, h_stride, stream(a[11]));
+}
+
 template <int (*kCall)(PyObject* const*), int kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != kArgs) {
@@ -270,6 +347,11 @@ PyMethodDef kMethods[] = {
     method<moe_gemm, 13>("moe_gemm"),
     method<expert_gemm, 9>("expert_gemm"),
     method<expert_wgrad, 8>("expert_wgrad"),
+    method<mxfp8_quantize, 4>("mxfp8_quantize"),
+    method<mxfp8_dequantize, 4>("mxfp8_dequantize"),
+    method<mxfp8_permute, 8>("mxfp8_permute"),
+    method<swiglu, 8>("swiglu"),
+    method<swiglu_backward, 12>("swiglu_backward"),
     {nullptr, nullptr, 0, nullptr},
 };
 
