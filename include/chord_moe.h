@@ -517,10 +517,11 @@ int chord_mxfp4_moe_gemm(const void* rows, size_t rows_bytes, const void* packed
  *   *_stride   in elements, multiples of 8; rows do not overlap.  Bases are
  *              16-byte aligned
  *   capacity   rows of x, dout and out
- *   workspace  chord_expert_gemm_workspace_bytes() bytes, 16-byte aligned,
- *              zeroed once when allocated; every call leaves its counters
- *              zero.  Calls that may overlap need their own.  After a call
- *              that recorded CHORD_ERR_TIMEOUT zero it again.
+ *   workspace  chord_expert_gemm_workspace_bytes() bytes, 16-byte aligned; its
+ *              first CHORD_EXPERT_GEMM_COUNTER_BYTES are zeroed once when it
+ *              is allocated, and every call leaves them zero.  Calls that may
+ *              overlap need their own.  After a call that recorded
+ *              CHORD_ERR_TIMEOUT zero them again.
  *   dev_status device int for errors found on the device (may be NULL):
  *              CHORD_ERR_INVALID_ARG where counts and offsets are no such
  *              order of `capacity` rows (nothing is computed then), a bounded
@@ -528,6 +529,7 @@ int chord_mxfp4_moe_gemm(const void* rows, size_t rows_bytes, const void* packed
  * Counts are read on the device, so the call never waits for the host.
  * Results are the same from call to call.  E_local <= 1024.
  */
+#define CHORD_EXPERT_GEMM_COUNTER_BYTES 1024
 size_t chord_expert_gemm_workspace_bytes(void);
 int chord_expert_gemm(const void* x, int dtype, int64_t x_stride, const void* w, int64_t w_stride,
                       int64_t w_expert_stride, int E_local, int N, int K, int transpose_w,

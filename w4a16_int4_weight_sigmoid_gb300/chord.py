@@ -38,6 +38,9 @@ CHORD_DTYPE_BF16 = 0
 CHORD_DTYPE_FP16 = 1
 CHORD_DTYPE_FP32 = 2
 
+# what of the experts' product's workspace has to be zero when it is first used
+CHORD_EXPERT_GEMM_COUNTER_BYTES = 1024
+
 CHORD_PATH_AUTO = 0
 CHORD_PATH_SMALL_M = 1
 CHORD_PATH_LARGE_M = 2
@@ -533,7 +536,7 @@ def chord_expert_gemm(x, w, expert_counts, expert_offsets, out, workspace, trans
                       stream=None):
     """out[r] = w[e] @ x[r] (transpose_w: w[e].T @ x[r]) for every expert e's rows r.  x and out are rows in expert
     order, w [E, N, K], all BF16 or FP16; workspace: uint8 tensor of chord_expert_gemm_workspace_bytes() bytes,
-    zeroed once when allocated."""
+    its first CHORD_EXPERT_GEMM_COUNTER_BYTES zeroed once when allocated."""
     rc = (_ext_module or _ext()).expert_gemm(x, w, expert_counts, expert_offsets, out, workspace, int(transpose_w),
                                              dev_status, None if stream is None else _stream(stream))
     if rc:

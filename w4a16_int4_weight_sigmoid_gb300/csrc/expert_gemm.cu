@@ -598,7 +598,7 @@ cudaError_t launch(const Maps& maps, const Args& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t expert_gemm_workspace_bytes() { return 256; }
+size_t expert_gemm_workspace_bytes() { return CHORD_EXPERT_GEMM_COUNTER_BYTES; }
 
 cudaError_t expert_gemm_launch(const ExpertGemm& g, cudaStream_t st) {
   Args a{};

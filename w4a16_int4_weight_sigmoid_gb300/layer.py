@@ -5,7 +5,9 @@ computes).  W4A16MoELayer uploads its weights once, repacked on the device by
 chord_w4a16_prepack; forward() is one chord_moe_layer call.  MXFP4MoELayer
 keeps MXFP4 weights and runs the experts with both operands in 4 bits.
 ExpertOrder holds a routing's aligned expert order, and permute_rows /
-unpermute_rows move rows into it and back with gradients.
+unpermute_rows move rows into it and back with gradients.  expert_product and
+expert_mlp train the experts in 16 bits between the two, expert_mlp with the
+activations that its backward pass needs held in 8.
 """
 from __future__ import annotations
 
@@ -89,7 +91,8 @@ class ExpertOrder:
 
     topk_weights [M, topk] FP32 and topk_ids [M, topk]; sorted_token_ids [capacity],
     sorted_positions [M * topk], num_tokens_post_padded [1], expert_counts [E_local]
-    and expert_offsets [E_local + 1], as chord_moe_align defines them."""
+    and expert_offsets [E_local + 1], as chord_moe_align defines them; dev_status [1], for
+    errors that the experts' products find on the device."""
 
     def __init__(self, M: int, topk: int, expert_begin: int, E_local: int, block_m: int = 16, device="cuda"):
         self.M, self.topk, self.expert_begin, self.E_local, self.block_m = M, topk, expert_begin, E_local, block_m
@@ -103,6 +106,7 @@ class ExpertOrder:
         self.num_tokens_post_padded = torch.empty(1, **i32)
         self.expert_counts = torch.empty(E_local, **i32)
         self.expert_offsets = torch.empty(E_local + 1, **i32)
+        self.dev_status = torch.zeros(1, **i32)
         nbytes = chord.chord_moe_align_workspace_bytes(M, topk, E_local)
         self._ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
         self._arrays = (self.topk_weights, self.topk_ids, self.sorted_token_ids, self.sorted_positions,
@@ -124,7 +128,7 @@ class ExpertOrder:
         if logits.dim() != 2 or logits.shape[0] != self.M:
             raise ValueError(f"logits must be [{self.M}, E_total] for this order, got {list(logits.shape)}")
         if stream not in self._streams and isinstance(stream, torch.cuda.Stream):
-            for t in (*self._arrays, *([] if self._ws is None else [self._ws])):
+            for t in (*self._arrays, self.dev_status, *([] if self._ws is None else [self._ws])):
                 t.record_stream(stream)
             self._streams.add(stream)
         if self.M == 0:   # arrays without elements have no address to give
@@ -207,6 +211,141 @@ def unpermute_rows(y, weights, order: ExpertOrder):
     if y.shape[0] != order.capacity:
         raise ValueError(f"y must hold the {order.capacity} rows of its order, got {y.shape[0]}")
     return _Unpermute.apply(y, weights, order)
+
+
+def _rows16(t):
+    """A gradient as the products read rows: 16-byte parts, rows apart from one another."""
+    t = _unit_columns(t)
+    fine = t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or (t.stride(0) % 8 == 0 and t.stride(0) >= t.shape[1]))
+    return t if fine else t.clone(memory_format=torch.contiguous_format)
+
+
+class _Products:
+    """The products of one pass over an order's experts.  Their workspace is memory of the pass
+    (or of the graph that captures it), so that passes on several streams share none."""
+
+    def __init__(self, counts, offsets, status):
+        self.counts, self.offsets, self.status = counts, offsets, status
+        self.ws = torch.empty(chord.chord_expert_gemm_workspace_bytes(), dtype=torch.uint8, device=counts.device)
+        self.ws[:chord.CHORD_EXPERT_GEMM_COUNTER_BYTES].zero_()
+
+    def rows(self, x, w, transpose=False, out=None):
+        if out is None:
+            out = torch.empty((x.shape[0], w.shape[2 if transpose else 1]), dtype=x.dtype, device=x.device)
+        chord.chord_expert_gemm(x, w, self.counts, self.offsets, out, self.ws, transpose, self.status)
+        return out
+
+    def weights(self, dout, x, like):
+        dw = torch.empty_like(like, memory_format=torch.contiguous_format)
+        chord.chord_expert_wgrad(dout, x, self.counts, self.offsets, dw, self.ws, self.status)
+        return dw
+
+
+class _ExpertProduct(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, w, order):
+        ctx.status = order.dev_status
+        ctx.save_for_backward(rows, w, *order._saved(order.expert_counts, order.expert_offsets))
+        # rows that are no expert's are not written by the call: zeros
+        out = torch.zeros((order.capacity, w.shape[1]), dtype=rows.dtype, device=rows.device)
+        return _Products(order.expert_counts, order.expert_offsets, order.dev_status).rows(rows, w, out=out)
+
+    @staticmethod
+    @_once
+    def backward(ctx, dout):
+        rows, w, counts, offsets = ctx.saved_tensors
+        products, dout = _Products(counts, offsets, ctx.status), _rows16(dout)
+        drows = dw = None
+        if ctx.needs_input_grad[0]:
+            drows = products.rows(dout, w, True, torch.zeros(rows.shape, dtype=rows.dtype, device=rows.device))
+        if ctx.needs_input_grad[1]:
+            dw = products.weights(dout, rows, w)
+        return drows, dw, None
+
+
+def expert_product(rows, w, order: ExpertOrder):
+    """rows [order.capacity, K] times each expert's w [E_local, N, K] -> [order.capacity, N], zeros in rows that
+    are no expert's; BF16 or FP16, differentiable once in rows and w."""
+    if rows.shape[0] != order.capacity or w.shape[0] != order.E_local:
+        raise ValueError(f"rows must hold the {order.capacity} rows of the order and w its {order.E_local} experts, "
+                         f"got {rows.shape[0]} and {w.shape[0]}")
+    return _ExpertProduct.apply(rows, w, order)
+
+
+class _ExpertMLP(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weights, w13, w2, order, held):
+        o, (M, H), I, cap = order, x.shape, w2.shape[2], order.capacity
+        empty = lambda *shape, dtype=x.dtype: torch.empty(shape, dtype=dtype, device=x.device)
+        codes8 = lambda n, k: (empty(n, k, dtype=torch.uint8), empty(n, k // 32, dtype=torch.uint8))
+        products = _Products(o.expert_counts, o.expert_offsets, o.dev_status)
+        rows, h, out = empty(cap, H), empty(cap, I), empty(M, H)
+        chord.chord_moe_permute(x, o.sorted_positions, o.sorted_token_ids, o.num_tokens_post_padded, o.topk, rows)
+        gu = products.rows(rows, w13)
+        kept = codes8(cap, 2 * I) if held else ()
+        chord.chord_swiglu(gu, weights, o.sorted_token_ids, o.num_tokens_post_padded, h, *kept)
+        y = products.rows(h, w2)
+        chord.chord_moe_permute_backward(y, o.sorted_positions, o.topk, out)   # the sum over a token's rows
+        if held:
+            x8 = codes8(M, H)
+            chord.chord_mxfp8_quantize(x, *x8)
+            kept = (*x8, *kept)
+        else:
+            kept = (x, gu)
+        ctx.held, ctx.topk, ctx.cap, ctx.status, ctx.dtype = held, o.topk, cap, o.dev_status, x.dtype
+        ctx.save_for_backward(weights, w13, w2, *o._saved(o.sorted_positions, o.sorted_token_ids,
+                                                         o.num_tokens_post_padded, o.expert_counts, o.expert_offsets),
+                              *kept)
+        return out
+
+    @staticmethod
+    @_once
+    def backward(ctx, dout):
+        weights, w13, w2, positions, token_ids, total, counts, offsets, *kept = ctx.saved_tensors
+        M, (twoI, H) = dout.shape[0], w13.shape[1:]
+        empty = lambda *shape: torch.empty(shape, dtype=ctx.dtype, device=dout.device)
+        products = _Products(counts, offsets, ctx.status)
+        dy, dgu, h, dweights = empty(ctx.cap, H), empty(ctx.cap, twoI), empty(ctx.cap, twoI // 2), torch.empty_like(weights)
+        chord.chord_moe_permute(_unit_columns(dout), positions, token_ids, total, ctx.topk, dy)
+        dh = products.rows(dy, w2, True)
+        gu, codes = (None, kept[2:]) if ctx.held else (kept[1], (None, None))
+        chord.chord_swiglu_backward(dh, gu, *codes, weights, positions, token_ids, total, dgu, dweights, h)
+        dx = dw13 = dw2 = None
+        if ctx.needs_input_grad[3]:
+            dw2 = products.weights(dy, h, w2)
+        if ctx.needs_input_grad[2]:
+            rows = dy   # (used up)
+            if ctx.held:
+                chord.chord_mxfp8_permute(*kept[:2], positions, token_ids, total, ctx.topk, rows)
+            else:
+                chord.chord_moe_permute(kept[0], positions, token_ids, total, ctx.topk, rows)
+            dw13 = products.weights(dgu, rows, w13)
+        if ctx.needs_input_grad[0]:
+            dx = empty(M, H)
+            chord.chord_moe_permute_backward(products.rows(dgu, w13, True), positions, ctx.topk, dx)
+        return dx, dweights if ctx.needs_input_grad[1] else None, dw13, dw2, None, None
+
+
+def expert_mlp(x, weights, w13, w2, order: ExpertOrder, held_in_8_bits: bool = True):
+    """The order's SiLU-gated experts over tokens x [M, H], summed back with the routing weights FP32 [M, topk]:
+    out[t] = sum_j weights[t, j] w2[e] (silu(gate) * up), gate and up the halves of w13[e] x[t], e the expert of
+    assignment (t, j) where it is local.  w13 [E_local, 2I, H] (rows 0..I-1 gate) and w2 [E_local, H, I]; x, w13 and
+    w2 BF16 or FP16, H and I multiples of 8.  Differentiable once in x, weights, w13 and w2.
+
+    The backward pass keeps x and the rows of gate and up: in 8 bits (MXFP8; H and I multiples of 32), which costs
+    the gradients of the weights and of the activation a relative rounding of up to 2^-4 per kept value, or as they
+    are.  The output is the same either way."""
+    if x.shape[0] != order.M or w13.shape[0] != order.E_local or w2.shape[0] != order.E_local:
+        raise ValueError(f"x must hold the order's {order.M} tokens and w13 and w2 its {order.E_local} experts, got "
+                         f"{x.shape[0]}, {w13.shape[0]} and {w2.shape[0]}")
+    if w13.shape[1] != 2 * w2.shape[2] or w13.shape[2] != x.shape[1] or w2.shape[1] != x.shape[1]:
+        raise ValueError(f"w13 {list(w13.shape)} and w2 {list(w2.shape)} must be [E, 2I, {x.shape[1]}] and "
+                         f"[E, {x.shape[1]}, I]")
+    if weights.shape != (order.M, order.topk):
+        raise ValueError(f"weights must be [{order.M}, {order.topk}], got {list(weights.shape)}")
+    if held_in_8_bits and (x.shape[1] % 32 or w2.shape[2] % 32):
+        raise ValueError(f"H={x.shape[1]} and I={w2.shape[2]} must be multiples of 32 to be held in 8 bits")
+    return _ExpertMLP.apply(_unit_columns(x), weights.contiguous(), w13, w2, order, held_in_8_bits)
 
 
 def quantize_mxfp4(w, stream=None):
