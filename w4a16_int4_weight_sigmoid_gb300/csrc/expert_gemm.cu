@@ -47,24 +47,29 @@ constexpr int kABytes = 128 * kStageK * 2;
 constexpr int kBlockBytes = 64 * kStageK * 2;      // 64 contiguous M or N values x 64 of the contraction
 constexpr int kMaxStages = 10, kMaxAcc = 8;
 __host__ __device__ constexpr int stage_bytes(int tok) { return kABytes + tok / 2 * kStageK * 2; }
-constexpr int kStageBudget = 6 * stage_bytes(kMaxTok);
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-constexpr int kItemWarp = 2, kZeroWarp = 3;
+constexpr int kItemWarp = 2;
+// Two zeroing warps take items in turn: each one's release to the other CTA's
+// MMAs takes about 0.8 us, half of a short item's time (few rows 489 -> 457 us).
+constexpr int kZeroWarp0 = 3, kZeroWarp1 = kEpiWarp0 + kEpiWarps;
+constexpr int kThreads = 32 * (kZeroWarp1 + 1);
 constexpr int kItemSlots = 8;
 constexpr int kMaxExperts = 1024;
 constexpr int kTmemCols = 512;
 constexpr int kGroupTiles = 8;         // row tiles that are taken together
 // An epilogue warp's staging: product 32 tokens x 32 weights (rows of 80
-// bytes spread over the banks); gradient 32 rows of 128 bytes.
-constexpr int kOutPitch = 80;
+// bytes spread over the banks); gradient two times 32 rows of 128 bytes, so that
+// one is filled while the other leaves, at the cost of a stage.
+constexpr int kOutPitch = 80, kOutBuf = 32 * 128;
 template <Mode kMode>
-constexpr int kOutBytes = kMode == kGradient ? 32 * 128 : 32 * kOutPitch;
+constexpr int kOutBytes = kMode == kGradient ? 2 * kOutBuf : 32 * kOutPitch;
 template <Mode kMode>
-constexpr int kSmemBytes = kStageBudget + kEpiWarps * kOutBytes<kMode> + 1024;
-static_assert(kMaxStages * stage_bytes(32) <= kStageBudget, "stage budget");
+constexpr int kStageBudget = (kMode == kGradient ? 5 : 6) * stage_bytes(kMaxTok);
+template <Mode kMode>
+constexpr int kSmemBytes = kStageBudget<kMode> + kEpiWarps * kOutBytes<kMode> + 1024;
+static_assert(kMaxStages * stage_bytes(32) <= kStageBudget<kProduct>, "stage budget");
 static_assert(kSmemBytes<kProduct> + (kMaxExperts + 1) * 4 + 2048 <= 232448, "shared memory budget");
-static_assert(kSmemBytes<kGradient> + 1536 <= 232448, "shared memory budget");
+static_assert(kSmemBytes<kGradient> + 1024 <= 232448, "shared memory budget");
 static_assert(3 * kThreads >= kMaxExperts, "three experts per thread at most");
 
 struct Args {
@@ -234,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   constexpr bool kGrad = kMode == kGradient;
   constexpr bool kMnA = kMode != kProduct, kMnB = kGrad;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[2][kMaxStages];   // tail: of each zeroing warp
   __shared__ __align__(8) uint64_t tfull[kMaxAcc], tempty[kMaxAcc], done_bar;
   __shared__ __align__(8) uint64_t item_full[kItemSlots], item_empty[kItemSlots];
   __shared__ Seg item_slots[kItemSlots];
@@ -251,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&full[s], 2);              // of the leading CTA: each CTA's bytes, or its zeroing warp
       mbar_init(&empty[s], 1);
-      mbar_init(&tail[s], 1);
+      mbar_init(&tail[0][s], 1);
+      mbar_init(&tail[1][s], 1);
     }
     for (int b = 0; b < kMaxAcc; ++b) {
       mbar_init(&tfull[b], 1);
@@ -260,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     mbar_init(&done_bar, 1);
     for (int q = 0; q < kItemSlots; ++q) {
       mbar_init(&item_full[q], 1);
-      mbar_init(&item_empty[q], 1 + (rank == 0 ? 1 : 0) + (kGrad ? 1 : 0) + kEpiWarps);
+      mbar_init(&item_empty[q], 1 + (rank == 0 ? 1 : 0) + (kGrad ? 2 : 0) + kEpiWarps);
     }
     fence_mbar_init();
   }
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   if (kGrad) tok = kMaxTok;
   tok = order_ok ? tok : 32;
   const int items = !order_ok ? 0 : kGrad ? a.E * a.m_tiles * a.n_tiles : prefix[a.E];
-  const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget / stage);
+  const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget<kMode> / stage);
   const int n_acc = min(kMaxAcc, kTmemCols / tok);
   ItemRing ring{item_full, item_empty, item_slots, a.test_timeout ? kTestWaitPolls : kWaitPolls, 0, 0};
   Seg w;
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // count on the leading CTA's barrier; a gradient's last box completes on
     // this CTA's own, for the zeroing warp.
     const uint32_t full0 = cluster_addr(&full[0], 0);
-    int it = 0, st = 0, ph = 0;
+    int it = 0, st = 0, ph = 0, turn = 0;
     while (ring.next(w, ok, a.status)) {
       const int half = w.cols >> 1;
       const CUtensorMap* mb = &maps.b[kGrad ? 0 : (half >> 4) - 1];
@@ -353,8 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int k0 = u * kStageK;
         uint32_t bar = full0 + 8 * st;
         if (kGrad && w.rows - k0 < kStageK && ((w.rows - k0) & 15)) {
-          bar = smem_u32(&tail[st]);
-          mbar_arrive_expect_tx_elect(&tail[st], bytes);
+          bar = smem_u32(&tail[turn][st]);
+          mbar_arrive_expect_tx_elect(&tail[turn][st], bytes);
+          turn ^= 1;
         } else {
           mbar_arrive_expect_tx_cluster_elect(bar, bytes);
         }
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t d = tmem_base + acc * tok;
       const uint32_t idesc = idesc_pair(!kF16, kMnA, kMnB, w.cols);
       uint32_t accumulate = 0;
-      if (use >= 1) ok = __all_sync(0xffffffffu, mbar_wait_cluster(&tempty[acc], (use - 1) & 1, a.status));
+      if (use >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&tempty[acc], (use - 1) & 1, a.status));
       tc_fence_after();
       for (int u = 0; ok && u < w.stages; ++u) {
         // (a last box was written by threads of the other CTA too)
@@ -439,17 +446,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       item += clusters;
       if (++slot == kItemSlots) slot = 0, ph ^= 1, first = false;
     }
-  } else if (kGrad && warp == kZeroWarp) {
+  } else if (kGrad && (warp == kZeroWarp0 || warp == kZeroWarp1)) {
     // ------------------------------------------- rows behind an expert's last
     const uint32_t full0 = cluster_addr(&full[0], 0);
     int st = 0;
-    uint32_t tail_ph = 0;                // a slot's phase turns when it holds a last box
+    const int mine = warp == kZeroWarp1;   // boxes are handed to the two warps in turn
+    int turn = 0;
+    uint32_t tail_ph = 0;                // of this warp's barriers: one turns when its slot holds a last box
     while (ring.next(w, ok, a.status)) {
       st = (st + w.stages) % n_stages;
       const int last = w.rows % kStageK;
       if (!(last & 15)) continue;
+      turn ^= 1;
+      if (turn == mine) continue;        // the other warp's: turn was its number
+      // Every phase of a warp's barriers is waited for, in order.
       const int at = (st ? st : n_stages) - 1;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&tail[at], (tail_ph >> at) & 1, a.status)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&tail[mine][at], (tail_ph >> at) & 1, a.status)))) break;
       tail_ph ^= 1u << at;
       // rows last .. next multiple of 16 of the four blocks of 64 values
       const uint32_t base = smem0 + at * stage + (lane & 7) * 16;
@@ -460,15 +472,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           st_shared_v4(base + b * kBlockBytes + r * 128, 0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(full0 + 8 * at);
+      if (lane == 0) mbar_arrive_release_cluster(full0 + 8 * at);
     }
-  } else if (warp >= kEpiWarp0) {
+  } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3, t = (warp - kEpiWarp0) / 4;   // TMEM lane quarter; which of the column chunks
-    const uint32_t out_stage = smem0 + kStageBudget + (warp - kEpiWarp0) * kOutBytes<kMode>;
+    const uint32_t out_stage = smem0 + kStageBudget<kMode> + (warp - kEpiWarp0) * kOutBytes<kMode>;
     const uint32_t tempty0 = cluster_addr(&tempty[0], 0);
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    int acc = 0, use = 0;
+    int acc = 0, use = 0, buf = 0;
     while (ring.next(w, ok, a.status)) {
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], use & 1, a.status)))) break;
       tc_fence_after();
@@ -493,43 +505,55 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           store_rows<kF16>(a, v[0], v[1], out + c0 * a.ldo, out_stage, m, lane, w.rows - c0);
         }
       } else {
-        // chunks of 128 bytes of dW's rows, 16-byte parts swizzled with the row
+        // 32 columns at a time, the next ones on their way; chunks of 128 bytes
+        // of dW's rows leave by TMA, 16-byte parts swizzled with the row
         const int width = a.f32 ? 32 : 64;
-        const uint32_t dst = out_stage + lane * 128;
+        const bool live = w.rows > 0;
+        uint32_t next[32];
+        auto load = [&](int c) {
+          if (live && c < w.cols) tmem_ld_32x32b_x32(taddr + c, next);
+        };
+        int c = width * t;
+        load(c);
 #pragma unroll 1
-        for (int c0 = width * t; c0 < w.cols; c0 += 2 * width) {
-          uint32_t v[2][32];
-          if (w.rows > 0) {
-            tmem_ld_32x32b_x32(taddr + c0, v[0]);
-            if (!a.f32 && c0 + 32 < w.cols) tmem_ld_32x32b_x32(taddr + c0 + 32, v[1]);
-            tmem_ld_wait();
-          } else {
+        while (c < w.cols) {
+          uint32_t v[32];
+          tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0;
+          for (int i = 0; i < 32; ++i) v[i] = live ? next[i] : 0;
+          const int half = a.f32 ? 0 : (c >> 5) & 1;      // of the chunk
+          const int ahead = a.f32 || half ? c + width + 32 : c + 32;
+          load(ahead);
+          if (!half) {
+            if (lane == 0) bulk_wait_read<1>();           // the store before the last has read its staging
+            __syncwarp();
           }
-          if (lane == 0) bulk_wait_read();   // the last store has read its staging
-          __syncwarp();
+          const uint32_t dst = out_stage + buf * kOutBuf + lane * 128;
           if (a.f32) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              st_shared_v4(dst + ((j ^ (lane & 7)) << 4), v[0][4 * j], v[0][4 * j + 1], v[0][4 * j + 2],
-                           v[0][4 * j + 3]);
+              st_shared_v4(dst + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t* x = &v[j / 4][8 * (j & 3)];
+            for (int j = 0; j < 4; ++j) {
               uint32_t p[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) p[i] = pack2<kF16>(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-              st_shared_v4(dst + ((j ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+              for (int i = 0; i < 4; ++i)
+                p[i] = pack2<kF16>(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
+              st_shared_v4(dst + (((j + 4 * half) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
             }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && m < a.m && w.n0 + c0 < a.k) {
-            tma_store_3d(&maps.out, out_stage, w.n0 + c0, m, w.e);
-            bulk_commit_group();
+          if (a.f32 || half || c + 32 >= w.cols) {        // a chunk is complete
+            fence_proxy_async_smem();
+            __syncwarp();
+            const int col = w.n0 + c - 32 * half;
+            if (lane == 0 && m < a.m && col < a.k) {
+              tma_store_3d(&maps.out, out_stage + buf * kOutBuf, col, m, w.e);
+              bulk_commit_group();
+            }
+            buf ^= 1;
           }
+          c = ahead;
         }
       }
       tc_fence_before();
