@@ -132,3 +132,65 @@ def test_weight_gradient(counts, K, N, dtype, out_dtype):
 @pytest.mark.parametrize("count", [1, 15, 16, 17, 63, 64, 65, 80, 127, 128])
 def test_weight_gradient_ends_inside_a_box(count):
     check_wgrad([count, 3, count], 136, 264, BF16, FP32, gaps=[1, 2, 0], extra=5)
+
+
+# few rows and a long contraction: items are cut (one tile in 76 parts, parts of
+# different lengths, an odd number of steps, cut items before whole ones)
+CUT = [
+    ([1], 7168, 8),
+    ([3], 1032, 264),
+    ([1] * 8, 2056, 512),
+    ([64, 0, 33, 5], 1640, 520),
+    ([2] * 90, 1024, 72),
+    ([7] * 50, 1096, 512),
+    ([32] * 3, 1984, 2600),
+]
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("counts,K,N", CUT)
+def test_product_cut_along_the_contraction(counts, K, N, transpose):
+    check_product(counts, N if transpose else K, K if transpose else N, transpose, BF16, gaps=[3] * len(counts))
+
+
+def test_one_workspace_for_many_calls():
+    """Calls that cut their items, one after another on one workspace, and random values: the same bits every time,
+    and every counter zero after each call."""
+    from w4a16_int4_weight_sigmoid_gb300 import chord
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ws = workspace()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first = {}
+    for turn in range(6):
+        for i, (counts, K, N) in enumerate(CUT):
+            c, o, rows = order(counts)
+            if turn == 0:
+                x = torch.randn((rows, K), generator=g, device="cuda").to(BF16)
+                w = torch.randn((len(counts), N, K), generator=g, device="cuda").to(BF16)
+                first[i] = (x, w, None)
+            x, w, want = first[i]
+            out = torch.full((rows, N), LEFT, dtype=BF16, device="cuda")
+            chord.chord_expert_gemm(x, w, c, o, out, ws, False, status)
+            assert not ws[:chord.CHORD_EXPERT_GEMM_COUNTER_BYTES].any()
+            if want is None:
+                first[i] = (x, w, out)
+            else:
+                assert torch.equal(out, want)
+    assert status.item() == 0
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("counts,K,N", [([2] * 8, 7168, 512), ([700, 30], 1000, 328)])
+def test_random_values(counts, K, N, transpose):
+    """Sums of n products in FP32, in any order, are off by at most n 2^-23 of the sum of the magnitudes, and one
+    rounding to BF16 by 2^-8 of the result."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    c, o, rows = order(counts)
+    inner = N if transpose else K
+    x = torch.randn((rows, inner), generator=g, device="cuda").to(BF16)
+    w = torch.randn((len(counts), N, K), generator=g, device="cuda").to(BF16)
+    got = product(x, w, c, o, transpose)
+    for e, at in rows_of(c, o):
+        we = w[e].double() if transpose else w[e].double().T
+        want, size = x[at].double() @ we, x[at].double().abs() @ we.abs()
+        assert ((got[at].double() - want).abs() <= 2.0 ** -8 * want.abs() + inner * 2.0 ** -23 * size).all()

@@ -16,7 +16,13 @@
 //     contiguous, and the gradient reads both operands so: only the TMA boxes
 //     and the descriptors differ;
 //   * an item is one output tile; clusters take items in turn, so that those
-//     at work at one time share weights and rows in L2;
+//     at work at one time share weights and rows in L2.  With few rows (up to
+//     kSplitTok to a tile) the items that do not divide evenly among the
+//     clusters come first and are cut along the contraction, a part to a
+//     cluster; the CTA that arrives last at its half of an item adds the parts
+//     in order, so results do not depend on timing;
+//   * with few rows a stage of the ring holds 128 of the contraction instead of
+//     64: its hand-offs, not its bytes, set the pace (0.27 us a stage);
 //   * one warp per CTA loads, one (of the leading CTA) issues MMAs, one decodes
 //     items for the others, eight store finished tiles from one accumulator
 //     while the next is filled;
@@ -31,6 +37,8 @@
 // Rows of a product's B that are not the expert's give columns that are not
 // stored, so they need no zeroing.
 // Every mbarrier wait is bounded; see mxfp4_gemm.cu.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "pair.cuh"
@@ -44,6 +52,13 @@ constexpr int kMaxTok = 256;           // largest row tile (columns of the accum
 constexpr int kTileM = 256;            // of the pair
 constexpr int kStageK = 64;
 constexpr int kABytes = 128 * kStageK * 2;
+constexpr int kSplitTok = 64;          // largest row tile of items that are cut, and of double stages
+constexpr int kSlotFloats = kSplitTok * 128;       // one CTA's part of an item that is cut
+constexpr int kMaxCtas = 160;
+static_assert(kMaxCtas * sizeof(int) <= CHORD_EXPERT_GEMM_COUNTER_BYTES, "a counter for each CTA");
+// Stages of 128 that cutting has to save to pay for adding the parts up, and
+// that a part has at least.
+constexpr int kSplitSaves = 6, kSplitLeast = 4;
 constexpr int kBlockBytes = 64 * kStageK * 2;      // 64 contiguous M or N values x 64 of the contraction
 constexpr int kMaxStages = 10, kMaxAcc = 8;
 __host__ __device__ constexpr int stage_bytes(int tok) { return kABytes + tok / 2 * kStageK * 2; }
@@ -78,6 +93,8 @@ struct Args {
   uint16_t* out;         // product
   long long ldo;
   int* status;
+  int* split_cnt;        // [CTAs] parts arrived, zero between launches
+  float* partial;        // [CTAs][rows / 4][128 weights][4]
   int E, capacity;
   int m, k;              // product: weights' side of the output, contraction; gradient: N, K
   int m_tiles, n_tiles;  // tiles of 256
@@ -92,8 +109,8 @@ struct Maps {
 
 struct alignas(16) Seg {
   int e, row0, rows, m0;   // expert; its rows of this item (gradient: all of them); first weight row
-  int n0, cols;            // gradient: first column of dW; columns of the accumulator
-  int stages, valid;       // of 64 of the contraction
+  int n0, cols;            // gradient: first column of dW; product: the part's item.  Columns of the accumulator
+  int u0, u1;              // of the contraction, in steps of 64; u1 < 0: the end of the work
 };
 
 __device__ __forceinline__ int up32(int v) { return (v + 31) & ~31; }
@@ -109,7 +126,6 @@ template <Mode kMode>
 __device__ __forceinline__ Seg decode(const Args& a, const int* prefix, int item, int& e) {
   const int lane = threadIdx.x & 31;
   Seg s{};
-  s.valid = 1;
   if constexpr (kMode == kGradient) {
     const int per = a.m_tiles * a.n_tiles;
     e = item / per;
@@ -119,7 +135,7 @@ __device__ __forceinline__ Seg decode(const Args& a, const int* prefix, int item
     s.cols = min(kMaxTok, up32(a.k - s.n0));
     s.row0 = ld_ca(a.offsets + e);
     s.rows = ld_ca(a.counts + e);
-    s.stages = (s.rows + kStageK - 1) / kStageK;
+    s.u1 = (s.rows + kStageK - 1) / kStageK;
   } else {
     // the largest e with prefix[e] <= item (items only grow)
     auto past = [&](int at) { return __ballot_sync(0xffffffffu, at > a.E || prefix[at] > item); };
@@ -148,7 +164,7 @@ __device__ __forceinline__ Seg decode(const Args& a, const int* prefix, int item
     }
     s.m0 = local * kTileM;
     s.cols = up32(s.rows);
-    s.stages = (a.k + kStageK - 1) / kStageK;
+    s.u1 = (a.k + kStageK - 1) / kStageK;
   }
   s.e = e;
   return s;
@@ -167,11 +183,11 @@ struct ItemRing {
     const int4* src = reinterpret_cast<const int4*>(&slots[slot]);
     const int4 lo = src[0], hi = src[1];
     s.e = lo.x, s.row0 = lo.y, s.rows = lo.z, s.m0 = lo.w;
-    s.n0 = hi.x, s.cols = hi.y, s.stages = hi.z, s.valid = hi.w;
+    s.n0 = hi.x, s.cols = hi.y, s.u0 = hi.z, s.u1 = hi.w;
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[slot]);
     if (++slot == kItemSlots) slot = 0, ph ^= 1;
-    return s.valid != 0;
+    return s.u1 >= 0;
   }
 };
 
@@ -233,6 +249,50 @@ __device__ __forceinline__ void store_rows(const Args& a, const uint32_t (&lo)[1
   __syncwarp();
 }
 
+// Whether `ok` holds in all threads of the epilogue warps.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred p, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u), "n"(32 * kEpiWarps)
+      : "memory");
+  return r != 0;
+}
+
+// The sum of an item's parts (of CTAs first, first + 2, ...) in order, for this
+// lane's weight and the rows c0 .. c0 + 3 and, where `both`, the four after
+// them, to `out` (the item's first row and this lane's column).  Six parts' loads
+// are in flight; parts past the last are loaded again, not added.
+template <bool kF16>
+__device__ __forceinline__ void add_parts(const float* partial, int first, int parts, int c0, int rows, uint16_t* out,
+                                          long long ldo, bool in) {
+  float f[8] = {};
+  for (int p0 = 0; p0 < parts; p0 += 6) {
+    float4 x[6][2];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      const float* src = partial + static_cast<size_t>(first + 2 * min(p0 + i, parts - 1)) * kSlotFloats + c0 * 128;
+      x[i][0] = ld_cg_f4(src);
+      x[i][1] = ld_cg_f4(src + (c0 + 4 < rows ? 512 : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+      if (p0 + i < parts)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          f[4 * c] += x[i][c].x, f[4 * c + 1] += x[i][c].y;
+          f[4 * c + 2] += x[i][c].z, f[4 * c + 3] += x[i][c].w;
+        }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (in && c0 + i < rows) out[(c0 + i) * ldo] = static_cast<uint16_t>(pack2<kF16>(f[i], 0.f));
+}
+
 template <Mode kMode, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     expert_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
@@ -246,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __shared__ uint32_t tmem_base_s;
   __shared__ int prefix[kGrad ? 1 : kMaxExperts + 1];
   __shared__ int warp_sum[kThreads / 32], warp_max[kThreads / 32];
+  __shared__ int last_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
@@ -334,7 +395,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   if (kGrad) tok = kMaxTok;
   tok = order_ok ? tok : 32;
   const int items = !order_ok ? 0 : kGrad ? a.E * a.m_tiles * a.n_tiles : prefix[a.E];
-  const int stage = stage_bytes(tok), n_stages = min(kMaxStages, kStageBudget<kMode> / stage);
+  const int subs = !kGrad && tok <= kSplitTok ? 2 : 1;      // steps of 64 in a stage
+  const int sub_bytes = stage_bytes(tok), stage = subs * sub_bytes;
+  const int n_stages = min(kMaxStages, kStageBudget<kMode> / stage);
+  // The items that are cut, and their parts: cluster i has part i % parts of
+  // item i / parts, then whole items like all others.
+  int cut = 0, parts = 0;
+  if constexpr (!kGrad) {
+    const int units = (a.k + 2 * kStageK - 1) / (2 * kStageK);
+    cut = items % clusters;
+    if (subs == 2 && cut > 0) parts = min(clusters / cut, units / kSplitLeast);
+    if (parts < 2 || units - (units + parts - 1) / parts < kSplitSaves) cut = parts = 0;
+  }
   const int n_acc = min(kMaxAcc, kTmemCols / tok);
   ItemRing ring{item_full, item_empty, item_slots, a.test_timeout ? kTestWaitPolls : kWaitPolls, 0, 0};
   Seg w;
@@ -353,31 +425,34 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t bytes = kABytes + (kGrad ? 2 * kBlockBytes : half * kStageK * 2);
       const int m = w.m0 + 128 * static_cast<int>(rank);
       const int n = kGrad ? w.n0 + half * static_cast<int>(rank) : w.row0 + half * static_cast<int>(rank);
-      for (int u = 0; u < w.stages; ++u, ++it) {
+      for (int u0 = w.u0; u0 < w.u1; u0 += subs, ++it) {
         if (it >= n_stages && !(ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], ph ^ 1, a.status)))) break;
-        const uint32_t dst = smem0 + st * stage;
-        const int k0 = u * kStageK;
-        uint32_t bar = full0 + 8 * st;
-        if (kGrad && w.rows - k0 < kStageK && ((w.rows - k0) & 15)) {
+        uint32_t dst = smem0 + st * stage, bar = full0 + 8 * st;
+        const int here = min(subs, w.u1 - u0);
+        const int left = w.rows - u0 * kStageK;            // (gradient)
+        if (kGrad && left < kStageK && (left & 15)) {
           bar = smem_u32(&tail[turn][st]);
           mbar_arrive_expect_tx_elect(&tail[turn][st], bytes);
           turn ^= 1;
         } else {
-          mbar_arrive_expect_tx_cluster_elect(bar, bytes);
+          mbar_arrive_expect_tx_cluster_elect(bar, here * bytes);
         }
-        if constexpr (kMode == kProduct) {
-          tma_pair_3d_elect(dst, &maps.a, k0, m, w.e, bar);
-          tma_pair_2d_elect(dst + kABytes, mb, k0, n, bar);
-        } else if constexpr (kMode == kTransposed) {
-          tma_pair_3d_elect(dst, &maps.a, m, k0, w.e, bar);
-          tma_pair_3d_elect(dst + kBlockBytes, &maps.a, m + 64, k0, w.e, bar);
-          tma_pair_2d_elect(dst + kABytes, mb, k0, n, bar);
-        } else {
-          const int row = w.row0 + k0;
-          tma_pair_2d_elect(dst, &maps.a, m, row, bar);
-          tma_pair_2d_elect(dst + kBlockBytes, &maps.a, m + 64, row, bar);
-          tma_pair_2d_elect(dst + kABytes, mb, n, row, bar);
-          tma_pair_2d_elect(dst + kABytes + kBlockBytes, mb, n + 64, row, bar);
+        for (int u = u0; u < u0 + here; ++u, dst += sub_bytes) {
+          const int k0 = u * kStageK;
+          if constexpr (kMode == kProduct) {
+            tma_pair_3d_elect(dst, &maps.a, k0, m, w.e, bar);
+            tma_pair_2d_elect(dst + kABytes, mb, k0, n, bar);
+          } else if constexpr (kMode == kTransposed) {
+            tma_pair_3d_elect(dst, &maps.a, m, k0, w.e, bar);
+            tma_pair_3d_elect(dst + kBlockBytes, &maps.a, m + 64, k0, w.e, bar);
+            tma_pair_2d_elect(dst + kABytes, mb, k0, n, bar);
+          } else {
+            const int row = w.row0 + k0;
+            tma_pair_2d_elect(dst, &maps.a, m, row, bar);
+            tma_pair_2d_elect(dst + kBlockBytes, &maps.a, m + 64, row, bar);
+            tma_pair_2d_elect(dst + kABytes, mb, n, row, bar);
+            tma_pair_2d_elect(dst + kABytes + kBlockBytes, mb, n + 64, row, bar);
+          }
         }
         if (++st == n_stages) st = 0, ph ^= 1;
       }
@@ -398,26 +473,29 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       uint32_t accumulate = 0;
       if (use >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&tempty[acc], (use - 1) & 1, a.status));
       tc_fence_after();
-      for (int u = 0; ok && u < w.stages; ++u) {
+      for (int u0 = w.u0; ok && u0 < w.u1; u0 += subs) {
+        const int left = w.rows - u0 * kStageK;            // (gradient)
         // (a last box was written by threads of the other CTA too)
-        ok = kGrad && w.rows - u * kStageK < kStageK ? mbar_wait_cluster(&full[st], ph, a.status)
-                                                      : mbar_wait(&full[st], ph, a.status);
+        ok = kGrad && left < kStageK ? mbar_wait_cluster(&full[st], ph, a.status) : mbar_wait(&full[st], ph, a.status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
-        const uint32_t sa = smem0 + st * stage, sb = sa + kABytes;
-        const uint64_t da = kMnA ? sw128_mnmajor_desc(sa, kBlockBytes) : sw128_kmajor_desc(sa);
-        const uint64_t db = kMnB ? sw128_mnmajor_desc(sb, kBlockBytes) : sw128_kmajor_desc(sb);
         // 16 of the contraction: 32 bytes on in a row, or 16 rows of 128 bytes
         constexpr int kStepA = kMnA ? 128 : 2, kStepB = kMnB ? 128 : 2;
-        const int steps = kGrad ? (min(w.rows - u * kStageK, kStageK) + 15) / 16 : 4;
-        if (!kGrad || steps == 4) {
-          tc_pair_mma4_elect<kStepA, kStepB>(d, da, db, idesc, accumulate);
-        } else {
-          for (int i = 0; i < steps; ++i)
-            tc_pair_mma_elect(d, da + i * kStepA, db + i * kStepB, idesc, accumulate | (i > 0));
+        uint32_t sa = smem0 + st * stage;
+        for (int u = u0; u < min(u0 + subs, w.u1); ++u, sa += sub_bytes) {
+          const uint32_t sb = sa + kABytes;
+          const uint64_t da = kMnA ? sw128_mnmajor_desc(sa, kBlockBytes) : sw128_kmajor_desc(sa);
+          const uint64_t db = kMnB ? sw128_mnmajor_desc(sb, kBlockBytes) : sw128_kmajor_desc(sb);
+          const int steps = kGrad ? (min(left, kStageK) + 15) / 16 : 4;
+          if (!kGrad || steps == 4) {
+            tc_pair_mma4_elect<kStepA, kStepB>(d, da, db, idesc, accumulate);
+          } else {
+            for (int i = 0; i < steps; ++i)
+              tc_pair_mma_elect(d, da + i * kStepA, db + i * kStepB, idesc, accumulate | (i > 0));
+          }
+          accumulate = 1;
         }
         tc_pair_commit_elect(&empty[st]);
-        accumulate = 1;
         issued = true;
         if (++st == n_stages) st = 0, ph ^= 1;
       }
@@ -433,17 +511,30 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp == kItemWarp) {
     // ----------------------------------------------------------------- items
     int slot = 0, ph = 0, e = 0;
-    int item = a.test_timeout ? -1 : cluster;
-    for (bool first = true, more = item >= 0; more;) {
+    bool part = cluster < cut * parts;
+    int item = part ? cluster / parts : cut + cluster;
+    for (bool first = true, more = !a.test_timeout; more;) {
       more = item < items;
       Seg s{};
-      if (more) s = decode<kMode>(a, prefix, item, e);
+      if (more) {
+        s = decode<kMode>(a, prefix, item, e);
+        if (part) {
+          // whole stages of two steps, the last one short where their number is odd
+          const int units = (s.u1 + 1) / 2, p = cluster - item * parts;
+          s.u0 = 2 * (p * units / parts);
+          s.u1 = min(s.u1, 2 * ((p + 1) * units / parts));
+          s.n0 = item;
+        }
+      } else {
+        s.u1 = -1;
+      }
       if (!first && !(ok = __all_sync(0xffffffffu, mbar_wait_backoff(&item_empty[slot], ph ^ 1, a.status)))) break;
       if (lane == 0) {
         item_slots[slot] = s;
         mbar_arrive(&item_full[slot]);   // release: the item is visible to the waiters
       }
-      item += clusters;
+      item = part ? cut + cluster : item + clusters;
+      part = false;
       if (++slot == kItemSlots) slot = 0, ph ^= 1, first = false;
     }
   } else if (kGrad && (warp == kZeroWarp0 || warp == kZeroWarp1)) {
@@ -454,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     int turn = 0;
     uint32_t tail_ph = 0;                // of this warp's barriers: one turns when its slot holds a last box
     while (ring.next(w, ok, a.status)) {
-      st = (st + w.stages) % n_stages;
+      st = (st + w.u1) % n_stages;
       const int last = w.rows % kStageK;
       if (!(last & 15)) continue;
       turn ^= 1;
@@ -481,12 +572,30 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tempty0 = cluster_addr(&tempty[0], 0);
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
     int acc = 0, use = 0, buf = 0;
-    while (ring.next(w, ok, a.status)) {
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], use & 1, a.status)))) break;
+    // A wait that ran out ends a warp; at an item that is cut, whose handling
+    // has barriers, the epilogue warps end together.
+    bool part = !kGrad && cluster < cut * parts;
+    while (true) {
+      const bool on = ring.next(w, ok, a.status);
+      bool go = on && (ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], use & 1, a.status)));
+      if (part && !a.test_timeout) go = epilogue_all(go);
+      if (!go) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + acc * tok + lanes;
       const int m = w.m0 + 128 * static_cast<int>(rank) + 32 * q;
-      if constexpr (!kGrad) {
+      if (!kGrad && part) {
+        // this CTA's part, four rows of a weight together
+        float* mine_p = a.partial + static_cast<size_t>(blockIdx.x) * kSlotFloats + (32 * q + lane) * 4;
+        for (int c0 = 32 * t; c0 < w.rows; c0 += 64) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(taddr + c0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            if (c0 + c < w.rows)
+              *reinterpret_cast<uint4*>(mine_p + (c0 + c) * 128) = make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        }
+      } else if constexpr (!kGrad) {
         // the next 32 rows' accumulators are on their way while these go out
         uint32_t next[2][16];
         auto load = [&](int c0) {
@@ -560,6 +669,26 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * acc);
       if (++acc == n_acc) acc = 0, ++use;
+      if (kGrad || !part) continue;
+      part = false;
+      const int first = 2 * w.n0 * parts + static_cast<int>(rank);   // the CTA with the item's first part
+      epilogue_all(true);
+      if (tid == 32 * kEpiWarp0) {
+        // releases the parts stored by all threads before the barrier, and
+        // acquires the others'
+        int arrived;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                     : "=r"(arrived)
+                     : "l"(a.split_cnt + first)
+                     : "memory");
+        last_flag = arrived == parts - 1;
+      }
+      epilogue_all(true);
+      if (!last_flag) continue;
+      if (tid == 32 * kEpiWarp0) a.split_cnt[first] = 0;   // for the next launch
+      for (int c0 = 8 * t; c0 < w.rows; c0 += 16)
+        add_parts<kF16>(a.partial + (32 * q + lane) * 4, first, parts, c0, w.rows, a.out + w.row0 * a.ldo + m + lane,
+                        a.ldo, m + lane < a.m);
     }
     if (kGrad && lane == 0) bulk_wait_all();
   }
@@ -616,19 +745,23 @@ template <Mode kMode, bool kF16>
 cudaError_t launch(const Maps& maps, const Args& a, cudaStream_t st) {
   cudaError_t err = ensure_smem_limit<expert_gemm_kernel<kMode, kF16>>(kSmemBytes<kMode>);
   if (err != cudaSuccess) return err;
-  return launch_kernel(expert_gemm_kernel<kMode, kF16>, dim3(sm_count() < 2 ? 2 : sm_count() & ~1), dim3(kThreads), kSmemBytes<kMode>, st,
-                       true, maps, a);
+  return launch_kernel(expert_gemm_kernel<kMode, kF16>, dim3(std::max(2, std::min(kMaxCtas, sm_count() & ~1))),
+                       dim3(kThreads), kSmemBytes<kMode>, st, true, maps, a);
 }
 
 }  // namespace
 
-size_t expert_gemm_workspace_bytes() { return CHORD_EXPERT_GEMM_COUNTER_BYTES; }
+size_t expert_gemm_workspace_bytes() {
+  return CHORD_EXPERT_GEMM_COUNTER_BYTES + sizeof(float) * kMaxCtas * kSlotFloats;
+}
 
 cudaError_t expert_gemm_launch(const ExpertGemm& g, cudaStream_t st) {
   Args a{};
   a.counts = g.counts, a.offsets = g.offsets, a.status = g.status;
   a.E = g.E, a.capacity = g.capacity, a.test_timeout = g.test_timeout ? 1 : 0;
   a.out = static_cast<uint16_t*>(g.out), a.ldo = g.ldo;
+  a.split_cnt = static_cast<int*>(g.ws);
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(g.ws) + CHORD_EXPERT_GEMM_COUNTER_BYTES);
   a.m = g.transposed ? g.K : g.N, a.k = g.transposed ? g.N : g.K;
   a.m_tiles = (a.m + kTileM - 1) / kTileM;
   Maps maps{};
