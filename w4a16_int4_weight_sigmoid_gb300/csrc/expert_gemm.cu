@@ -21,8 +21,9 @@
 //     clusters come first and are cut along the contraction, a part to a
 //     cluster; the CTA that arrives last at its half of an item adds the parts
 //     in order, so results do not depend on timing;
-//   * with few rows a stage of the ring holds 128 of the contraction instead of
-//     64: its hand-offs, not its bytes, set the pace (0.27 us a stage);
+//   * a product's stage of the ring holds 128 of the contraction: with few rows
+//     a stage's hand-offs, not its bytes, set the pace (one token, 64 to a stage:
+//     18.6 us against 17.3; many rows 612 against 600);
 //   * one warp per CTA loads, one (of the leading CTA) issues MMAs, one decodes
 //     items for the others, eight store finished tiles from one accumulator
 //     while the next is filled;
@@ -52,7 +53,9 @@ constexpr int kMaxTok = 256;           // largest row tile (columns of the accum
 constexpr int kTileM = 256;            // of the pair
 constexpr int kStageK = 64;
 constexpr int kABytes = 128 * kStageK * 2;
-constexpr int kSplitTok = 64;          // largest row tile of items that are cut, and of double stages
+template <Mode kMode>
+constexpr int kSubs = kMode == kGradient ? 1 : 2;  // steps of 64 of the contraction in a stage
+constexpr int kSplitTok = 64;          // largest row tile of items that are cut
 constexpr int kSlotFloats = kSplitTok * 128;       // one CTA's part of an item that is cut
 constexpr int kMaxCtas = 160;
 static_assert(kMaxCtas * sizeof(int) <= CHORD_EXPERT_GEMM_COUNTER_BYTES, "a counter for each CTA");
@@ -113,6 +116,16 @@ struct alignas(16) Seg {
   int u0, u1;              // of the contraction, in steps of 64; u1 < 0: the end of the work
 };
 
+// a / b for a >= 0, b > 0.  A launch's first instructions are fetched as they
+// run, and an integer division is three times as many as this one of small
+// numbers (the correction makes up for a quotient that is one off).
+__device__ __forceinline__ int quick_div(int a, int b) {
+  if (a >= 1 << 22) return a / b;
+  int q = static_cast<int>(__fdividef(static_cast<float>(a), static_cast<float>(b)));
+  q -= q * b > a;
+  q += (q + 1) * b <= a;
+  return q;
+}
 __device__ __forceinline__ int up32(int v) { return (v + 31) & ~31; }
 __device__ __forceinline__ int row_tiles(int cnt) { return (cnt + kMaxTok - 1) / kMaxTok; }
 // Rows of an expert's row tiles: equal to within the rounding to 32.
@@ -128,8 +141,8 @@ __device__ __forceinline__ Seg decode(const Args& a, const int* prefix, int item
   Seg s{};
   if constexpr (kMode == kGradient) {
     const int per = a.m_tiles * a.n_tiles;
-    e = item / per;
-    const int local = item - e * per, mt = local / a.n_tiles;
+    e = quick_div(item, per);
+    const int local = item - e * per, mt = quick_div(local, a.n_tiles);
     s.m0 = mt * kTileM;
     s.n0 = (local - mt * a.n_tiles) * kMaxTok;
     s.cols = min(kMaxTok, up32(a.k - s.n0));
@@ -332,6 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(&tmem_base_s, kTmemCols);
+  if (warp == 0 && lane < 10) {   // the descriptors' first use would wait for them
+    const CUtensorMap* map = lane == 0 ? &maps.a : lane == 9 ? &maps.out : &maps.b[lane - 1];
+    if (kGrad ? lane == 0 || lane == 1 || lane == 9 : lane < 9) prefetch_tensormap(map);
+  }
   // programmatic launch: nothing above touches global memory
   grid_dep_wait();
   grid_dep_launch();
@@ -395,17 +412,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   if (kGrad) tok = kMaxTok;
   tok = order_ok ? tok : 32;
   const int items = !order_ok ? 0 : kGrad ? a.E * a.m_tiles * a.n_tiles : prefix[a.E];
-  const int subs = !kGrad && tok <= kSplitTok ? 2 : 1;      // steps of 64 in a stage
+  constexpr int subs = kSubs<kMode>;
   const int sub_bytes = stage_bytes(tok), stage = subs * sub_bytes;
   const int n_stages = min(kMaxStages, kStageBudget<kMode> / stage);
   // The items that are cut, and their parts: cluster i has part i % parts of
   // item i / parts, then whole items like all others.
   int cut = 0, parts = 0;
   if constexpr (!kGrad) {
-    const int units = (a.k + 2 * kStageK - 1) / (2 * kStageK);
-    cut = items % clusters;
-    if (subs == 2 && cut > 0) parts = min(clusters / cut, units / kSplitLeast);
-    if (parts < 2 || units - (units + parts - 1) / parts < kSplitSaves) cut = parts = 0;
+    const int units = (a.k + 2 * kStageK - 1) / (2 * kStageK);   // stages
+    if (tok <= kSplitTok) {
+      cut = items - quick_div(items, clusters) * clusters;
+      if (cut > 0) parts = min(quick_div(clusters, cut), units / kSplitLeast);
+      if (parts < 2 || units - quick_div(units + parts - 1, parts) < kSplitSaves) cut = parts = 0;
+    }
   }
   const int n_acc = min(kMaxAcc, kTmemCols / tok);
   ItemRing ring{item_full, item_empty, item_slots, a.test_timeout ? kTestWaitPolls : kWaitPolls, 0, 0};
@@ -512,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ----------------------------------------------------------------- items
     int slot = 0, ph = 0, e = 0;
     bool part = cluster < cut * parts;
-    int item = part ? cluster / parts : cut + cluster;
+    int item = part ? quick_div(cluster, parts) : cut + cluster;
     for (bool first = true, more = !a.test_timeout; more;) {
       more = item < items;
       Seg s{};
@@ -521,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (part) {
           // whole stages of two steps, the last one short where their number is odd
           const int units = (s.u1 + 1) / 2, p = cluster - item * parts;
-          s.u0 = 2 * (p * units / parts);
-          s.u1 = min(s.u1, 2 * ((p + 1) * units / parts));
+          s.u0 = 2 * quick_div(p * units, parts);
+          s.u1 = min(s.u1, 2 * quick_div((p + 1) * units, parts));
           s.n0 = item;
         }
       } else {

@@ -140,6 +140,9 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint3
   return d;
 }
 
+__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // Tiled TMA loads into this CTA's shared memory by one elected lane, completing
 // on a barrier of either CTA of the pair (cluster_addr).  The inner coordinate
 // is a multiple of 8 values (16 bytes); what is out of range reads zeros.
