@@ -29,6 +29,8 @@ struct Mx8Args {
   int K, topk, assignments, lanes;
 };
 
+constexpr int kUnroll = 4;
+
 template <typename T, int B>
 __global__ void __launch_bounds__(kRowThreads) mxfp8_quantize_kernel(Mx8Args a) {
   constexpr int kN = B / sizeof(T);
@@ -37,23 +39,30 @@ __global__ void __launch_bounds__(kRowThreads) mxfp8_quantize_kernel(Mx8Args a) 
   const int lane = threadIdx.x % a.lanes, per = kRowThreads / a.lanes;
   const long long step = static_cast<long long>(gridDim.x) * per;
   const int chunks = a.K / kN;
-  // (the row of a warp is the same for all its lanes)
+  // (the row of a warp is the same for all its lanes, and so are its turns)
   for (long long r = static_cast<long long>(blockIdx.x) * per + threadIdx.x / a.lanes; r < a.rows; r += step) {
     const T* x = static_cast<const T*>(a.x) + r * a.ld;
-    for (int c0 = lane & ~31; c0 < chunks; c0 += a.lanes) {
-      const int c = c0 + (lane & 31);
-      const bool in = c < chunks;
-      Chunk<B> v{};
-      if (in) load_chunk<B>(x + c * kN, v);
-      const uint32_t s = block_scale(block_top<T, B>(v));
-      if (!in) continue;
-      float f[kN];
+    for (int c0 = lane; c0 - (lane & 31) < chunks; c0 += kUnroll * a.lanes) {
+      Chunk<B> v[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kN; ++i) f[i] = chunk_f32<T, B>(v, i);
-      uint32_t code[kN < 4 ? 1 : kN / 4];
-      to_codes<kN>(f, s, code);
-      store_codes<kN>(a.codes + r * a.K + c * kN, code);
-      if ((c * kN) % kMx8Block == 0) a.scales[r * (a.K / kMx8Block) + c * kN / kMx8Block] = static_cast<uint8_t>(s);
+      for (int i = 0; i < kUnroll; ++i) {
+        v[i] = Chunk<B>{};
+        if (c0 + i * a.lanes < chunks) load_chunk<B>(x + (c0 + i * a.lanes) * kN, v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + i * a.lanes;
+        if (i > 0 && c - (lane & 31) >= chunks) break;
+        const uint32_t s = block_scale(block_top<T, B>(v[i]));
+        if (c >= chunks) continue;
+        float f[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) f[j] = chunk_f32<T, B>(v[i], j);
+        uint32_t code[kN < 4 ? 1 : kN / 4];
+        to_codes<kN>(f, s, code);
+        store_codes<kN>(a.codes + r * a.K + c * kN, code);
+        if ((c * kN) % kMx8Block == 0) a.scales[r * (a.K / kMx8Block) + c * kN / kMx8Block] = static_cast<uint8_t>(s);
+      }
     }
   }
 }
@@ -94,14 +103,24 @@ __global__ void __launch_bounds__(kRowThreads) mxfp8_dequantize_kernel(Mx8Args a
     const uint8_t* codes = a.codes_in + from * a.K;
     const uint8_t* scales = a.scales_in + from * (a.K / kMx8Block);
     T* out = static_cast<T*>(a.out) + r * a.ld;
-    for (int c = lane; c < chunks; c += a.lanes) {
-      Chunk<B> v{};
+    for (int c0 = lane; c0 < chunks; c0 += kUnroll * a.lanes) {
+      uint32_t code[kUnroll][kN < 4 ? 1 : kN / 4], scale[kUnroll];
       if (filled) {
-        uint32_t code[kN < 4 ? 1 : kN / 4];
-        load_codes<kN>(codes + c * kN, code);
-        typed_values<T, B>(code, load_scale(scales + c * kN / kMx8Block), v);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+          const int c = min(c0 + i * a.lanes, chunks - 1);
+          load_codes<kN>(codes + c * kN, code[i]);
+          scale[i] = load_scale(scales + c * kN / kMx8Block);
+        }
       }
-      store_chunk<B>(out + c * kN, v);
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + i * a.lanes;
+        if (c >= chunks) break;
+        Chunk<B> v{};
+        if (filled) typed_values<T, B>(code[i], scale[i], v);
+        store_chunk<B>(out + c * kN, v);
+      }
     }
   }
 }
@@ -109,7 +128,7 @@ __global__ void __launch_bounds__(kRowThreads) mxfp8_dequantize_kernel(Mx8Args a
 template <typename T, int B>
 cudaError_t launch(const Mx8Args& args, int what, cudaStream_t st) {
   Mx8Args a = args;
-  a.lanes = row_lanes(a.rows, a.K / static_cast<int>(B / sizeof(T)));
+  a.lanes = row_lanes(a.rows, a.K / static_cast<int>(B / sizeof(T)), kUnroll);
   const long long per = kRowThreads / a.lanes, want = (a.rows + per - 1) / per, most = 32LL * sm_count();
   const dim3 grid(static_cast<unsigned>(want < most ? want : most));
   auto kern = what == 0 ? mxfp8_quantize_kernel<T, B>

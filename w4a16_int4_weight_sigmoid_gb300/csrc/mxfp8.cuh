@@ -49,18 +49,20 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t top) {
 __device__ __forceinline__ float scale_value(uint32_t s) {
   return s == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(s ? s << 23 : 0x400000u);
 }
-// 2^(127 - s) for the scales that block_scale gives.
-__device__ __forceinline__ float inverse_scale(uint32_t s) { return s == 255 ? 0.f : __uint_as_float((254u - s) << 23); }
+// 2^(127 - s) for scales of finite blocks (255: some value).
+__device__ __forceinline__ float inverse_scale(uint32_t s) { return __uint_as_float((254u - s) << 23); }
 
 // kN codes as bytes of words, from values over the scale.
 template <int kN>
 __device__ __forceinline__ void to_codes(const float (&v)[kN], uint32_t s, uint32_t (&code)[kN < 4 ? 1 : kN / 4]) {
   const float inv = inverse_scale(s);
-  // 256 times 2^120, the scale of values from 2^127 on, is past FP32
-  const float top = s == 247 ? 240.f : 448.f;
   float q[kN];
 #pragma unroll
-  for (int i = 0; i < kN; ++i) q[i] = s == 255 ? 0.f : fminf(fmaxf(v[i] * inv, -top), top);
+  for (int i = 0; i < kN; ++i) q[i] = v[i] * inv;   // at most 448
+  if (s >= 247) {   // 256 times 2^120, the scale of values from 2^127 on, is past FP32; infinities and NaN
+#pragma unroll
+    for (int i = 0; i < kN; ++i) q[i] = s == 255 ? 0.f : fminf(fmaxf(q[i], -240.f), 240.f);
+  }
   auto pair = [](float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -119,12 +121,14 @@ __device__ __forceinline__ uint32_t load_scale(const uint8_t* p) {
 }
 
 // How a CTA of kRowThreads threads shares rows: `lanes` threads (a power of
-// two, whole warps) to a row.  A warp to a row where there are rows for all
-// SMs, more threads where few rows would leave them idle.
+// two, whole warps) to a row, each with up to `unroll` of its chunks in flight.
+// Enough threads that a row takes one turn where there are few rows (the
+// capacity of an order is several times the rows of one rank), two otherwise.
 constexpr int kRowThreads = 256;
-inline int row_lanes(long long rows, int chunks) {
+inline int row_lanes(long long rows, int chunks, int unroll) {
+  const int turns = rows < 16384 ? 1 : 2;
   int lanes = 32;
-  while (lanes < kRowThreads && lanes < chunks && rows * lanes < 152LL * 1024) lanes *= 2;
+  while (lanes < kRowThreads && lanes * unroll * turns < chunks) lanes *= 2;
   return lanes;
 }
 

@@ -44,6 +44,9 @@ __device__ __forceinline__ void sigmoids(float g, float& s, float& rest) {
   rest = g < 0.f ? d : t * d;
 }
 
+// Chunks of a row that a thread has in flight.
+constexpr int kUnroll = 2;
+
 template <typename T, int B, bool kKeep>
 __global__ void __launch_bounds__(kRowThreads) swiglu_kernel(SwigluArgs a) {
   constexpr int kN = B / sizeof(T);
@@ -58,43 +61,54 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_kernel(SwigluArgs a) {
     const float w = filled ? ld_ca(a.w + f) : 0.f;
     const T* gu = static_cast<const T*>(a.gu) + r * a.ldg;
     T* h = static_cast<T*>(a.h) + r * a.ldh;
-    for (int c0 = lane & ~31; c0 < chunks; c0 += a.lanes) {
-      const int c = c0 + (lane & 31);
-      const bool in = c < chunks;
-      Chunk<B> g{}, u{}, o{};
-      if (in && filled) {
-        load_chunk<B>(gu + c * kN, g);
-        load_chunk<B>(gu + a.I + c * kN, u);
-      }
-      float fg[kN], fu[kN], fo[kN];
+    for (int c0 = lane; c0 - (lane & 31) < chunks; c0 += kUnroll * a.lanes) {
+      Chunk<B> gs[kUnroll], us[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kN; ++i) fg[i] = chunk_f32<T, B>(g, i), fu[i] = chunk_f32<T, B>(u, i);
-      if constexpr (kKeep) {
-        const uint32_t sg = block_scale(block_top<T, B>(g)), su = block_scale(block_top<T, B>(u));
-        uint32_t code[kN < 4 ? 1 : kN / 4];
-        if (in) {
-          uint8_t* codes = a.codes + static_cast<long long>(r) * 2 * a.I + c * kN;
-          to_codes<kN>(fg, sg, code);
-          store_codes<kN>(codes, code);
-          to_codes<kN>(fu, su, code);
-          store_codes<kN>(codes + a.I, code);
-          if ((c * kN) % kMx8Block == 0) {
-            uint8_t* scales = a.scales + static_cast<long long>(r) * (2 * a.I / kMx8Block) + c * kN / kMx8Block;
-            scales[0] = static_cast<uint8_t>(sg);
-            scales[a.I / kMx8Block] = static_cast<uint8_t>(su);
-          }
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + i * a.lanes;
+        gs[i] = us[i] = Chunk<B>{};
+        if (c < chunks && filled) {
+          load_chunk<B>(gu + c * kN, gs[i]);
+          load_chunk<B>(gu + a.I + c * kN, us[i]);
         }
       }
-      if (!in) continue;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        float s, rest;
-        sigmoids<sizeof(T) == 4>(fg[i], s, rest);
-        fo[i] = w * (fg[i] * s) * fu[i];
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + i * a.lanes;
+        if (i > 0 && c - (lane & 31) >= chunks) break;
+        const Chunk<B>&g = gs[i], &u = us[i];
+        float fg[kN], fu[kN], fo[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) fg[j] = chunk_f32<T, B>(g, j), fu[j] = chunk_f32<T, B>(u, j);
+        if constexpr (kKeep) {
+          const uint32_t sg = block_scale(block_top<T, B>(g)), su = block_scale(block_top<T, B>(u));
+          uint32_t code[kN < 4 ? 1 : kN / 4];
+          if (c < chunks) {
+            uint8_t* codes = a.codes + static_cast<long long>(r) * 2 * a.I + c * kN;
+            to_codes<kN>(fg, sg, code);
+            store_codes<kN>(codes, code);
+            to_codes<kN>(fu, su, code);
+            store_codes<kN>(codes + a.I, code);
+            if ((c * kN) % kMx8Block == 0) {
+              uint8_t* scales = a.scales + static_cast<long long>(r) * (2 * a.I / kMx8Block) + c * kN / kMx8Block;
+              scales[0] = static_cast<uint8_t>(sg);
+              scales[a.I / kMx8Block] = static_cast<uint8_t>(su);
+            }
+          }
+        }
+        if (c >= chunks) continue;
+        Chunk<B> o{};
+        if (filled) {
+#pragma unroll
+          for (int j = 0; j < kN; ++j) {
+            float s, rest;
+            sigmoids<sizeof(T) == 4>(fg[j], s, rest);
+            fo[j] = w * (fg[j] * s) * fu[j];
+          }
+          f32_chunk<T, B>(o, fo);
+        }
+        store_chunk<B>(h + c * kN, o);
       }
-      f32_chunk<T, B>(o, fo);
-      if (!filled) o = Chunk<B>{};
-      store_chunk<B>(h + c * kN, o);
     }
   }
 }
@@ -119,46 +133,61 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_backward_kernel(SwigluArgs
     const float w = filled ? ld_ca(a.w + f) : 0.f;
     const long long row = r;
     float sum = 0.f;
-    for (int c = r < total ? lane : chunks; c < chunks; c += a.lanes) {
-      Chunk<B> d{}, x{}, y{}, o{};
-      float fg[kN], fu[kN];
+    for (int c0 = r < total ? lane : chunks; c0 < chunks; c0 += kUnroll * a.lanes) {
+      Chunk<B> ds[kUnroll], xs[kKeep ? 1 : kUnroll], ys[kKeep ? 1 : kUnroll];
+      uint32_t cg[kKeep ? kUnroll : 1][kW], cu[kKeep ? kUnroll : 1][kW], sg[kUnroll], su[kUnroll];
       if (filled) {
-        load_chunk<B>(static_cast<const T*>(a.dh) + row * a.ldd + c * kN, d);
-        if constexpr (kKeep) {
-          const uint8_t* codes = a.codes + row * 2 * a.I + c * kN;
-          const uint8_t* scales = a.scales + row * (2 * a.I / kMx8Block) + c * kN / kMx8Block;
-          uint32_t cg[kW], cu[kW];
-          load_codes<kN>(codes, cg);
-          load_codes<kN>(codes + a.I, cu);
-          const float sg = scale_value(load_scale(scales)), su = scale_value(load_scale(scales + a.I / kMx8Block));
-          from_codes<kN>(cg, sg, fg);
-          from_codes<kN>(cu, su, fu);
-        } else {
-          const T* gu = static_cast<const T*>(a.gu) + row * a.ldg + c * kN;
-          load_chunk<B>(gu, x);
-          load_chunk<B>(gu + a.I, y);
 #pragma unroll
-          for (int i = 0; i < kN; ++i) fg[i] = chunk_f32<T, B>(x, i), fu[i] = chunk_f32<T, B>(y, i);
+        for (int i = 0; i < kUnroll; ++i) {
+          const int c = min(c0 + i * a.lanes, chunks - 1);
+          load_chunk<B>(static_cast<const T*>(a.dh) + row * a.ldd + c * kN, ds[i]);
+          if constexpr (kKeep) {
+            const uint8_t* codes = a.codes + row * 2 * a.I + c * kN;
+            const uint8_t* scales = a.scales + row * (2 * a.I / kMx8Block) + c * kN / kMx8Block;
+            load_codes<kN>(codes, cg[i]);
+            load_codes<kN>(codes + a.I, cu[i]);
+            sg[i] = load_scale(scales);
+            su[i] = load_scale(scales + a.I / kMx8Block);
+          } else {
+            const T* gu = static_cast<const T*>(a.gu) + row * a.ldg + c * kN;
+            load_chunk<B>(gu, xs[i]);
+            load_chunk<B>(gu + a.I, ys[i]);
+          }
         }
-        float og[kN], ou[kN], oh[kN];
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          float s, rest;
-          sigmoids<sizeof(T) == 4>(fg[i], s, rest);
-          const float silu = fg[i] * s, dh = chunk_f32<T, B>(d, i), wd = w * dh;
-          sum += dh * silu * fu[i];
-          og[i] = wd * fu[i] * (s + silu * rest);
-          ou[i] = wd * silu;
-          oh[i] = w * silu * fu[i];
-        }
-        f32_chunk<T, B>(x, og);
-        f32_chunk<T, B>(y, ou);
-        f32_chunk<T, B>(o, oh);
       }
-      T* dgu = static_cast<T*>(a.dgu) + row * a.ldo + c * kN;
-      store_chunk<B>(dgu, x);
-      store_chunk<B>(dgu + a.I, y);
-      if (a.h) store_chunk<B>(static_cast<T*>(a.h) + row * a.ldh + c * kN, o);
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + i * a.lanes;
+        if (c >= chunks) break;
+        Chunk<B> x{}, y{}, o{};
+        if (filled) {
+          float fg[kN], fu[kN], oh[kN];
+          if constexpr (kKeep) {
+            from_codes<kN>(cg[i], scale_value(sg[i]), fg);
+            from_codes<kN>(cu[i], scale_value(su[i]), fu);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kN; ++j) fg[j] = chunk_f32<T, B>(xs[i], j), fu[j] = chunk_f32<T, B>(ys[i], j);
+          }
+#pragma unroll
+          for (int j = 0; j < kN; ++j) {
+            float s, rest;
+            sigmoids<sizeof(T) == 4>(fg[j], s, rest);
+            const float silu = fg[j] * s, dh = chunk_f32<T, B>(ds[i], j), wd = w * dh, up = fu[j];
+            sum += dh * silu * up;
+            oh[j] = w * silu * up;
+            fg[j] = wd * up * (s + silu * rest);
+            fu[j] = wd * silu;
+          }
+          f32_chunk<T, B>(x, fg);
+          f32_chunk<T, B>(y, fu);
+          f32_chunk<T, B>(o, oh);
+        }
+        T* dgu = static_cast<T*>(a.dgu) + row * a.ldo + c * kN;
+        store_chunk<B>(dgu, x);
+        store_chunk<B>(dgu + a.I, y);
+        if (a.h) store_chunk<B>(static_cast<T*>(a.h) + row * a.ldh + c * kN, o);
+      }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -177,7 +206,7 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_backward_kernel(SwigluArgs
 template <typename T, int B>
 cudaError_t launch(const SwigluArgs& args, bool backward, cudaStream_t st) {
   SwigluArgs a = args;
-  a.lanes = row_lanes(a.rows, a.I / static_cast<int>(B / sizeof(T)));
+  a.lanes = row_lanes(a.rows, a.I / static_cast<int>(B / sizeof(T)), kUnroll);
   const long long per = kRowThreads / a.lanes, want = (a.rows + per - 1) / per, most = 32LL * sm_count();
   const dim3 grid(static_cast<unsigned>(want < most ? want : most));
   auto kern = backward ? (a.codes ? swiglu_backward_kernel<T, B, true> : swiglu_backward_kernel<T, B, false>)
