@@ -25,6 +25,28 @@ __device__ __forceinline__ void from_f32(Bf16& d, float f) { d.v = __bfloat16_as
 __device__ __forceinline__ void from_f32(Fp16& d, float f) { d.v = __half_as_ushort(__float2half_rn(f)); }
 __device__ __forceinline__ void from_f32(float& d, float f) { d = f; }
 
+// Two FP32 operations in one instruction, each rounded to nearest.
+#define CHORD_F32X2(name, op)                                                                             \
+  __device__ __forceinline__ float2 name(float2 a, float2 b) {                                            \
+    float2 d;                                                                                             \
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t" op                     \
+        ".rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"                                                 \
+        : "=f"(d.x), "=f"(d.y)                                                                            \
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));                                                        \
+    return d;                                                                                             \
+  }
+CHORD_F32X2(mul2, "mul")
+CHORD_F32X2(add2, "add")
+#undef CHORD_F32X2
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // B bytes as one access (32: one 256-bit access), kept in program order: a
 // programmatic launch reads nothing before its wait.
 template <int B>

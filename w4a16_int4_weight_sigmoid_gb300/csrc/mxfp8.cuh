@@ -58,7 +58,11 @@ __device__ __forceinline__ void to_codes(const float (&v)[kN], uint32_t s, uint3
   const float inv = inverse_scale(s);
   float q[kN];
 #pragma unroll
-  for (int i = 0; i < kN; ++i) q[i] = v[i] * inv;   // at most 448
+  for (int i = 0; i < kN; i += 2) {                 // at most 448
+    const float2 two = mul2(make_float2(v[i], i + 1 < kN ? v[i + 1] : 0.f), make_float2(inv, inv));
+    q[i] = two.x;
+    if (i + 1 < kN) q[i + 1] = two.y;
+  }
   if (s >= 247) {   // 256 times 2^120, the scale of values from 2^127 on, is past FP32; infinities and NaN
 #pragma unroll
     for (int i = 0; i < kN; ++i) q[i] = s == 255 ? 0.f : fminf(fmaxf(q[i], -240.f), 240.f);
@@ -86,8 +90,9 @@ __device__ __forceinline__ void from_codes(const uint32_t (&code)[kN < 4 ? 1 : k
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
     const __half2 x = *reinterpret_cast<const __half2*>(&h);
-    v[i] = __low2float(x) * scale;
-    if (i + 1 < kN) v[i + 1] = __high2float(x) * scale;
+    const float2 f = mul2(__half22float2(x), make_float2(scale, scale));
+    v[i] = f.x;
+    if (i + 1 < kN) v[i + 1] = f.y;
   }
 }
 template <int kN>
@@ -123,10 +128,10 @@ __device__ __forceinline__ uint32_t load_scale(const uint8_t* p) {
 // How a CTA of kRowThreads threads shares rows: `lanes` threads (a power of
 // two, whole warps) to a row, each with up to `unroll` of its chunks in flight.
 // Enough threads that a row takes one turn where there are few rows (the
-// capacity of an order is several times the rows of one rank), two otherwise.
+// capacity of an order is several times the rows of one rank), four otherwise.
 constexpr int kRowThreads = 256;
 inline int row_lanes(long long rows, int chunks, int unroll) {
-  const int turns = rows < 16384 ? 1 : 2;
+  const int turns = rows < 16384 ? 1 : 4;
   int lanes = 32;
   while (lanes < kRowThreads && lanes * unroll * turns < chunks) lanes *= 2;
   return lanes;

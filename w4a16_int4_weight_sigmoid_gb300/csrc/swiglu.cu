@@ -9,10 +9,16 @@
 // With w here, the second product's rows are summed back to tokens without
 // weights, and its output is not needed for the weights' gradient:
 // <dout, W2 h> = <W2^T dout, h>.
-// All bound by memory: one pass over the rows, up to 32 bytes an access, a row
-// to one warp or more (row_lanes); 1 - s is formed from the exponential of
-// -|gate| as s is, so neither loses digits near 1.  dweight is added up in
-// FP32 in an order fixed by the call's sizes.
+// All bound by memory: one pass over the rows, a row to one warp or more
+// (row_lanes).  dweight is added up in FP32 in an order fixed by the call's
+// sizes.  Accesses of up to 32 bytes forward and 16 backward, where a value
+// needs twice the registers: compiled for three and four CTAs per SM (16384
+// rows, I = 2048 BF16, held in 8 bits: forward 45 us against 50 uncapped,
+// backward 59 against 84 and, with 32 bytes, 64).  What a pass moves then goes
+// at 5.7 to 6.0 TB/s of the 6.8 of a copy; loading a step ahead, or half the
+// instructions (two values in one FP32 operation), changed nothing.
+#include <utility>
+
 #include "kernels.h"
 #include "mxfp8.cuh"
 
@@ -35,20 +41,46 @@ struct SwigluArgs {
   int rows, I, assignments, lanes;
 };
 
-// s = sigmoid(g) and 1 - s.
+// Two gates: silu(g) = max(g, 0) - |g| t / (1 + t) with t = exp(-|g|), which
+// loses no digits on either side, and sigmoid(g).  For 16-bit types t is the
+// square of exp2(-|g| log2(e) / 2), which stays a normal number where t does
+// not, and the fast reciprocal's operand lies in [1, 2].
 template <bool kPrecise>
-__device__ __forceinline__ void sigmoids(float g, float& s, float& rest) {
-  const float t = kPrecise ? expf(-fabsf(g)) : __expf(-fabsf(g));   // at most 1
-  const float d = kPrecise ? 1.f / (1.f + t) : __fdividef(1.f, 1.f + t);
-  s = g < 0.f ? t * d : d;
-  rest = g < 0.f ? d : t * d;
+__device__ __forceinline__ void gates(float2 g, float2& silu, float2& s) {
+  const float2 size = make_float2(fabsf(g.x), fabsf(g.y));
+  float2 t, d;
+  if (kPrecise) {
+    t = make_float2(expf(-size.x), expf(-size.y));
+    d = make_float2(1.f / (1.f + t.x), 1.f / (1.f + t.y));
+  } else {
+    const float2 half = mul2(size, make_float2(-0.72134752f, -0.72134752f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.x) : "f"(half.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t.y) : "f"(half.y));
+    t = mul2(t, t);
+    d = add2(t, make_float2(1.f, 1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d.y) : "f"(d.y));
+  }
+  const float2 q = mul2(t, d);                              // sigmoid(-|g|)
+  silu = fma2(make_float2(-size.x, -size.y), q, make_float2(fmaxf(g.x, 0.f), fmaxf(g.y, 0.f)));
+  s = make_float2(g.x < 0.f ? q.x : d.x, g.y < 0.f ? q.y : d.y);
+}
+// Values i and i + 1 of an array of kN (one: 0 for the second).
+template <int kN>
+__device__ __forceinline__ float2 two(const float (&f)[kN], int i) {
+  return make_float2(f[i], i + 1 < kN ? f[i + 1] : 0.f);
+}
+template <int kN>
+__device__ __forceinline__ void set(float (&f)[kN], int i, float2 v) {
+  f[i] = v.x;
+  if (i + 1 < kN) f[i + 1] = v.y;
 }
 
 // Chunks of a row that a thread has in flight.
 constexpr int kUnroll = 2;
 
 template <typename T, int B, bool kKeep>
-__global__ void __launch_bounds__(kRowThreads) swiglu_kernel(SwigluArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 3) swiglu_kernel(SwigluArgs a) {
   constexpr int kN = B / sizeof(T);
   grid_dep_wait();
   grid_dep_launch();
@@ -100,10 +132,10 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_kernel(SwigluArgs a) {
         Chunk<B> o{};
         if (filled) {
 #pragma unroll
-          for (int j = 0; j < kN; ++j) {
-            float s, rest;
-            sigmoids<sizeof(T) == 4>(fg[j], s, rest);
-            fo[j] = w * (fg[j] * s) * fu[j];
+          for (int j = 0; j < kN; j += 2) {
+            float2 silu, s;
+            gates<sizeof(T) == 4>(two(fg, j), silu, s);
+            set(fo, j, mul2(mul2(silu, make_float2(w, w)), two(fu, j)));
           }
           f32_chunk<T, B>(o, fo);
         }
@@ -114,7 +146,7 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_kernel(SwigluArgs a) {
 }
 
 template <typename T, int B, bool kKeep>
-__global__ void __launch_bounds__(kRowThreads) swiglu_backward_kernel(SwigluArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 4) swiglu_backward_kernel(SwigluArgs a) {
   constexpr int kN = B / sizeof(T), kW = kN < 4 ? 1 : kN / 4;
   __shared__ float sums[kRowThreads / 32];
   grid_dep_wait();
@@ -132,7 +164,7 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_backward_kernel(SwigluArgs
     const bool filled = f >= 0 && f < a.assignments;
     const float w = filled ? ld_ca(a.w + f) : 0.f;
     const long long row = r;
-    float sum = 0.f;
+    float2 sum = make_float2(0.f, 0.f);
     for (int c0 = r < total ? lane : chunks; c0 < chunks; c0 += kUnroll * a.lanes) {
       Chunk<B> ds[kUnroll], xs[kKeep ? 1 : kUnroll], ys[kKeep ? 1 : kUnroll];
       uint32_t cg[kKeep ? kUnroll : 1][kW], cu[kKeep ? kUnroll : 1][kW], sg[kUnroll], su[kUnroll];
@@ -169,15 +201,21 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_backward_kernel(SwigluArgs
 #pragma unroll
             for (int j = 0; j < kN; ++j) fg[j] = chunk_f32<T, B>(xs[i], j), fu[j] = chunk_f32<T, B>(ys[i], j);
           }
+          float dh[kN];
 #pragma unroll
-          for (int j = 0; j < kN; ++j) {
-            float s, rest;
-            sigmoids<sizeof(T) == 4>(fg[j], s, rest);
-            const float silu = fg[j] * s, dh = chunk_f32<T, B>(ds[i], j), wd = w * dh, up = fu[j];
-            sum += dh * silu * up;
-            oh[j] = w * silu * up;
-            fg[j] = wd * up * (s + silu * rest);
-            fu[j] = wd * silu;
+          for (int j = 0; j < kN; ++j) dh[j] = chunk_f32<T, B>(ds[i], j);
+#pragma unroll
+          for (int j = 0; j < kN; j += 2) {
+            const float2 ww = make_float2(w, w), d = two(dh, j), up = two(fu, j);
+            float2 silu, s;
+            gates<sizeof(T) == 4>(two(fg, j), silu, s);
+            const float2 act = mul2(silu, up), wd = mul2(ww, d);
+            // 1 - s is off by 2^-25, silu times that by less than the slope's own rounding times |gate|
+            const float2 slope = fma2(silu, make_float2(1.f - s.x, 1.f - s.y), s);
+            sum = fma2(d, act, sum);
+            set(oh, j, mul2(ww, act));
+            set(fg, j, mul2(mul2(wd, up), slope));
+            set(fu, j, mul2(wd, silu));
           }
           f32_chunk<T, B>(x, fg);
           f32_chunk<T, B>(y, fu);
@@ -189,51 +227,55 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_backward_kernel(SwigluArgs
         if (a.h) store_chunk<B>(static_cast<T*>(a.h) + row * a.ldh + c * kN, o);
       }
     }
+    float all = sum.x + sum.y;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     if (a.lanes > 32) {
       const int warp = threadIdx.x >> 5;
-      if ((threadIdx.x & 31) == 0) sums[warp] = sum;
+      if ((threadIdx.x & 31) == 0) sums[warp] = all;
       __syncthreads();
       if (lane == 0)
-        for (int i = 1; i < a.lanes / 32; ++i) sum += sums[warp + i];
+        for (int i = 1; i < a.lanes / 32; ++i) all += sums[warp + i];
       __syncthreads();
     }
-    if (lane == 0 && filled) a.dw[f] = sum;
+    if (lane == 0 && filled) a.dw[f] = all;
   }
 }
 
-template <typename T, int B>
-cudaError_t launch(const SwigluArgs& args, bool backward, cudaStream_t st) {
+template <typename T, int B, bool kBackward>
+cudaError_t launch(const SwigluArgs& args, cudaStream_t st) {
   SwigluArgs a = args;
   a.lanes = row_lanes(a.rows, a.I / static_cast<int>(B / sizeof(T)), kUnroll);
-  const long long per = kRowThreads / a.lanes, want = (a.rows + per - 1) / per, most = 32LL * sm_count();
+  const long long per = kRowThreads / a.lanes, want = (a.rows + per - 1) / per, most = 8LL * sm_count();
   const dim3 grid(static_cast<unsigned>(want < most ? want : most));
-  auto kern = backward ? (a.codes ? swiglu_backward_kernel<T, B, true> : swiglu_backward_kernel<T, B, false>)
-                       : (a.codes ? swiglu_kernel<T, B, true> : swiglu_kernel<T, B, false>);
+  void (*kern)(SwigluArgs);
+  if constexpr (kBackward) kern = a.codes ? swiglu_backward_kernel<T, B, true> : swiglu_backward_kernel<T, B, false>;
+  else kern = a.codes ? swiglu_kernel<T, B, true> : swiglu_kernel<T, B, false>;
   return launch_kernel(kern, grid, dim3(kRowThreads), 0, st, true, a);
 }
 // The widest access that all matrices of the call allow.
-template <typename T>
-cudaError_t launch(const SwigluArgs& a, bool backward, cudaStream_t st) {
-  int b = 32;
-  auto allow = [&](const void* p, long long ld) { b = std::min(b, p ? row_access_bytes(p, ld, a.I, sizeof(T), 32) : 32); };
-  allow(a.gu, a.ldg), allow(a.h, a.ldh), allow(a.dh, a.ldd), allow(a.dgu, a.ldo);
+template <typename T, bool kBackward>
+cudaError_t launch(const SwigluArgs& a, cudaStream_t st) {
+  int b = kBackward ? 16 : 32;
+  for (auto [p, ld] : {std::pair{a.gu, a.ldg}, {a.h, a.ldh}, {a.dh, a.ldd}, {a.dgu, a.ldo}})
+    if (p) b = std::min(b, row_access_bytes(p, ld, a.I, sizeof(T), 32));
   switch (b) {
-    case 32: return launch<T, 32>(a, backward, st);
-    case 16: return launch<T, 16>(a, backward, st);
-    case 8: return launch<T, 8>(a, backward, st);
-    case 4: return launch<T, 4>(a, backward, st);
+    case 32:
+      if constexpr (!kBackward) return launch<T, 32, kBackward>(a, st);
+    case 16: return launch<T, 16, kBackward>(a, st);
+    case 8: return launch<T, 8, kBackward>(a, st);
+    case 4: return launch<T, 4, kBackward>(a, st);
     default:
-      if constexpr (sizeof(T) == 2) return launch<T, 2>(a, backward, st);
+      if constexpr (sizeof(T) == 2) return launch<T, 2, kBackward>(a, st);
       return cudaErrorInvalidValue;   // (elements are aligned)
   }
 }
-cudaError_t launch(const SwigluArgs& a, int dtype, bool backward, cudaStream_t st) {
+template <bool kBackward>
+cudaError_t launch(const SwigluArgs& a, int dtype, cudaStream_t st) {
   switch (dtype) {
-    case CHORD_DTYPE_BF16: return launch<Bf16>(a, backward, st);
-    case CHORD_DTYPE_FP16: return launch<Fp16>(a, backward, st);
-    default: return launch<float>(a, backward, st);
+    case CHORD_DTYPE_BF16: return launch<Bf16, kBackward>(a, st);
+    case CHORD_DTYPE_FP16: return launch<Fp16, kBackward>(a, st);
+    default: return launch<float, kBackward>(a, st);
   }
 }
 
@@ -245,7 +287,7 @@ cudaError_t swiglu_launch(const Swiglu& s, int dtype, bool backward, cudaStream_
   a.h = s.h, a.dgu = s.dgu, a.codes = s.codes, a.scales = s.scales, a.dw = s.dw;
   a.ldg = s.ldg, a.ldh = s.ldh, a.ldd = s.ldd, a.ldo = s.ldo;
   a.rows = s.rows, a.I = s.I, a.assignments = s.assignments;
-  return launch(a, dtype, backward, st);
+  return backward ? launch<true>(a, dtype, st) : launch<false>(a, dtype, st);
 }
 
 }  // namespace chord
