@@ -194,3 +194,19 @@ def test_random_values(counts, K, N, transpose):
         we = w[e].double() if transpose else w[e].double().T
         want, size = x[at].double() @ we, x[at].double().abs() @ we.abs()
         assert ((got[at].double() - want).abs() <= 2.0 ** -8 * want.abs() + inner * 2.0 ** -23 * size).all()
+
+
+# uneven popularity: experts are taken by falling rows up to 256 of them, in their order above
+@pytest.mark.parametrize("experts", [2, 40, 255, 256, 257, 300])
+def test_uneven_popularity(experts):
+    counts = [(i * i * 37 + 11) % 290 if i % 5 else 0 for i in range(experts)]
+    counts[experts // 2] = 700
+    for transpose in (False, True):
+        check_product(counts, 72, 136, transpose, BF16, gaps=[i % 3 for i in range(experts)])
+    check_wgrad(counts, 72, 136, FP16, FP32, gaps=[i % 3 for i in range(experts)])
+
+
+def test_equal_experts_in_many_rounds():
+    """More items than clusters, dealt forth and back."""
+    check_product([96] * 60, 136, 1288, False, BF16)
+    check_wgrad([96] * 60, 520, 520, BF16, BF16)

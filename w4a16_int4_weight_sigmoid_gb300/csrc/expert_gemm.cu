@@ -75,6 +75,10 @@ constexpr int kItemSlots = 8;
 constexpr int kMaxExperts = 1024;
 constexpr int kTmemCols = 512;
 constexpr int kGroupTiles = 8;         // row tiles that are taken together
+// Up to this many experts are taken in descending order of their rows, and
+// dealt forth and back, so that experts of uneven popularity leave the clusters
+// about evenly busy.
+constexpr int kMaxSorted = 256;
 // An epilogue warp's staging: product 32 tokens x 32 weights (rows of 80
 // bytes spread over the banks); gradient two times 32 rows of 128 bytes, so that
 // one is filled while the other leaves, at the cost of a stage.
@@ -87,7 +91,7 @@ template <Mode kMode>
 constexpr int kSmemBytes = kStageBudget<kMode> + kEpiWarps * kOutBytes<kMode> + 1024;
 static_assert(kMaxStages * stage_bytes(32) <= kStageBudget<kProduct>, "stage budget");
 static_assert(kSmemBytes<kProduct> + (kMaxExperts + 1) * 4 + 2048 <= 232448, "shared memory budget");
-static_assert(kSmemBytes<kGradient> + 1024 <= 232448, "shared memory budget");
+static_assert(kSmemBytes<kGradient> + 1536 <= 232448, "shared memory budget");
 static_assert(3 * kThreads >= kMaxExperts, "three experts per thread at most");
 
 struct Args {
@@ -131,12 +135,12 @@ __device__ __forceinline__ int row_tiles(int cnt) { return (cnt + kMaxTok - 1) /
 // Rows of an expert's row tiles: equal to within the rounding to 32.
 __device__ __forceinline__ int tile_rows(int cnt, int n) { return up32(n > 1 ? (cnt + n - 1) / n : cnt); }
 
-// The items in the order in which they are dealt.
+// The items in the order in which they are dealt, `e` the expert's place.
 //   product: experts in order; per expert groups of kGroupTiles row tiles; per
 //   group the weight tiles; per weight tile the group's row tiles
 //   gradient: experts in order; per expert tiles of N, per tile tiles of K
 template <Mode kMode>
-__device__ __forceinline__ Seg decode(const Args& a, const int* prefix, int item, int& e) {
+__device__ __forceinline__ Seg decode(const Args& a, const int* prefix, const uint8_t* order, int item, int& e) {
   const int lane = threadIdx.x & 31;
   Seg s{};
   if constexpr (kMode == kGradient) {
@@ -146,8 +150,9 @@ __device__ __forceinline__ Seg decode(const Args& a, const int* prefix, int item
     s.m0 = mt * kTileM;
     s.n0 = (local - mt * a.n_tiles) * kMaxTok;
     s.cols = min(kMaxTok, up32(a.k - s.n0));
-    s.row0 = ld_ca(a.offsets + e);
-    s.rows = ld_ca(a.counts + e);
+    s.e = order ? order[e] : e;
+    s.row0 = ld_ca(a.offsets + s.e);
+    s.rows = ld_ca(a.counts + s.e);
     s.u1 = (s.rows + kStageK - 1) / kStageK;
   } else {
     // the largest e with prefix[e] <= item (items only grow)
@@ -160,9 +165,10 @@ __device__ __forceinline__ Seg decode(const Args& a, const int* prefix, int item
       found = past(e + 1 + lane);
     }
     e += __ffs(found) - 1;
-    const int cnt = ld_ca(a.counts + e);
+    s.e = order ? order[e] : e;
+    const int cnt = ld_ca(a.counts + s.e);
     int local = item - prefix[e], rt = 0;
-    s.row0 = ld_ca(a.offsets + e);
+    s.row0 = ld_ca(a.offsets + s.e);
     s.rows = cnt;
     if (cnt > kMaxTok) {
       const int n = row_tiles(cnt), per = tile_rows(cnt, n);
@@ -179,7 +185,6 @@ __device__ __forceinline__ Seg decode(const Args& a, const int* prefix, int item
     s.cols = up32(s.rows);
     s.u1 = (a.k + kStageK - 1) / kStageK;
   }
-  s.e = e;
   return s;
 }
 
@@ -203,6 +208,17 @@ struct ItemRing {
     return s.u1 >= 0;
   }
 };
+
+// The sum over the lanes up to this one.
+__device__ __forceinline__ int scan_warp(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
 
 template <bool kF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -318,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __shared__ Seg item_slots[kItemSlots];
   __shared__ uint32_t tmem_base_s;
   __shared__ int prefix[kGrad ? 1 : kMaxExperts + 1];
+  __shared__ uint8_t order_s[kMaxSorted];
   __shared__ int warp_sum[kThreads / 32], warp_max[kThreads / 32];
   __shared__ int last_flag;
 
@@ -344,6 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     fence_mbar_init();
   }
+  __syncwarp();
+  cluster_arrive();   // the barriers are there
   if (warp == 1) tmem_alloc_pair(&tmem_base_s, kTmemCols);
   if (warp == 0 && lane < 10) {   // the descriptors' first use would wait for them
     const CUtensorMap* map = lane == 0 ? &maps.a : lane == 9 ? &maps.out : &maps.b[lane - 1];
@@ -356,12 +375,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   // The order is checked, and for a product the first item of each expert and
   // the largest row tile are found: thread i covers experts [i * per, (i + 1) * per).
   const int per = 1 + (a.E > kThreads) + (a.E > 2 * kThreads);
-  int mine = 0, most = 32, bad = 0;
+  int mine = 0, most = 32, bad = 0, cnt = 0;
 #pragma unroll 1
   for (int i = 0; i < per; ++i) {
     const int e = tid * per + i;
     if (e >= a.E) break;
-    int cnt = ld_ca(a.counts + e);
+    cnt = ld_ca(a.counts + e);
     const int off = ld_ca(a.offsets + e), next = ld_ca(a.offsets + e + 1);
     // Experts that end before the next one begins have disjoint rows.
     if (cnt < 0 || off < 0 || cnt > a.capacity || off > a.capacity - cnt || off + cnt > next) bad = 1, cnt = 0;
@@ -374,29 +393,44 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
     }
   }
-  int inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += t;
-  }
+  // (scratch: the staging that the epilogue will use)
+  int* cnt_s = reinterpret_cast<int*>(smem_raw + (smem0 - smem_u32(smem_raw)) + kStageBudget<kMode>);
+  if (a.E <= kMaxSorted && tid < kMaxSorted) cnt_s[tid] = tid < a.E ? cnt : -1;
+  int inc = kGrad ? 0 : scan_warp(mine);
   most = __reduce_max_sync(0xffffffffu, bad ? 1 << 16 : most);
   if (lane == 31) {
     warp_sum[warp] = inc;
     warp_max[warp] = most;
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  int sum = lane < kThreads / 32 ? warp_sum[lane] : 0;
   int tok = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? warp_max[lane] : 0);
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, sum, o);
-    if (lane >= o) sum += t;
+  const bool order_ok = tok < 1 << 16;   // else nothing is computed
+  if (!order_ok && tid == 0) set_status(a.status, CHORD_ERR_INVALID_ARG);
+  // With few rows in every tile a product's items take the same time.
+  const bool sorted = a.E > 1 && a.E <= kMaxSorted && (kGrad || tok > kSplitTok);
+  if (sorted) {
+    if (tid < a.E) {
+      int place = 0;
+      for (int i = 0; i < a.E; i += 4) {
+        const int4 c = *reinterpret_cast<const int4*>(cnt_s + i);
+        place += (c.x > cnt || (c.x == cnt && i < tid)) + (c.y > cnt || (c.y == cnt && i + 1 < tid)) +
+                 (c.z > cnt || (c.z == cnt && i + 2 < tid)) + (c.w > cnt || (c.w == cnt && i + 3 < tid));
+      }
+      order_s[place] = static_cast<uint8_t>(tid);
+      cnt_s[kMaxSorted + place] = mine;
+    }
+    __syncthreads();
+    if constexpr (!kGrad) {
+      mine = tid < a.E ? cnt_s[kMaxSorted + tid] : 0;
+      if (tid < a.E) prefix[tid] = 0;
+      inc = scan_warp(mine);
+      if (lane == 31) warp_sum[warp] = inc;
+      __syncthreads();
+    }
   }
-  const int run = inc - mine + (warp ? __shfl_sync(0xffffffffu, sum, warp - 1) : 0);
   if constexpr (!kGrad) {
+    const int sum = scan_warp(lane < kThreads / 32 ? warp_sum[lane] : 0);
+    const int run = inc - mine + (warp ? __shfl_sync(0xffffffffu, sum, warp - 1) : 0);
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
       const int e = tid * per + i;
@@ -405,9 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     if (tid == kThreads - 1) prefix[a.E] = run + mine;   // the last thread ends at the total
   }
-  const bool order_ok = tok < 1 << 16;   // else nothing is computed
-  if (!order_ok && tid == 0) set_status(a.status, CHORD_ERR_INVALID_ARG);
-  cluster_sync();                        // also: the peer's barriers are there
+  const uint8_t* order = sorted ? order_s : nullptr;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_wait();                        // the peer's barriers are there
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, tmem_base_s, 0);
   if (kGrad) tok = kMaxTok;
   tok = order_ok ? tok : 32;
@@ -531,12 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ----------------------------------------------------------------- items
     int slot = 0, ph = 0, e = 0;
     bool part = cluster < cut * parts;
-    int item = part ? quick_div(cluster, parts) : cut + cluster;
+    int item = part ? quick_div(cluster, parts) : cut + cluster, round = cut;
     for (bool first = true, more = !a.test_timeout; more;) {
       more = item < items;
       Seg s{};
       if (more) {
-        s = decode<kMode>(a, prefix, item, e);
+        s = decode<kMode>(a, prefix, order, item, e);
         if (part) {
           // whole stages of two steps, the last one short where their number is odd
           const int units = (s.u1 + 1) / 2, p = cluster - item * parts;
@@ -552,7 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         item_slots[slot] = s;
         mbar_arrive(&item_full[slot]);   // release: the item is visible to the waiters
       }
-      item = part ? cut + cluster : item + clusters;
+      if (!part) round += clusters;
+      item = round + cluster;
+      // forth and back over items of falling size
+      if (sorted && quick_div(round, clusters) & 1) item = round + clusters - 1 - cluster;
       part = false;
       if (++slot == kItemSlots) slot = 0, ph ^= 1, first = false;
     }

@@ -17,6 +17,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// Its two halves, for what is needed later.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // The cluster-wide address of a shared-memory object in the CTA of rank `r`.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t r) {
   uint32_t a;
