@@ -343,7 +343,7 @@ int chord_swiglu(const void* gu, int dtype, int64_t gu_stride, const float* topk
   if (rc) return rc;
   if (I > (1 << 23)) return fail(CHORD_ERR_INVALID_ARG, "I=%d > 2^23", I);
   const bool keep = codes || scales;
-  if (keep && (rc = check_mx("swiglu in 8 bits", I))) return rc;
+  if (keep && I % 32 != 0) return fail(CHORD_ERR_INVALID_ARG, "I=%d must be a multiple of 32 to be held in 8 bits", I);
   if (M == 0 || capacity == 0) return CHORD_OK;
   if ((rc = check_matrix("gu", gu, dtype, gu_stride, 2 * I, false))) return rc;
   if ((rc = check_matrix("h", h, dtype, h_stride, I, true))) return rc;
@@ -366,7 +366,7 @@ int chord_swiglu_backward(const void* dh, int dtype, int64_t dh_stride, const vo
   if (I > (1 << 23)) return fail(CHORD_ERR_INVALID_ARG, "I=%d > 2^23", I);
   const bool keep = codes || scales;
   if (keep && gu) return fail(CHORD_ERR_INVALID_ARG, "gu and its codes: one of them");
-  if (keep && (rc = check_mx("swiglu in 8 bits", I))) return rc;
+  if (keep && I % 32 != 0) return fail(CHORD_ERR_INVALID_ARG, "I=%d must be a multiple of 32 to be held in 8 bits", I);
   if (M == 0) return CHORD_OK;
   if (!dweights) return fail(CHORD_ERR_INVALID_ARG, "null pointer: dweights");
   if (capacity == 0)

@@ -80,16 +80,16 @@ constexpr int kGroupTiles = 8;         // row tiles that are taken together
 // about evenly busy.
 constexpr int kMaxSorted = 256;
 // An epilogue warp's staging: product 32 tokens x 32 weights (rows of 80
-// bytes spread over the banks); gradient two times 32 rows of 128 bytes, so that
-// one is filled while the other leaves, at the cost of a stage.
-constexpr int kOutPitch = 80, kOutBuf = 32 * 128;
+// bytes spread over the banks); gradient 32 rows of 128 bytes (twice that, at
+// the cost of a stage of the ring, gained 1.5 % where an expert's rows are few
+// and lost 4 % where they are many).
+constexpr int kOutPitch = 80;
 template <Mode kMode>
-constexpr int kOutBytes = kMode == kGradient ? 2 * kOutBuf : 32 * kOutPitch;
+constexpr int kOutBytes = kMode == kGradient ? 32 * 128 : 32 * kOutPitch;
+constexpr int kStageBudget = 6 * stage_bytes(kMaxTok);
 template <Mode kMode>
-constexpr int kStageBudget = (kMode == kGradient ? 5 : 6) * stage_bytes(kMaxTok);
-template <Mode kMode>
-constexpr int kSmemBytes = kStageBudget<kMode> + kEpiWarps * kOutBytes<kMode> + 1024;
-static_assert(kMaxStages * stage_bytes(32) <= kStageBudget<kProduct>, "stage budget");
+constexpr int kSmemBytes = kStageBudget + kEpiWarps * kOutBytes<kMode> + 1024;
+static_assert(kMaxStages * stage_bytes(32) <= kStageBudget, "stage budget");
 static_assert(kSmemBytes<kProduct> + (kMaxExperts + 1) * 4 + 2048 <= 232448, "shared memory budget");
 static_assert(kSmemBytes<kGradient> + 1536 <= 232448, "shared memory budget");
 static_assert(3 * kThreads >= kMaxExperts, "three experts per thread at most");
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
   }
   // (scratch: the staging that the epilogue will use)
-  int* cnt_s = reinterpret_cast<int*>(smem_raw + (smem0 - smem_u32(smem_raw)) + kStageBudget<kMode>);
+  int* cnt_s = reinterpret_cast<int*>(smem_raw + (smem0 - smem_u32(smem_raw)) + kStageBudget);
   if (a.E <= kMaxSorted && tid < kMaxSorted) cnt_s[tid] = tid < a.E ? cnt : -1;
   int inc = kGrad ? 0 : scan_warp(mine);
   most = __reduce_max_sync(0xffffffffu, bad ? 1 << 16 : most);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int items = !order_ok ? 0 : kGrad ? a.E * a.m_tiles * a.n_tiles : prefix[a.E];
   constexpr int subs = kSubs<kMode>;
   const int sub_bytes = stage_bytes(tok), stage = subs * sub_bytes;
-  const int n_stages = min(kMaxStages, kStageBudget<kMode> / stage);
+  const int n_stages = min(kMaxStages, kStageBudget / stage);
   // The items that are cut, and their parts: cluster i has part i % parts of
   // item i / parts, then whole items like all others.
   int cut = 0, parts = 0;
@@ -626,10 +626,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3, t = (warp - kEpiWarp0) / 4;   // TMEM lane quarter; which of the column chunks
-    const uint32_t out_stage = smem0 + kStageBudget<kMode> + (warp - kEpiWarp0) * kOutBytes<kMode>;
+    const uint32_t out_stage = smem0 + kStageBudget + (warp - kEpiWarp0) * kOutBytes<kMode>;
     const uint32_t tempty0 = cluster_addr(&tempty[0], 0);
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    int acc = 0, use = 0, buf = 0;
+    int acc = 0, use = 0;
     // A wait that ran out ends a warp; at an item that is cut, whose handling
     // has barriers, the epilogue warps end together.
     bool part = !kGrad && cluster < cut * parts;
@@ -692,10 +692,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           const int ahead = a.f32 || half ? c + width + 32 : c + 32;
           load(ahead);
           if (!half) {
-            if (lane == 0) bulk_wait_read<1>();           // the store before the last has read its staging
+            if (lane == 0) bulk_wait_read();              // the last store has read its staging
             __syncwarp();
           }
-          const uint32_t dst = out_stage + buf * kOutBuf + lane * 128;
+          const uint32_t dst = out_stage + lane * 128;
           if (a.f32) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -715,10 +715,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             const int col = w.n0 + c - 32 * half;
             if (lane == 0 && m < a.m && col < a.k) {
-              tma_store_3d(&maps.out, out_stage + buf * kOutBuf, col, m, w.e);
+              tma_store_3d(&maps.out, out_stage, col, m, w.e);
               bulk_commit_group();
             }
-            buf ^= 1;
           }
           c = ahead;
         }
