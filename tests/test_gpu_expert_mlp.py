@@ -257,3 +257,39 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for (out, grads), (want, exact) in zip(results, alone):
         assert torch.equal(out, want) and all(torch.equal(a, b) for a, b in zip(grads, exact))
+
+
+@pytest.mark.parametrize("held", [False, True])
+def test_example(held):
+    """The training example runs, and its router's and experts' gradients are those of its formula in 64 bits."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_training.py")
+    spec = importlib.util.spec_from_file_location("moe_training", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer, losses = example.train(M=96, H=64, I=32, steps=3, held_in_8_bits=held)
+    assert all(torch.isfinite(torch.tensor(losses)))
+    assert all(torch.isfinite(p).all() for p in layer.parameters())
+    if held:
+        return
+    x, target = randn(96, 64, seed=1).to(BF16), randn(96, 64, seed=2)
+    layer.zero_grad()
+    (layer(x).float() - target).square().mean().backward()
+    router, w13, w2 = (p.detach().double() for p in (layer.router, layer.w13.to(BF16), layer.w2.to(BF16)))
+    leaves = [t.requires_grad_() for t in (router, w13, w2)]
+    xd = x.double()
+    logits = xd @ router.T
+    ids = torch.topk(torch.sigmoid((x.float() @ layer.router.T)), layer.topk, 1).indices
+    score = torch.sigmoid(logits).gather(1, ids)
+    weights = score / score.sum(1, keepdim=True)
+    out = torch.zeros_like(xd)
+    for e in range(w13.shape[0]):
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        gate, up = (xd[t] @ w13[e].T).chunk(2, 1)
+        out = out.index_add(0, t, (weights[t, j][:, None] * torch.nn.functional.silu(gate) * up) @ w2[e].T)
+    (out - target.double()).square().mean().backward()
+    # the 16-bit roundings on the way (see test_expert_mlp), and that of the loss's gradient
+    tol = 12 * torch.finfo(BF16).eps / 2
+    for p, leaf in zip((layer.router, layer.w13, layer.w2), leaves):
+        assert off(p.grad, leaf.grad) <= tol
