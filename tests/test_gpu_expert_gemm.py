@@ -89,6 +89,25 @@ SHAPES = [
 @pytest.mark.parametrize("counts,K,N", SHAPES)
 def test_product(counts, K, N, transpose, dtype):
     check_product(counts, K, N, transpose, dtype)
+    if not transpose:
+        check_product(counts, K, N, False, dtype, extra=200)     # (no longer a handful of rows for the host)
+
+
+# a handful of rows: dot products, K shared by all warps, by some, by one; runs of many lengths; more rows of an
+# expert than go at once; experts without rows; more than one run a CTA (an order of other counts than the host expects)
+FEW = [
+    ([1], 8, 8), ([1], 256, 7168), ([2], 264, 72), ([3], 1000, 520), ([1, 0, 2, 0, 7], 4104, 136), ([1] * 8, 7168, 512),
+    ([0] * 500 + [1, 2] * 6, 136, 264), ([8], 520, 4096), ([1] * 100, 72, 1000), ([5] * 16, 2048, 512),
+    ([0, 64, 0, 0, 0, 0, 0, 0], 512, 264), ([1] * 12 + [0] * 4, 16400, 200), ([0] * 1000 + [3] * 24, 72, 40),
+    ([1] * 100, 520, 520),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("counts,K,N", FEW)
+def test_product_of_a_handful_of_rows(counts, K, N, dtype):
+    check_product(counts, K, N, False, dtype)
+    check_product(counts, K, N, False, dtype, gaps=[1 if i < 5 else 0 for i in range(len(counts))], seed=1)
 
 
 @pytest.mark.parametrize("transpose", [False, True])
@@ -150,7 +169,7 @@ CUT = [
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("counts,K,N", CUT)
 def test_product_cut_along_the_contraction(counts, K, N, transpose):
-    check_product(counts, N if transpose else K, K if transpose else N, transpose, BF16, gaps=[3] * len(counts))
+    check_product(counts, N if transpose else K, K if transpose else N, transpose, BF16, gaps=[3] * len(counts), extra=200)
 
 
 def test_one_workspace_for_many_calls():
@@ -164,6 +183,7 @@ def test_one_workspace_for_many_calls():
     for turn in range(6):
         for i, (counts, K, N) in enumerate(CUT):
             c, o, rows = order(counts)
+            rows += 200                  # (not a handful for the host)
             if turn == 0:
                 x = torch.randn((rows, K), generator=g, device="cuda").to(BF16)
                 w = torch.randn((len(counts), N, K), generator=g, device="cuda").to(BF16)
@@ -180,7 +200,7 @@ def test_one_workspace_for_many_calls():
 
 
 @pytest.mark.parametrize("transpose", [False, True])
-@pytest.mark.parametrize("counts,K,N", [([2] * 8, 7168, 512), ([700, 30], 1000, 328)])
+@pytest.mark.parametrize("counts,K,N", [([2] * 8, 7168, 512), ([2] * 80, 2048, 328), ([700, 30], 1000, 328)])
 def test_random_values(counts, K, N, transpose):
     """Sums of n products in FP32, in any order, are off by at most n 2^-23 of the sum of the magnitudes, and one
     rounding to BF16 by 2^-8 of the result."""

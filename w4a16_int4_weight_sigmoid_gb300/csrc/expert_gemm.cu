@@ -813,6 +813,7 @@ size_t expert_gemm_workspace_bytes() {
 }
 
 cudaError_t expert_gemm_launch(const ExpertGemm& g, cudaStream_t st) {
+  if (!g.transposed && !g.test_timeout && expert_gemv_serves(g)) return expert_gemv_launch(g, st);
   Args a{};
   a.counts = g.counts, a.offsets = g.offsets, a.status = g.status;
   a.E = g.E, a.capacity = g.capacity, a.test_timeout = g.test_timeout ? 1 : 0;

@@ -151,6 +151,9 @@ struct ExpertWgrad {
 };
 size_t expert_gemm_workspace_bytes();
 cudaError_t expert_gemm_launch(const ExpertGemm& g, cudaStream_t st);
+// The product of a handful of rows (not transposed), and whether it is the faster one.
+bool expert_gemv_serves(const ExpertGemm& g);
+cudaError_t expert_gemv_launch(const ExpertGemm& g, cudaStream_t st);
 cudaError_t expert_wgrad_launch(const ExpertWgrad& g, cudaStream_t st);
 
 // Rows in 8 bits (MXFP8): codes and scales of rows, and back; token rows into
