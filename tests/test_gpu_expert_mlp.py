@@ -170,6 +170,11 @@ def test_gradient_of_a_sum_and_of_a_transposed_input():
     w = w13.clone().requires_grad_()
     expert_product(rows, w, order).sum().backward()
     assert torch.isfinite(rows.grad).all() and torch.isfinite(w.grad).all()
+    # rows at an odd element, further apart
+    wide = torch.zeros((rows.shape[0], 67), dtype=BF16, device="cuda")
+    wide[:, 1:65] = rows.detach()
+    out = expert_product(wide[:, 1:65], w13, order)
+    assert torch.equal(out, expert_product(rows.detach(), w13, order))
 
 
 def test_routing_again_before_the_backward_pass_is_an_error():

@@ -32,9 +32,9 @@
 //     leave by TMA, which stops at the edges of dW;
 //   * the gradient's contraction ends inside a box of 64 rows.  What lies
 //     behind an expert's last row may be anything (another expert's, NaN), so
-//     a warp of each CTA zeroes up to 15 rows of both operands in shared
-//     memory before the MMAs of a last box run; MMAs that would see no row at
-//     all are left out.
+//     one of two warps of each CTA zeroes up to 15 rows of both operands in
+//     shared memory before the MMAs of a last box run; MMAs that would see no
+//     row at all are left out.
 // Rows of a product's B that are not the expert's give columns that are not
 // stored, so they need no zeroing.
 // Every mbarrier wait is bounded; see mxfp4_gemm.cu.
@@ -364,10 +364,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __syncwarp();
   cluster_arrive();   // the barriers are there
   if (warp == 1) tmem_alloc_pair(&tmem_base_s, kTmemCols);
-  if (warp == 0 && lane < 10) {   // the descriptors' first use would wait for them
-    const CUtensorMap* map = lane == 0 ? &maps.a : lane == 9 ? &maps.out : &maps.b[lane - 1];
-    if (kGrad ? lane == 0 || lane == 1 || lane == 9 : lane < 9) prefetch_tensormap(map);
-  }
   // programmatic launch: nothing above touches global memory
   grid_dep_wait();
   grid_dep_launch();

@@ -26,7 +26,10 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t r) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(r));
   return a;
 }
-// Arrivals on a barrier of either CTA (addresses of cluster_addr).
+// Arrivals on a barrier of either CTA (addresses of cluster_addr).  The first
+// kind hands over TMEM that this thread has read (its loads are complete, and
+// tcgen05 fences stand on both sides), no memory; the second what its warp wrote,
+// which takes about 0.8 us.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -143,9 +146,6 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint3
   return d;
 }
 
-__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
 // Tiled TMA loads into this CTA's shared memory by one elected lane, completing
 // on a barrier of either CTA of the pair (cluster_addr).  The inner coordinate
 // is a multiple of 8 values (16 bytes); what is out of range reads zeros.

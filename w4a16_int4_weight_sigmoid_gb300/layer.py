@@ -214,7 +214,7 @@ def unpermute_rows(y, weights, order: ExpertOrder):
 
 
 def _rows16(t):
-    """A gradient as the products read rows: 16-byte parts, rows apart from one another."""
+    """Rows as the products read them: 16-byte parts, rows apart from one another."""
     t = _unit_columns(t)
     fine = t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or (t.stride(0) % 8 == 0 and t.stride(0) >= t.shape[1]))
     return t if fine else t.clone(memory_format=torch.contiguous_format)
@@ -269,7 +269,7 @@ def expert_product(rows, w, order: ExpertOrder):
     if rows.shape[0] != order.capacity or w.shape[0] != order.E_local:
         raise ValueError(f"rows must hold the {order.capacity} rows of the order and w its {order.E_local} experts, "
                          f"got {rows.shape[0]} and {w.shape[0]}")
-    return _ExpertProduct.apply(rows, w, order)
+    return _ExpertProduct.apply(_rows16(rows), w, order)
 
 
 class _ExpertMLP(torch.autograd.Function):
