@@ -230,3 +230,27 @@ def test_equal_experts_in_many_rounds():
     """More items than clusters, dealt forth and back."""
     check_product([96] * 60, 136, 1288, False, BF16)
     check_wgrad([96] * 60, 520, 520, BF16, BF16)
+
+
+@pytest.mark.parametrize("count", [767, 768, 769, 832, 1536, 1537, 3000, 5001])
+def test_fp32_gradient_added_up_in_parts(count):
+    """Sums over more than 768 rows: the parts between others' rows, edges of dW, an empty expert, short ones."""
+    check_wgrad([count, 0, 70], 328, 264, BF16, FP32, gaps=[3, 0, 5], extra=70)
+
+
+@pytest.mark.parametrize("mean", [0.0, 1.0])
+def test_fp32_gradient_of_many_rows_keeps_its_accuracy(mean):
+    """16 rows at a time go into an FP32 sum that is cut off: 48 times 2^-23 of the partial sum at most in a part, and
+    each of the 11 additions of parts rounds by 2^-24: below 2^-17 of the sum of the magnitudes.  The result was off by
+    2e-5 of itself in the 2-norm where one sum took all rows; here by less than 3e-6 (48 / 2 cuts of 2^-24 on average,
+    against sums of growing size)."""
+    rows = 8192
+    g = torch.Generator(device="cuda").manual_seed(1)
+    c, o, _ = order([rows])
+    d = (torch.randn((rows, 256), generator=g, device="cuda") + mean).to(BF16)
+    x = (torch.randn((rows, 264), generator=g, device="cuda") + mean).to(BF16)
+    got = wgrad(d, x, c, o, FP32)[0].double()
+    want, size = d.double().T @ x.double(), d.double().abs().T @ x.double().abs()
+    assert ((got - want).abs() <= 2.0 ** -17 * size).all()
+    assert (got - want).norm() <= 3e-6 * want.norm()
+    assert torch.equal(got, wgrad(d, x, c, o, FP32)[0].double())

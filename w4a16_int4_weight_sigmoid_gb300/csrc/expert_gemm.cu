@@ -87,6 +87,13 @@ constexpr int kOutPitch = 80;
 template <Mode kMode>
 constexpr int kOutBytes = kMode == kGradient ? 32 * 128 : 32 * kOutPitch;
 constexpr int kStageBudget = 6 * stage_bytes(kMaxTok);
+// The tensor cores cut their sums off toward zero, once for each 16 of the
+// contraction: over n rows a gradient's FP32 sums come out about 1e-9 n too
+// small (measured: 4e-6 at 4096 rows, 2e-5 at 16384, where FP32 sums in another
+// order have 3e-7).  An FP32 gradient is therefore added up, rounding to
+// nearest, from parts of at most this many boxes (768 rows: 8e-7); in 16 bits
+// the result's own rounding is 25 times 2e-5.
+constexpr int kExactBoxes = 12;
 template <Mode kMode>
 constexpr int kSmemBytes = kStageBudget + kEpiWarps * kOutBytes<kMode> + 1024;
 static_assert(kMaxStages * stage_bytes(32) <= kStageBudget, "stage budget");
@@ -564,10 +571,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     int slot = 0, ph = 0, e = 0;
     bool part = cluster < cut * parts;
     int item = part ? quick_div(cluster, parts) : cut + cluster, round = cut;
+    int boxes = 0, piece = 0;            // of a gradient's item, and of each of its parts
+    Seg s{};
     for (bool first = true, more = !a.test_timeout; more;) {
-      more = item < items;
-      Seg s{};
-      if (more) {
+      if (kGrad && s.u1 < boxes) {       // the item's next part
+        s.u0 = s.u1;
+        s.u1 = min(boxes, s.u0 + piece);
+      } else if ((more = item < items)) {
         s = decode<kMode>(a, prefix, order, item, e);
         if (part) {
           // whole stages of two steps, the last one short where their number is odd
@@ -576,6 +586,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           s.u1 = min(s.u1, 2 * quick_div((p + 1) * units, parts));
           s.n0 = item;
         }
+        boxes = s.u1;
+        if (kGrad && a.f32 && boxes > kExactBoxes) {
+          const int n = (boxes + kExactBoxes - 1) / kExactBoxes;
+          s.u1 = piece = (boxes + n - 1) / n;
+        }
+        if (!part) round += clusters;
+        item = round + cluster;
+        // forth and back over items of falling size
+        if (sorted && quick_div(round, clusters) & 1) item = round + clusters - 1 - cluster;
+        part = false;
       } else {
         s.u1 = -1;
       }
@@ -584,11 +604,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         item_slots[slot] = s;
         mbar_arrive(&item_full[slot]);   // release: the item is visible to the waiters
       }
-      if (!part) round += clusters;
-      item = round + cluster;
-      // forth and back over items of falling size
-      if (sorted && quick_div(round, clusters) & 1) item = round + clusters - 1 - cluster;
-      part = false;
       if (++slot == kItemSlots) slot = 0, ph ^= 1, first = false;
     }
   } else if (kGrad && (warp == kZeroWarp0 || warp == kZeroWarp1)) {
@@ -599,9 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     int turn = 0;
     uint32_t tail_ph = 0;                // of this warp's barriers: one turns when its slot holds a last box
     while (ring.next(w, ok, a.status)) {
-      st = (st + w.u1) % n_stages;
+      st = (st + w.u1 - w.u0) % n_stages;
       const int last = w.rows % kStageK;
-      if (!(last & 15)) continue;
+      if (!(last & 15) || w.u1 * kStageK < w.rows) continue;
       turn ^= 1;
       if (turn == mine) continue;        // the other warp's: turn was its number
       // Every phase of a warp's barriers is waited for, in order.
@@ -678,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         };
         int c = width * t;
         load(c);
+        if (w.u0 > 0 && lane == 0) bulk_wait_all();       // the item's parts before are there to be added to
 #pragma unroll 1
         while (c < w.cols) {
           uint32_t v[32];
@@ -711,7 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             const int col = w.n0 + c - 32 * half;
             if (lane == 0 && m < a.m && col < a.k) {
-              tma_store_3d(&maps.out, out_stage, col, m, w.e);
+              if (w.u0 > 0) tma_add_3d(&maps.out, out_stage, col, m, w.e);
+              else tma_store_3d(&maps.out, out_stage, col, m, w.e);
               bulk_commit_group();
             }
           }
