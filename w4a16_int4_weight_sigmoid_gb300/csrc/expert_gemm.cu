@@ -47,14 +47,15 @@
 namespace chord {
 namespace {
 
-enum Mode { kProduct, kTransposed, kGradient };
+enum Mode { kProduct, kTransposed, kGradient, kGradient32 };   // the last: dW in FP32
+constexpr bool is_gradient(Mode m) { return m >= kGradient; }
 
 constexpr int kMaxTok = 256;           // largest row tile (columns of the accumulator)
 constexpr int kTileM = 256;            // of the pair
 constexpr int kStageK = 64;
 constexpr int kABytes = 128 * kStageK * 2;
 template <Mode kMode>
-constexpr int kSubs = kMode == kGradient ? 1 : 2;  // steps of 64 of the contraction in a stage
+constexpr int kSubs = is_gradient(kMode) ? 1 : 2;  // steps of 64 of the contraction in a stage
 constexpr int kSplitTok = 64;          // largest row tile of items that are cut
 constexpr int kSlotFloats = kSplitTok * 128;       // one CTA's part of an item that is cut
 constexpr int kMaxCtas = 160;
@@ -85,7 +86,7 @@ constexpr int kMaxSorted = 256;
 // and lost 4 % where they are many).
 constexpr int kOutPitch = 80;
 template <Mode kMode>
-constexpr int kOutBytes = kMode == kGradient ? 32 * 128 : 32 * kOutPitch;
+constexpr int kOutBytes = is_gradient(kMode) ? 32 * 128 : 32 * kOutPitch;
 constexpr int kStageBudget = 6 * stage_bytes(kMaxTok);
 // The tensor cores cut their sums off toward zero, once for each 16 of the
 // contraction: over n rows a gradient's FP32 sums come out about 1e-9 n too
@@ -112,7 +113,6 @@ struct Args {
   int E, capacity;
   int m, k;              // product: weights' side of the output, contraction; gradient: N, K
   int m_tiles, n_tiles;  // tiles of 256
-  int f32;               // gradient: dW in FP32
   int test_timeout;      // test of the timeout path: no item is handed out, waits for one are short
 };
 // The product's B boxes (rows of x) have the height of half a row tile: one
@@ -150,7 +150,7 @@ template <Mode kMode>
 __device__ __forceinline__ Seg decode(const Args& a, const int* prefix, const uint8_t* order, int item, int& e) {
   const int lane = threadIdx.x & 31;
   Seg s{};
-  if constexpr (kMode == kGradient) {
+  if constexpr (is_gradient(kMode)) {
     const int per = a.m_tiles * a.n_tiles;
     e = quick_div(item, per);
     const int local = item - e * per, mt = quick_div(local, a.n_tiles);
@@ -332,7 +332,7 @@ __device__ __forceinline__ void add_parts(const float* partial, int first, int p
 template <Mode kMode, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     expert_gemm_kernel(const __grid_constant__ Maps maps, const Args a) {
-  constexpr bool kGrad = kMode == kGradient;
+  constexpr bool kGrad = is_gradient(kMode), kF32 = kMode == kGradient32;
   constexpr bool kMnA = kMode != kProduct, kMnB = kGrad;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[2][kMaxStages];   // tail: of each zeroing warp
@@ -571,10 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     int slot = 0, ph = 0, e = 0;
     bool part = cluster < cut * parts;
     int item = part ? quick_div(cluster, parts) : cut + cluster, round = cut;
-    int boxes = 0, piece = 0;            // of a gradient's item, and of each of its parts
+    int boxes = 0, piece = 0;            // of an FP32 gradient's item, and of each of its parts
     Seg s{};
     for (bool first = true, more = !a.test_timeout; more;) {
-      if (kGrad && s.u1 < boxes) {       // the item's next part
+      if (kF32 && s.u1 < boxes) {        // the item's next part
         s.u0 = s.u1;
         s.u1 = min(boxes, s.u0 + piece);
       } else if ((more = item < items)) {
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           s.n0 = item;
         }
         boxes = s.u1;
-        if (kGrad && a.f32 && boxes > kExactBoxes) {
+        if (kF32 && boxes > kExactBoxes) {
           const int n = (boxes + kExactBoxes - 1) / kExactBoxes;
           s.u1 = piece = (boxes + n - 1) / n;
         }
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     while (ring.next(w, ok, a.status)) {
       st = (st + w.u1 - w.u0) % n_stages;
       const int last = w.rows % kStageK;
-      if (!(last & 15) || w.u1 * kStageK < w.rows) continue;
+      if (!(last & 15) || (kF32 && w.u1 * kStageK < w.rows)) continue;
       turn ^= 1;
       if (turn == mine) continue;        // the other warp's: turn was its number
       // Every phase of a warp's barriers is waited for, in order.
@@ -683,56 +683,56 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           store_rows<kF16>(a, v[0], v[1], out + c0 * a.ldo, out_stage, m, lane, w.rows - c0);
         }
       } else {
-        // 32 columns at a time, the next ones on their way; chunks of 128 bytes
-        // of dW's rows leave by TMA, 16-byte parts swizzled with the row
-        const int width = a.f32 ? 32 : 64;
-        const bool live = w.rows > 0;
+        // chunks of 128 bytes of dW's rows leave by TMA, 16-byte parts swizzled
+        // with the row; 32 columns at a time, the next ones on their way
+        constexpr int width = kF32 ? 32 : 64;
+        const uint32_t dst = out_stage + lane * 128;
         uint32_t next[32];
         auto load = [&](int c) {
-          if (live && c < w.cols) tmem_ld_32x32b_x32(taddr + c, next);
-        };
-        int c = width * t;
-        load(c);
-        if (w.u0 > 0 && lane == 0) bulk_wait_all();       // the item's parts before are there to be added to
-#pragma unroll 1
-        while (c < w.cols) {
-          uint32_t v[32];
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = live ? next[i] : 0;
-          const int half = a.f32 ? 0 : (c >> 5) & 1;      // of the chunk
-          const int ahead = a.f32 || half ? c + width + 32 : c + 32;
-          load(ahead);
-          if (!half) {
-            if (lane == 0) bulk_wait_read();              // the last store has read its staging
-            __syncwarp();
-          }
-          const uint32_t dst = out_stage + lane * 128;
-          if (a.f32) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              st_shared_v4(dst + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          if (w.rows > 0 && c < w.cols) {
+            tmem_ld_32x32b_x32(taddr + c, next);
           } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t p[4];
+            for (int i = 0; i < 32; ++i) next[i] = 0;
+          }
+        };
+        load(width * t);
+        if (kF32 && w.u0 > 0 && lane == 0) bulk_wait_all();   // the item's parts before are there to be added to
+#pragma unroll 1
+        for (int c0 = width * t; c0 < w.cols; c0 += 2 * width) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                p[i] = pack2<kF16>(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
-              st_shared_v4(dst + (((j + 4 * half) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+          for (int half = 0; half < width / 32; ++half) {
+            uint32_t v[32];
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = next[i];
+            load(half + 1 < width / 32 ? c0 + 32 : c0 + 2 * width);
+            if (half == 0) {
+              if (lane == 0) bulk_wait_read();                // the last store has read its staging
+              __syncwarp();
+            }
+            if constexpr (kF32) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                st_shared_v4(dst + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  p[i] = pack2<kF16>(__uint_as_float(v[8 * j + 2 * i]), __uint_as_float(v[8 * j + 2 * i + 1]));
+                st_shared_v4(dst + (((j + 4 * half) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+              }
             }
           }
-          if (a.f32 || half || c + 32 >= w.cols) {        // a chunk is complete
-            fence_proxy_async_smem();
-            __syncwarp();
-            const int col = w.n0 + c - 32 * half;
-            if (lane == 0 && m < a.m && col < a.k) {
-              if (w.u0 > 0) tma_add_3d(&maps.out, out_stage, col, m, w.e);
-              else tma_store_3d(&maps.out, out_stage, col, m, w.e);
-              bulk_commit_group();
-            }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && m < a.m && w.n0 + c0 < a.k) {
+            if (kF32 && w.u0 > 0) tma_add_3d(&maps.out, out_stage, w.n0 + c0, m, w.e);
+            else tma_store_3d(&maps.out, out_stage, w.n0 + c0, m, w.e);
+            bulk_commit_group();
           }
-          c = ahead;
         }
       }
       tc_fence_before();
@@ -849,7 +849,7 @@ cudaError_t expert_wgrad_launch(const ExpertWgrad& g, cudaStream_t st) {
   Args a{};
   a.counts = g.counts, a.offsets = g.offsets, a.status = g.status;
   a.E = g.E, a.capacity = g.capacity, a.test_timeout = g.test_timeout ? 1 : 0;
-  a.m = g.N, a.k = g.K, a.f32 = g.f32 ? 1 : 0;
+  a.m = g.N, a.k = g.K;
   a.m_tiles = (g.N + kTileM - 1) / kTileM;
   a.n_tiles = (g.K + kMaxTok - 1) / kMaxTok;
   Maps maps{};
@@ -857,6 +857,7 @@ cudaError_t expert_wgrad_launch(const ExpertWgrad& g, cudaStream_t st) {
       !encode(&maps.b[0], g.x, g.f16, false, g.K, g.capacity, g.ldx, 0, 0, kStageK) ||
       !encode(&maps.out, g.dw, g.f16, g.f32, g.K, g.N, g.K, g.E, static_cast<long long>(g.N) * g.K, 32))
     return cudaErrorInvalidValue;
+  if (g.f32) return g.f16 ? launch<kGradient32, true>(maps, a, st) : launch<kGradient32, false>(maps, a, st);
   return g.f16 ? launch<kGradient, true>(maps, a, st) : launch<kGradient, false>(maps, a, st);
 }
 
