@@ -68,8 +68,14 @@ constexpr int kMaxStages = 10, kMaxAcc = 8;
 __host__ __device__ constexpr int stage_bytes(int tok) { return kABytes + tok / 2 * kStageK * 2; }
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
 constexpr int kItemWarp = 2;
-// Two zeroing warps take items in turn: each one's release to the other CTA's
-// MMAs takes about 0.8 us, half of a short item's time (few rows 489 -> 457 us).
+// Two zeroing warps take items in turn.  They hand the zeros to the MMAs of the
+// leading CTA: from the other one by a release at cluster scope, 0.8 us, or by a
+// copy of 128 bytes of zeros that completes there.  The copy is faster (170 rows
+// an expert 512 us against 571, 341 rows 743 / 836).  But where items have two
+// boxes or less and DRAM sets the pace, the slow way keeps the CTAs in step, and
+// dW's lines reach DRAM in a better order (21 rows 443 us against 485, 43 rows 440
+// / 492, 85 rows 461 / 486; 128 rows 506 / 475; 48 experts of 4096 x 7168).
+constexpr int kPacedBoxes = 2;
 constexpr int kZeroWarp0 = 3, kZeroWarp1 = kEpiWarp0 + kEpiWarps;
 constexpr int kThreads = 32 * (kZeroWarp1 + 1);
 constexpr int kItemSlots = 8;
@@ -116,7 +122,7 @@ struct Args {
   int test_timeout;      // test of the timeout path: no item is handed out, waits for one are short
 };
 // The product's B boxes (rows of x) have the height of half a row tile: one
-// map for each multiple of 16.
+// map for each multiple of 16.  A gradient's b[0] has 64 rows, b[1] one.
 struct Maps {
   CUtensorMap a, b[8], out;
 };
@@ -344,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __shared__ uint8_t order_s[kMaxSorted];
   __shared__ int warp_sum[kThreads / 32], warp_max[kThreads / 32];
   __shared__ int last_flag;
+  __shared__ alignas(128) uint8_t note[kGrad ? 2 : 1][128];   // where each zeroing warp's copy goes
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
@@ -632,7 +639,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           st_shared_v4(base + b * kBlockBytes + r * 128, 0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_release_cluster(full0 + 8 * at);
+      if (w.u1 - w.u0 <= kPacedBoxes) {
+        if (lane == 0) mbar_arrive_release_cluster(full0 + 8 * at);
+      } else if (rank == 0) {
+        if (lane == 0) mbar_arrive(&full[at]);
+      } else {
+        // a copy that this thread starts after its fence: what it completes on
+        // the other CTA's barrier comes after the zeros
+        mbar_arrive_expect_tx_cluster_elect(full0 + 8 * at, 128);
+        tma_pair_2d_elect(smem_u32(note[mine]), &maps.b[1], 0, a.capacity, full0 + 8 * at);
+      }
     }
   } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
     // -------------------------------------------------------------- epilogue
@@ -859,6 +875,7 @@ cudaError_t expert_wgrad_launch(const ExpertWgrad& g, cudaStream_t st) {
   Maps maps{};
   if (!encode(&maps.a, g.dout, g.f16, false, g.N, g.capacity, g.ldd, 0, 0, kStageK) ||
       !encode(&maps.b[0], g.x, g.f16, false, g.K, g.capacity, g.ldx, 0, 0, kStageK) ||
+      !encode(&maps.b[1], g.x, g.f16, false, g.K, g.capacity, g.ldx, 0, 0, 1) ||
       !encode(&maps.out, g.dw, g.f16, g.f32, g.K, g.N, g.K, g.E, static_cast<long long>(g.N) * g.K, 32))
     return cudaErrorInvalidValue;
   if (g.f32) return g.f16 ? launch<kGradient32, true>(maps, a, st) : launch<kGradient32, false>(maps, a, st);
