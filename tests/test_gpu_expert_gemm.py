@@ -254,3 +254,19 @@ def test_fp32_gradient_of_many_rows_keeps_its_accuracy(mean):
     assert ((got - want).abs() <= 2.0 ** -17 * size).all()
     assert (got - want).norm() <= 3e-6 * want.norm()
     assert torch.equal(got, wgrad(d, x, c, o, FP32)[0].double())
+
+
+@pytest.mark.parametrize("K,N", [(1 << 20, 8), (8, 1 << 20)])
+def test_the_largest_sizes(K, N):
+    """Up to 2^20 of N and K: the sums of 2^20 products of at most 4 are below 2^24, exact in FP32."""
+    for transpose in (False, True):
+        check_product([3, 0, 1], K, N, transpose, BF16)
+        check_product([3, 0, 1], K, N, transpose, BF16, extra=200)
+    check_wgrad([3, 0, 1], K, N, BF16, FP32)
+
+
+def test_no_rows_at_all():
+    for extra in (3, 300):
+        for transpose in (False, True):
+            check_product([0, 0, 0], 64, 72, transpose, BF16, extra=extra)
+        check_wgrad([0, 0, 0], 64, 72, BF16, BF16, extra=extra)

@@ -298,3 +298,45 @@ def test_example(held):
     tol = 12 * torch.finfo(BF16).eps / 2
     for p, leaf in zip((layer.router, layer.w13, layer.w2), leaves):
         assert off(p.grad, leaf.grad) <= tol
+
+
+def test_without_gradients():
+    """The same output in inference mode and without gradients, also with an order made there."""
+    order, x, w13, w2, _ = make(64, 128, 96, 8, 8, 2)
+    w = order.topk_weights
+    want = run(order, x, w, w13, w2, torch.zeros_like(x), True)[0]
+    with torch.no_grad():
+        assert torch.equal(expert_mlp(x, w, w13, w2, order), want)
+    with torch.inference_mode():
+        inner = ExpertOrder(64, 2, 0, 8, 16).route(randn(64, 8), torch.zeros(8, device="cuda"))
+        assert torch.equal(expert_mlp(x, inner.topk_weights, w13, w2, inner), want)
+    leaf = w13.clone().requires_grad_()
+    out = expert_mlp(x, w, leaf, w2, inner)
+    out.sum().backward()
+    assert torch.equal(out.detach(), want) and torch.isfinite(leaf.grad).all()
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import torch
+from w4a16_int4_weight_sigmoid_gb300.layer import ExpertOrder, expert_mlp
+order = ExpertOrder(40, 2, 0, 4).route(torch.randn(40, 4, device="cuda"), torch.zeros(4, device="cuda"))
+x = torch.randn(40, 64, device="cuda").bfloat16()
+w13, w2 = torch.randn(4, 64, 64, device="cuda").bfloat16(), torch.randn(4, 64, 32, device="cuda").bfloat16()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = expert_mlp(x, order.topk_weights, w13, w2, order)
+graph.replay()
+assert torch.equal(out, expert_mlp(x, order.topk_weights, w13, w2, order))
+print("FINE")
+"""
+
+
+def test_the_first_call_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "FINE" in r.stdout, r.stdout + r.stderr
