@@ -79,6 +79,11 @@ constexpr int kPacedBoxes = 2;
 constexpr int kZeroWarp0 = 3, kZeroWarp1 = kEpiWarp0 + kEpiWarps;
 constexpr int kThreads = 32 * (kZeroWarp1 + 1);
 constexpr int kItemSlots = 8;
+// Barriers in one array, so that each is initialised by a thread of its own (one
+// thread for all took 0.15 us of every launch).
+constexpr int kEmptyBar = kMaxStages, kTfullBar = kEmptyBar + kMaxStages, kTemptyBar = kTfullBar + kMaxAcc,
+              kItemFullBar = kTemptyBar + kMaxAcc, kItemEmptyBar = kItemFullBar + kItemSlots,
+              kDoneBar = kItemEmptyBar + kItemSlots, kTailBar = kDoneBar + 1, kBars = kTailBar + 2 * kMaxStages;
 constexpr int kMaxExperts = 1024;
 constexpr int kTmemCols = 512;
 constexpr int kGroupTiles = 8;         // row tiles that are taken together
@@ -106,6 +111,7 @@ constexpr int kSmemBytes = kStageBudget + kEpiWarps * kOutBytes<kMode> + 1024;
 static_assert(kMaxStages * stage_bytes(32) <= kStageBudget, "stage budget");
 static_assert(kSmemBytes<kProduct> + (kMaxExperts + 1) * 4 + 2048 <= 232448, "shared memory budget");
 static_assert(kSmemBytes<kGradient> + 1536 <= 232448, "shared memory budget");
+static_assert(kBars <= kThreads, "a thread for each barrier");
 static_assert(3 * kThreads >= kMaxExperts, "three experts per thread at most");
 
 struct Args {
@@ -341,9 +347,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   constexpr bool kGrad = is_gradient(kMode), kF32 = kMode == kGradient32;
   constexpr bool kMnA = kMode != kProduct, kMnB = kGrad;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tail[2][kMaxStages];   // tail: of each zeroing warp
-  __shared__ __align__(8) uint64_t tfull[kMaxAcc], tempty[kMaxAcc], done_bar;
-  __shared__ __align__(8) uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+  __shared__ __align__(8) uint64_t bars[kBars];
+  uint64_t *full = bars, *empty = bars + kEmptyBar, *tfull = bars + kTfullBar, *tempty = bars + kTemptyBar;
+  uint64_t *item_full = bars + kItemFullBar, *item_empty = bars + kItemEmptyBar, *done_bar = bars + kDoneBar;
+  uint64_t* tail = bars + kTailBar;      // [zeroing warp][stage]
   __shared__ Seg item_slots[kItemSlots];
   __shared__ uint32_t tmem_base_s;
   __shared__ int prefix[kGrad ? 1 : kMaxExperts + 1];
@@ -357,22 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
   const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
 
-  if (tid == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(&full[s], 2);              // of the leading CTA: each CTA's bytes, or its zeroing warp
-      mbar_init(&empty[s], 1);
-      mbar_init(&tail[0][s], 1);
-      mbar_init(&tail[1][s], 1);
-    }
-    for (int b = 0; b < kMaxAcc; ++b) {
-      mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * kEpiWarps);   // of the leading CTA
-    }
-    mbar_init(&done_bar, 1);
-    for (int q = 0; q < kItemSlots; ++q) {
-      mbar_init(&item_full[q], 1);
-      mbar_init(&item_empty[q], 1 + (rank == 0 ? 1 : 0) + (kGrad ? 2 : 0) + kEpiWarps);
-    }
+  if (tid < kBars) {
+    int count = 1;
+    if (tid < kEmptyBar) count = 2;                                  // of the leading CTA: each CTA's bytes, or zeros
+    if (tid >= kTemptyBar && tid < kItemFullBar) count = 2 * kEpiWarps;   // of the leading CTA
+    if (tid >= kItemEmptyBar && tid < kDoneBar) count = 1 + (rank == 0 ? 1 : 0) + (kGrad ? 2 : 0) + kEpiWarps;
+    mbar_init(&bars[tid], count);
     fence_mbar_init();
   }
   __syncwarp();
@@ -496,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int here = min(subs, w.u1 - u0);
         const int left = w.rows - u0 * kStageK;            // (gradient)
         if (kGrad && left < kStageK && (left & 15)) {
-          bar = smem_u32(&tail[turn][st]);
-          mbar_arrive_expect_tx_elect(&tail[turn][st], bytes);
+          bar = smem_u32(&tail[turn * kMaxStages + st]);
+          mbar_arrive_expect_tx_elect(&tail[turn * kMaxStages + st], bytes);
           turn ^= 1;
         } else {
           mbar_arrive_expect_tx_cluster_elect(bar, here * bytes);
@@ -570,8 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     // all issued MMAs complete before TMEM can be freed
     if (issued) {
-      tc_commit_pair_local_elect(&done_bar);
-      ok = mbar_wait(&done_bar, 0, a.status) && ok;
+      tc_commit_pair_local_elect(done_bar);
+      ok = mbar_wait(done_bar, 0, a.status) && ok;
     }
   } else if (warp == kItemWarp) {
     // ----------------------------------------------------------------- items
@@ -628,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (turn == mine) continue;        // the other warp's: turn was its number
       // Every phase of a warp's barriers is waited for, in order.
       const int at = (st ? st : n_stages) - 1;
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&tail[mine][at], (tail_ph >> at) & 1, a.status)))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&tail[mine * kMaxStages + at], (tail_ph >> at) & 1, a.status)))) break;
       tail_ph ^= 1u << at;
       // rows last .. next multiple of 16 of the four blocks of 64 values
       const uint32_t base = smem0 + at * stage + (lane & 7) * 16;
