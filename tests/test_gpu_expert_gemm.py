@@ -270,3 +270,17 @@ def test_no_rows_at_all():
         for transpose in (False, True):
             check_product([0, 0, 0], 64, 72, transpose, BF16, extra=extra)
         check_wgrad([0, 0, 0], 64, 72, BF16, BF16, extra=extra)
+
+
+# the items of a last round that would leave half of the clusters idle are divided: few items in all, few behind
+# whole rounds, one, edges that leave a slice nothing
+@pytest.mark.parametrize("counts,K,N", [
+    ([200], 136, 264), ([256] * 3, 64, 512), ([255] * 20, 72, 1024), ([90] * 77, 64, 200), ([33, 250, 100], 328, 2056),
+    ([129], 1000, 8), ([70], 8, 520), ([1024], 264, 264),
+])
+def test_last_rounds(counts, K, N):
+    for transpose in (False, True):
+        check_product(counts, K, N, transpose, BF16, gaps=[1] * len(counts), extra=200)
+    for out in (BF16, FP32):
+        check_wgrad(counts, K, N, BF16, out, gaps=[1] * len(counts))
+        check_wgrad(counts, N, K, BF16, out, gaps=[1] * len(counts))
