@@ -503,7 +503,8 @@ int chord_mxfp4_moe_gemm(const void* rows, size_t rows_bytes, const void* packed
  * chord_moe_unpermute, or decode with 16-bit weights.  Expert e's rows are the
  * expert_counts[e] rows from expert_offsets[e] on: any number of rows, none
  * too, from any row on, an expert's last before the next one's first
- * (chord_moe_align's order is one; padding is not needed).
+ * (chord_moe_align's order is one; padding is not needed).  expert_offsets has
+ * E_local + 1 entries, the last one at or behind the last expert's end.
  *   gemm    out[r, n] = sum_k x[r, k] w[e, n, k]                  transpose_w 0
  *           out[r, k] = sum_n x[r, n] w[e, n, k]                  transpose_w 1
  *           (the second is the gradient of the first one's x, with dout for x)
@@ -513,7 +514,8 @@ int chord_mxfp4_moe_gemm(const void* rows, size_t rows_bytes, const void* packed
  * and rounded once; dw is of `dtype` or FP32 (`dw_dtype`), contiguous.  Rows
  * of out that are no expert's are not written, and rows that are no expert's
  * reach no result, whatever they hold.
- *   N, K       multiples of 8 (16-byte accesses), up to 2^20
+ *   N, K       multiples of 8 (16-byte accesses), up to 2^20; rows that begin
+ *              on 128-byte boundaries are read fastest
  *   *_stride   in elements, multiples of 8; rows do not overlap.  Bases are
  *              16-byte aligned
  *   capacity   rows of x, dout and out

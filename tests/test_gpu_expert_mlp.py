@@ -110,7 +110,8 @@ def test_8_bits_keep_less_memory():
         kept = []
         with torch.autograd.graph.saved_tensors_hooks(lambda t: kept.append(t) or t, lambda t: t):
             expert_mlp(x, order.topk_weights, leaf, w2, order, held)
-        large = [t for t in kept if t.numel() * t.element_size() > 1e5 and t.data_ptr() not in (w13.data_ptr(), w2.data_ptr())]
+        large = [t for t in kept if t.numel() * t.element_size() > 1e5
+                 and t.data_ptr() not in (w13.data_ptr(), w2.data_ptr())]
         sizes[held] = sum(t.numel() * t.element_size() for t in large)
     assert 0 < sizes[True] <= sizes[False] * 33 / 64
 
