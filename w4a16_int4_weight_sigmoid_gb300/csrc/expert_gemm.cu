@@ -32,9 +32,9 @@
 //     leave by TMA, which stops at the edges of dW;
 //   * the gradient's contraction ends inside a box of 64 rows.  What lies
 //     behind an expert's last row may be anything (another expert's, NaN), so
-//     one of two warps of each CTA zeroes up to 15 rows of both operands in
-//     shared memory before the MMAs of a last box run; MMAs that would see no
-//     row at all are left out.
+//     a warp of the leading CTA has up to 15 rows of both operands filled with
+//     zeros in both CTAs' shared memory before the MMAs of a last box run; MMAs
+//     that would see no row at all are left out.
 // Rows of a product's B that are not the expert's give columns that are not
 // stored, so they need no zeroing.
 // Every mbarrier wait is bounded; see mxfp4_gemm.cu.
@@ -68,16 +68,25 @@ constexpr int kMaxStages = 10, kMaxAcc = 8;
 __host__ __device__ constexpr int stage_bytes(int tok) { return kABytes + tok / 2 * kStageK * 2; }
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
 constexpr int kItemWarp = 2;
-// Two zeroing warps take items in turn.  They hand the zeros to the MMAs of the
-// leading CTA: from the other one by a release at cluster scope, 0.8 us, or by a
-// copy of 128 bytes of zeros that completes there.  The copy is faster (170 rows
-// an expert 512 us against 571, 341 rows 743 / 836).  But where items have two
-// boxes or less and DRAM sets the pace, the slow way keeps the CTAs in step, and
-// dW's lines reach DRAM in a better order (21 rows 443 us against 485, 43 rows 440
-// / 492, 85 rows 461 / 486; 128 rows 506 / 475; 48 experts of 4096 x 7168).
-constexpr int kPacedBoxes = 2;
+// Two zeroing warps of the leading CTA take items in turn.  Both CTAs' last box
+// completes on a barrier of theirs.  Then they start copies from behind the
+// tensor's end, which fill with zeros, to the same rows of both CTAs; these
+// complete on the stage's barrier, for which the MMAs wait anyway, so that nothing
+// but completed copies has to be seen from the other CTA.  (Zeros stored by threads
+// of the CTA that holds them need a release at cluster scope, 0.8 us, zeros stored
+// into the other CTA a fence: 170 rows an expert 571 and 541 us, 341 rows 836 and
+// 835; here 533 and 757.)
 constexpr int kZeroWarp0 = 3, kZeroWarp1 = kEpiWarp0 + kEpiWarps;
 constexpr int kThreads = 32 * (kZeroWarp1 + 1);
+// Where a dW passes through DRAM and its tiles have one box, what the clusters
+// store sets the pace, and they drift apart: dW's lines then reach DRAM in a worse
+// order.  A fence at cluster scope for each such box (two in FP32: twice the bytes)
+// slows the zeroing warps to about that pace and keeps the clusters in step: 48
+// experts of 4096 x 7168 with 43 rows each 494 us without, 431 with it, FP32 960
+// and 916; 48 of 2048 x 2048 75.5 / 72.0.  Where dW nearly fits in L2 (129 MB) it
+// only takes time: 128 MB 25.9 without, 26.4 with it, 192 MB 35.7 / 35.4, 256 MB
+// 46.4 / 45.9, FP32 of 256 MB 49.6 / 49.6.
+constexpr size_t kPacedBytes = size_t{256} << 20;
 constexpr int kItemSlots = 8;
 // Barriers in one array, so that each is initialised by a thread of its own (one
 // thread for all took 0.15 us of every launch).
@@ -125,10 +134,12 @@ struct Args {
   int E, capacity;
   int m, k;              // product: weights' side of the output, contraction; gradient: N, K
   int m_tiles, n_tiles;  // tiles of 256
+  int paced;             // (gradient)
   int test_timeout;      // test of the timeout path: no item is handed out, waits for one are short
 };
 // The product's B boxes (rows of x) have the height of half a row tile: one
-// map for each multiple of 16.  A gradient's b[0] has 64 rows, b[1] one.
+// map for each multiple of 16.  A gradient's b[0] has 64 rows, its b[3] to b[7]
+// have 1, 2, 4, 8 and 16, for zeros.
 struct Maps {
   CUtensorMap a, b[8], out;
 };
@@ -148,6 +159,10 @@ __device__ __forceinline__ int quick_div(int a, int b) {
   q -= q * b > a;
   q += (q + 1) * b <= a;
   return q;
+}
+// Whether a gradient's last box of an expert passes through a zeroing warp.
+__device__ __forceinline__ bool zeroed(const Args& a, int rows) {
+  return (rows & 15) || (a.paced && rows > 0 && rows <= kStageK);
 }
 __device__ __forceinline__ int up32(int v) { return (v + 31) & ~31; }
 __device__ __forceinline__ int row_tiles(int cnt) { return (cnt + kMaxTok - 1) / kMaxTok; }
@@ -350,14 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __shared__ __align__(8) uint64_t bars[kBars];
   uint64_t *full = bars, *empty = bars + kEmptyBar, *tfull = bars + kTfullBar, *tempty = bars + kTemptyBar;
   uint64_t *item_full = bars + kItemFullBar, *item_empty = bars + kItemEmptyBar, *done_bar = bars + kDoneBar;
-  uint64_t* tail = bars + kTailBar;      // [zeroing warp][stage]
+  uint64_t* tail = bars + kTailBar;      // [zeroing warp][stage], of the leading CTA
   __shared__ Seg item_slots[kItemSlots];
   __shared__ uint32_t tmem_base_s;
   __shared__ int prefix[kGrad ? 1 : kMaxExperts + 1];
   __shared__ uint8_t order_s[kMaxSorted];
   __shared__ int warp_sum[kThreads / 32], warp_max[kThreads / 32];
   __shared__ int last_flag;
-  __shared__ alignas(128) uint8_t note[kGrad ? 2 : 1][128];   // where each zeroing warp's copy goes
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
@@ -366,9 +380,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
   if (tid < kBars) {
     int count = 1;
-    if (tid < kEmptyBar) count = 2;                                  // of the leading CTA: each CTA's bytes, or zeros
+    if (tid < kEmptyBar || tid >= kTailBar) count = 2;               // of the leading CTA: each CTA's bytes, or zeros
     if (tid >= kTemptyBar && tid < kItemFullBar) count = 2 * kEpiWarps;   // of the leading CTA
-    if (tid >= kItemEmptyBar && tid < kDoneBar) count = 1 + (rank == 0 ? 1 : 0) + (kGrad ? 2 : 0) + kEpiWarps;
+    if (tid >= kItemEmptyBar && tid < kDoneBar) count = 1 + (rank == 0 ? (kGrad ? 3 : 1) : 0) + kEpiWarps;
     mbar_init(&bars[tid], count);
     fence_mbar_init();
   }
@@ -480,9 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   if (warp == 0) {
     // ----------------------------------------------------------------- loads
     // The whole warp runs the loop, one elected lane issues.  Both CTAs' bytes
-    // count on the leading CTA's barrier; a gradient's last box completes on
-    // this CTA's own, for the zeroing warp.
-    const uint32_t full0 = cluster_addr(&full[0], 0);
+    // count on barriers of the leading CTA: the stage's, or for a gradient's last
+    // box the zeroing warp's.
+    const uint32_t full0 = cluster_addr(&full[0], 0), tail0 = cluster_addr(&tail[0], 0);
     int it = 0, st = 0, ph = 0, turn = 0;
     while (ring.next(w, ok, a.status)) {
       const int half = w.cols >> 1;
@@ -495,13 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t dst = smem0 + st * stage, bar = full0 + 8 * st;
         const int here = min(subs, w.u1 - u0);
         const int left = w.rows - u0 * kStageK;            // (gradient)
-        if (kGrad && left < kStageK && (left & 15)) {
-          bar = smem_u32(&tail[turn * kMaxStages + st]);
-          mbar_arrive_expect_tx_elect(&tail[turn * kMaxStages + st], bytes);
+        if (kGrad && left <= kStageK && zeroed(a, w.rows)) {
+          bar = tail0 + 8 * (turn * kMaxStages + st);
           turn ^= 1;
-        } else {
-          mbar_arrive_expect_tx_cluster_elect(bar, here * bytes);
         }
+        mbar_arrive_expect_tx_cluster_elect(bar, here * bytes);
         for (int u = u0; u < u0 + here; ++u, dst += sub_bytes) {
           const int k0 = u * kStageK;
           if constexpr (kMode == kProduct) {
@@ -540,9 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       tc_fence_after();
       for (int u0 = w.u0; ok && u0 < w.u1; u0 += subs) {
         const int left = w.rows - u0 * kStageK;            // (gradient)
-        // (a last box was written by threads of the other CTA too)
-        ok = kGrad && left < kStageK ? mbar_wait_cluster(&full[st], ph, a.status) : mbar_wait(&full[st], ph, a.status);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&full[st], ph, a.status)))) break;
         tc_fence_after();
         // 16 of the contraction: 32 bytes on in a row, or 16 rows of 128 bytes
         constexpr int kStepA = kMnA ? 128 : 2, kStepB = kMnB ? 128 : 2;
@@ -613,42 +623,38 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
       if (++slot == kItemSlots) slot = 0, ph ^= 1, first = false;
     }
-  } else if (kGrad && (warp == kZeroWarp0 || warp == kZeroWarp1)) {
+  } else if (kGrad && rank == 0 && (warp == kZeroWarp0 || warp == kZeroWarp1)) {
     // ------------------------------------------- rows behind an expert's last
     const uint32_t full0 = cluster_addr(&full[0], 0);
-    int st = 0;
     const int mine = warp == kZeroWarp1;   // boxes are handed to the two warps in turn
-    int turn = 0;
-    uint32_t tail_ph = 0;                // of this warp's barriers: one turns when its slot holds a last box
+    int st = 0, turn = 0;
+    uint32_t tail_ph = 0;                // of this warp's barriers: one turns when its stage holds a box for it
     while (ring.next(w, ok, a.status)) {
       st = (st + w.u1 - w.u0) % n_stages;
-      const int last = w.rows % kStageK;
-      if (!(last & 15) || (kF32 && w.u1 * kStageK < w.rows)) continue;
+      if (!zeroed(a, w.rows) || (kF32 && w.u1 * kStageK < w.rows)) continue;
       turn ^= 1;
       if (turn == mine) continue;        // the other warp's: turn was its number
       // Every phase of a warp's barriers is waited for, in order.
       const int at = (st ? st : n_stages) - 1;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(&tail[mine * kMaxStages + at], (tail_ph >> at) & 1, a.status)))) break;
       tail_ph ^= 1u << at;
-      // rows last .. next multiple of 16 of the four blocks of 64 values
-      const uint32_t base = smem0 + at * stage + (lane & 7) * 16;
-      const int end = (last + 15) & ~15;
+      if (a.paced && w.rows <= kStageK)
+        for (int i = 0; i < (kF32 ? 2 : 1); ++i) fence_cluster();
+      // n rows from `last` on of the four blocks of 64 values: 16 rows where the box
+      // has them (no MMA reads the ones past n; 170 rows an expert 544 us without, 533
+      // with it), else once or twice the largest power of two, from both ends
+      const int last = w.rows % kStageK, n = -last & 15;
+      const int log = last <= kStageK - 16 ? 4 : 31 - __clz(n), h = n ? 1 << log : 0;
+      const int copies = n ? n > h ? 8 : 4 : 0;
+      const uint32_t base = smem0 + at * stage + last * 128;
+      // both CTAs' arrivals and bytes; a release, for the boxes that were waited for
+      mbar_arrive_expect_tx_elect(&full[at], copies * h * 128);
+      mbar_arrive_expect_tx_elect(&full[at], copies * h * 128);
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        for (int r = last + (lane >> 3); r < end; r += 4)
-          st_shared_v4(base + b * kBlockBytes + r * 128, 0, 0, 0, 0);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (w.u1 - w.u0 <= kPacedBoxes) {
-        if (lane == 0) mbar_arrive_release_cluster(full0 + 8 * at);
-      } else if (rank == 0) {
-        if (lane == 0) mbar_arrive(&full[at]);
-      } else {
-        // a copy that this thread starts after its fence: what it completes on
-        // the other CTA's barrier comes after the zeros
-        mbar_arrive_expect_tx_cluster_elect(full0 + 8 * at, 128);
-        tma_pair_2d_elect(smem_u32(note[mine]), &maps.b[1], 0, a.capacity, full0 + 8 * at);
-      }
+      for (int i = 0; i < 8; ++i)
+        if (i < copies)
+          tma_pair_2d_both_elect(base + (i & 3) * kBlockBytes + (i >> 2) * (n - h) * 128, &maps.b[3 + log], 0, a.capacity,
+                                 full0 + 8 * at);
     }
   } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
     // -------------------------------------------------------------- epilogue
@@ -872,12 +878,14 @@ cudaError_t expert_wgrad_launch(const ExpertWgrad& g, cudaStream_t st) {
   a.m = g.N, a.k = g.K;
   a.m_tiles = (g.N + kTileM - 1) / kTileM;
   a.n_tiles = (g.K + kMaxTok - 1) / kMaxTok;
+  a.paced = static_cast<size_t>(g.E) * g.N * g.K * (g.f32 ? 4 : 2) >= kPacedBytes;
   Maps maps{};
   if (!encode(&maps.a, g.dout, g.f16, false, g.N, g.capacity, g.ldd, 0, 0, kStageK) ||
       !encode(&maps.b[0], g.x, g.f16, false, g.K, g.capacity, g.ldx, 0, 0, kStageK) ||
-      !encode(&maps.b[1], g.x, g.f16, false, g.K, g.capacity, g.ldx, 0, 0, 1) ||
       !encode(&maps.out, g.dw, g.f16, g.f32, g.K, g.N, g.K, g.E, static_cast<long long>(g.N) * g.K, 32))
     return cudaErrorInvalidValue;
+  for (int i = 0; i < 5; ++i)
+    if (!encode(&maps.b[3 + i], g.x, g.f16, false, g.K, g.capacity, g.ldx, 0, 0, 1 << i)) return cudaErrorInvalidValue;
   if (g.f32) return g.f16 ? launch<kGradient32, true>(maps, a, st) : launch<kGradient32, false>(maps, a, st);
   return g.f16 ? launch<kGradient, true>(maps, a, st) : launch<kGradient, false>(maps, a, st);
 }

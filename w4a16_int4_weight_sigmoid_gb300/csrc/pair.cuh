@@ -20,21 +20,18 @@ __device__ __forceinline__ void cluster_sync() {
 // Its two halves, for what is needed later.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 // The cluster-wide address of a shared-memory object in the CTA of rank `r`.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t r) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(r));
   return a;
 }
-// Arrivals on a barrier of either CTA (addresses of cluster_addr).  The first
-// kind hands over TMEM that this thread has read (its loads are complete, and
-// tcgen05 fences stand on both sides), no memory; the second what its warp wrote,
-// which takes about 0.8 us.
+// An arrival on a barrier of either CTA (an address of cluster_addr) that hands
+// over TMEM that this thread has read (its loads are complete, and tcgen05 fences
+// stand on both sides), no memory.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // (relaxed: the bytes that are awaited order themselves; a release at cluster
 // scope in each stage of the load loop took 0.8 us)
@@ -46,24 +43,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster_elect(uint32_t bar
       "r"(bytes)
       : "memory");
 }
-// Waits for a phase that threads of the other CTA arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int* status,
-                                                  uint32_t polls = kWaitPolls) {
-  for (uint32_t i = 0; i < polls; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
-  set_status(status, CHORD_ERR_TIMEOUT);
-  return false;
-}
-
 // TMEM of both CTAs: one warp of each calls these.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
@@ -155,6 +134,18 @@ __device__ __forceinline__ void tma_pair_2d_elect(uint32_t dst, const CUtensorMa
       "elect.sync r|e, 0xffffffff;\n\t"
       "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
       "{%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+// The same box to the same place of both CTAs; the bytes of both complete on `bar`.
+__device__ __forceinline__ void tma_pair_2d_both_elect(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                                       uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t.reg .b16 m;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "mov.b16 m, 3;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+      ".cta_group::2 [%0], [%1, {%2, %3}], [%4], m;\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
