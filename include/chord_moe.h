@@ -585,6 +585,8 @@ int chord_mxfp8_permute(const uint8_t* codes, const uint8_t* scales, const int32
  *             both NULL for none.  backward: read in the place of gu, which is
  *             NULL then.  I % 32 == 0 and codes 16-byte aligned with them, any
  *             I without
+ * At gates of +inf and -inf silu and silu' are their limits (inf and 1, 0 and
+ * 0); a NaN gate gives NaN.
  *   *_stride  row strides in elements, as for chord_moe_permute
  * Results are the same from call to call.  topk <= 32.
  */

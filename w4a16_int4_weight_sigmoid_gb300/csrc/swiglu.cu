@@ -17,6 +17,7 @@
 // backward 59 against 84 and, with 32 bytes, 64).  What a pass moves then goes
 // at 5.7 to 6.0 TB/s of the 6.8 of a copy; loading a step ahead, or half the
 // instructions (two values in one FP32 operation), changed nothing.
+#include <cfloat>
 #include <utility>
 
 #include "kernels.h"
@@ -44,7 +45,8 @@ struct SwigluArgs {
 // Two gates: silu(g) = max(g, 0) - |g| t / (1 + t) with t = exp(-|g|), which
 // loses no digits on either side, and sigmoid(g).  For 16-bit types t is the
 // square of exp2(-|g| log2(e) / 2), which stays a normal number where t does
-// not, and the fast reciprocal's operand lies in [1, 2].
+// not, and the fast reciprocal's operand lies in [1, 2].  At the ends silu has its
+// limits, infinity and 0: the |g| that t = 0 multiplies is a number there.
 template <bool kPrecise>
 __device__ __forceinline__ void gates(float2 g, float2& silu, float2& s) {
   const float2 size = make_float2(fabsf(g.x), fabsf(g.y));
@@ -62,7 +64,8 @@ __device__ __forceinline__ void gates(float2 g, float2& silu, float2& s) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d.y) : "f"(d.y));
   }
   const float2 q = mul2(t, d);                              // sigmoid(-|g|)
-  silu = fma2(make_float2(-size.x, -size.y), q, make_float2(fmaxf(g.x, 0.f), fmaxf(g.y, 0.f)));
+  silu = fma2(make_float2(-fminf(size.x, FLT_MAX), -fminf(size.y, FLT_MAX)), q,
+              make_float2(fmaxf(g.x, 0.f), fmaxf(g.y, 0.f)));
   s = make_float2(g.x < 0.f ? q.x : d.x, g.y < 0.f ? q.y : d.y);
 }
 // Values i and i + 1 of an array of kN (one: 0 for the second).
@@ -210,8 +213,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) swiglu_backward_kernel(SwigluA
             float2 silu, s;
             gates<sizeof(T) == 4>(two(fg, j), silu, s);
             const float2 act = mul2(silu, up), wd = mul2(ww, d);
-            // 1 - s is off by 2^-25, silu times that by less than the slope's own rounding times |gate|
-            const float2 slope = fma2(silu, make_float2(1.f - s.x, 1.f - s.y), s);
+            // 1 - s is off by 2^-25, silu times that by less than the slope's own rounding times |gate|; it is 0
+            // from a gate of 18 on, where silu's size does not matter (but for an infinity)
+            const float2 slope =
+                fma2(make_float2(fminf(silu.x, 64.f), fminf(silu.y, 64.f)), make_float2(1.f - s.x, 1.f - s.y), s);
             sum = fma2(d, act, sum);
             set(oh, j, mul2(ww, act));
             set(fg, j, mul2(mul2(wd, up), slope));
