@@ -1,5 +1,5 @@
 """The gated activation at the ends of the range: infinities, NaN and the largest values in rows
-that hold assignments."""
+that hold assignments, and the forward pass's rows made again."""
 import pytest
 import torch
 
@@ -7,7 +7,7 @@ from w4a16_int4_weight_sigmoid_gb300 import chord
 from w4a16_int4_weight_sigmoid_gb300.layer import ExpertOrder
 
 from gpu_util import ensure_lib
-from test_gpu_swiglu import BF16, FP16, FP32
+from test_gpu_swiglu import BF16, FP16, FP32, case
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +75,30 @@ def test_an_infinite_gate_while_rows_are_kept():
     assert again[at[0], :32].isnan().all() and torch.equal(again[at[0], 32:], h[at[0], 32:])
     assert dgu[at[0], :32].isnan().all() and torch.isfinite(dgu[at[0], 32:64]).all()
     assert torch.isfinite(dgu[at[1]]).all() and dw[0, 0].isnan() and torch.isfinite(dw[1, 0])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("I", [64, 333])
+def test_the_rows_made_again_are_the_forward_pass_s(I, dtype):
+    """Bit for bit, from whole rows and from what 8 bits hold of them."""
+    order, gu, dh, _, filled, _ = case(60, 12, 5, 3, 16, I, dtype)
+    gu[~filled], dh[~filled] = 0, 0
+    w = order.topk_weights
+    h, again, *_ = passes(order, gu, dh, w)
+    assert torch.equal(h, again)
+    if I % 32 or dtype == FP16:      # (FP16 rounds the largest values that 8 bits hold)
+        return
+    _, again, _, _, kept = passes(order, gu, dh, w, keep=True)
+    values = torch.zeros_like(gu)
+    chord.chord_mxfp8_dequantize(*kept, values)
+    assert torch.equal(passes(order, values, dh, w)[0], again)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_products_past_the_range_on_the_way(dtype):
+    """w silu(gate) up is a number where silu(gate) up is past FP32: in both passes."""
+    order = ExpertOrder(1, 1, 0, 1, 8).route(torch.zeros(1, 1, device="cuda"), torch.zeros(1, device="cuda"))
+    gu = torch.full((order.capacity, 64), 2.0 ** 70, dtype=dtype, device="cuda")
+    h, again, *_ = passes(order, gu, torch.ones_like(gu[:, :32]), torch.full((1, 1), 2.0 ** -60, device="cuda"))
+    at = order.sorted_positions.long()
+    assert (h[at] == 2.0 ** 80).all() and (again[at] == 2.0 ** 80).all()

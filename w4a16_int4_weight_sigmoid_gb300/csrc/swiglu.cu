@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) swiglu_backward_kernel(SwigluA
             const float2 slope =
                 fma2(make_float2(fminf(silu.x, 64.f), fminf(silu.y, 64.f)), make_float2(1.f - s.x, 1.f - s.y), s);
             sum = fma2(d, act, sum);
-            set(oh, j, mul2(ww, act));
+            set(oh, j, mul2(mul2(silu, ww), up));       // as in the forward pass, whose bits it has
             set(fg, j, mul2(mul2(wd, up), slope));
             set(fu, j, mul2(wd, silu));
           }
