@@ -286,12 +286,15 @@ class _ExpertMLP(torch.autograd.Function):
         chord.chord_swiglu(gu, weights, o.sorted_token_ids, o.num_tokens_post_padded, h, *kept)
         y = products.rows(h, w2)
         chord.chord_moe_permute_backward(y, o.sorted_positions, o.topk, out)   # the sum over a token's rows
-        if held:
-            x8 = codes8(M, H)
-            chord.chord_mxfp8_quantize(x, *x8)
-            kept = (*x8, *kept)
-        else:
-            kept = (x, gu)
+        if not held:
+            kept = (gu,)
+        if ctx.needs_input_grad[2]:   # (x is needed for w13's gradient alone)
+            if held:
+                x8 = codes8(M, H)
+                chord.chord_mxfp8_quantize(x, *x8)
+                kept = (*kept, *x8)
+            else:
+                kept = (gu, x)
         ctx.held, ctx.topk, ctx.cap, ctx.status, ctx.dtype = held, o.topk, cap, o.dev_status, x.dtype
         ctx.save_for_backward(weights, w13, w2, *o._saved(o.sorted_positions, o.sorted_token_ids,
                                                          o.num_tokens_post_padded, o.expert_counts, o.expert_offsets),
@@ -305,10 +308,11 @@ class _ExpertMLP(torch.autograd.Function):
         M, (twoI, H) = dout.shape[0], w13.shape[1:]
         empty = lambda *shape: torch.empty(shape, dtype=ctx.dtype, device=dout.device)
         products = _Products(counts, offsets, ctx.status)
-        dy, dgu, h, dweights = empty(ctx.cap, H), empty(ctx.cap, twoI), empty(ctx.cap, twoI // 2), torch.empty_like(weights)
+        dy, dgu, dweights = empty(ctx.cap, H), empty(ctx.cap, twoI), torch.empty_like(weights)
+        h = empty(ctx.cap, twoI // 2) if ctx.needs_input_grad[3] else None
         chord.chord_moe_permute(_unit_columns(dout), positions, token_ids, total, ctx.topk, dy)
         dh = products.rows(dy, w2, True)
-        gu, codes = (None, kept[2:]) if ctx.held else (kept[1], (None, None))
+        gu, codes, kept_x = (None, kept[:2], kept[2:]) if ctx.held else (kept[0], (None, None), kept[1:])
         chord.chord_swiglu_backward(dh, gu, *codes, weights, positions, token_ids, total, dgu, dweights, h)
         dx = dw13 = dw2 = None
         if ctx.needs_input_grad[3]:
@@ -316,9 +320,9 @@ class _ExpertMLP(torch.autograd.Function):
         if ctx.needs_input_grad[2]:
             rows = dy   # (used up)
             if ctx.held:
-                chord.chord_mxfp8_permute(*kept[:2], positions, token_ids, total, ctx.topk, rows)
+                chord.chord_mxfp8_permute(*kept_x, positions, token_ids, total, ctx.topk, rows)
             else:
-                chord.chord_moe_permute(kept[0], positions, token_ids, total, ctx.topk, rows)
+                chord.chord_moe_permute(*kept_x, positions, token_ids, total, ctx.topk, rows)
             dw13 = products.weights(dgu, rows, w13)
         if ctx.needs_input_grad[0]:
             dx = empty(M, H)
@@ -332,7 +336,7 @@ def expert_mlp(x, weights, w13, w2, order: ExpertOrder, held_in_8_bits: bool = T
     assignment (t, j) where it is local.  w13 [E_local, 2I, H] (rows 0..I-1 gate) and w2 [E_local, H, I]; x, w13 and
     w2 BF16 or FP16, H and I multiples of 8.  Differentiable once in x, weights, w13 and w2.
 
-    The backward pass keeps x and the rows of gate and up: in 8 bits (MXFP8; H and I multiples of 32), which costs
+    The backward pass keeps the rows of gate and up, and x where w13 needs a gradient: in 8 bits (MXFP8; H and I multiples of 32), which costs
     the gradients of the weights and of the activation a relative rounding of up to 2^-4 per kept value, or as they
     are.  The output is the same either way."""
     if x.shape[0] != order.M or w13.shape[0] != order.E_local or w2.shape[0] != order.E_local:
@@ -345,7 +349,9 @@ def expert_mlp(x, weights, w13, w2, order: ExpertOrder, held_in_8_bits: bool = T
         raise ValueError(f"weights must be [{order.M}, {order.topk}], got {list(weights.shape)}")
     if held_in_8_bits and (x.shape[1] % 32 or w2.shape[2] % 32):
         raise ValueError(f"H={x.shape[1]} and I={w2.shape[2]} must be multiples of 32 to be held in 8 bits")
-    return _ExpertMLP.apply(_unit_columns(x), weights.contiguous(), w13, w2, order, held_in_8_bits)
+    # nothing is kept, and nothing quantised, where no gradient can follow
+    held = held_in_8_bits and torch.is_grad_enabled() and any(t.requires_grad for t in (x, weights, w13, w2))
+    return _ExpertMLP.apply(_unit_columns(x), weights.contiguous(), w13, w2, order, held)
 
 
 def quantize_mxfp4(w, stream=None):
