@@ -112,20 +112,32 @@ void* stream(PyObject* o) {
   return reinterpret_cast<void*>(integer(o));
 }
 
+// Tensors that a kernel launched now may use: on the current device.
+template <typename... O>
+void here(O... objects) {
+  const int device = c10::cuda::current_device();
+  for (PyObject* o : {objects...})
+    if (o != Py_None && THPVariable_Check(o) && THPVariable_Unpack(o).get_device() != device)
+      raise(PyExc_ValueError, "all tensors must be on the current device (cuda:%d)", device);
+}
+
 int permute(PyObject* const* a) {
   const Rows x(a[0], "x"), out(a[5], "out", x);
   const int k = narrow(integer(a[4]), "topk"), M = narrow(x.n, "tokens");
-  return chord_moe_permute(x.p, x.dtype, x.stride, ints(a[1], x.n * k, "sorted_positions"),
-                           ints(a[2], out.n, "sorted_token_ids"), ints(a[3], 1, "num_tokens_post_padded"), M, k,
-                           narrow(x.h, "row length"), out.n, out.p, out.stride, stream(a[6]));
+  const int32_t *pos = ints(a[1], x.n * k, "sorted_positions"), *sorted = ints(a[2], out.n, "sorted_token_ids");
+  const int32_t* total = ints(a[3], 1, "num_tokens_post_padded");
+  here(a[0], a[1], a[2], a[3], a[5]);
+  return chord_moe_permute(x.p, x.dtype, x.stride, pos, sorted, total, M, k, narrow(x.h, "row length"), out.n, out.p,
+                           out.stride, stream(a[6]));
 }
 
 int permute_backward(PyObject* const* a) {
   const Rows dout(a[0], "dout"), dx(a[3], "dx", dout);
   const int k = narrow(integer(a[2]), "topk");
-  return chord_moe_permute_backward(dout.p, dout.dtype, dout.stride, ints(a[1], dx.n * k, "sorted_positions"),
-                                    narrow(dx.n, "tokens"), k, narrow(dx.h, "row length"), dout.n, dx.p, dx.stride,
-                                    stream(a[4]));
+  const int32_t* pos = ints(a[1], dx.n * k, "sorted_positions");
+  here(a[0], a[1], a[3]);
+  return chord_moe_permute_backward(dout.p, dout.dtype, dout.stride, pos, narrow(dx.n, "tokens"), k,
+                                    narrow(dx.h, "row length"), dout.n, dx.p, dx.stride, stream(a[4]));
 }
 
 int unpermute(PyObject* const* a) {
@@ -133,8 +145,10 @@ int unpermute(PyObject* const* a) {
   const Rows y(a[0], "y");
   const float* w = weights(a[1], M, k);
   const Rows out(a[3], "out", y, M);
-  return chord_moe_unpermute(y.p, y.dtype, y.stride, w, ints(a[2], M * k, "sorted_positions"), narrow(M, "tokens"),
-                             narrow(k, "topk"), narrow(y.h, "row length"), y.n, out.p, out.stride, stream(a[4]));
+  const int32_t* pos = ints(a[2], M * k, "sorted_positions");
+  here(a[0], a[1], a[2], a[3]);
+  return chord_moe_unpermute(y.p, y.dtype, y.stride, w, pos, narrow(M, "tokens"), narrow(k, "topk"),
+                             narrow(y.h, "row length"), y.n, out.p, out.stride, stream(a[4]));
 }
 
 int unpermute_backward(PyObject* const* a) {
@@ -142,11 +156,13 @@ int unpermute_backward(PyObject* const* a) {
   const float* w = weights(a[2], M, k);
   const Rows dout(a[0], "dout"), y(a[1], "y", dout), dy(a[6], "dy", dout, y.n);
   if (dout.n != M) raise(PyExc_ValueError, "dout has %lld rows, need %lld", (long long)dout.n, (long long)M);
-  return chord_moe_unpermute_backward(
-      dout.p, y.p, dout.dtype, dout.stride, y.stride, w, ints(a[3], M * k, "sorted_positions"),
-      ints(a[4], y.n, "sorted_token_ids"), ints(a[5], 1, "num_tokens_post_padded"), narrow(M, "tokens"),
-      narrow(k, "topk"), narrow(y.h, "row length"), y.n, dy.p, dy.stride,
-      values<float>(a[7], at::kFloat, M * k, "dweights"), stream(a[8]));
+  const int32_t *pos = ints(a[3], M * k, "sorted_positions"), *sorted = ints(a[4], y.n, "sorted_token_ids");
+  const int32_t* total = ints(a[5], 1, "num_tokens_post_padded");
+  float* dw = values<float>(a[7], at::kFloat, M * k, "dweights");
+  here(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
+  return chord_moe_unpermute_backward(dout.p, y.p, dout.dtype, dout.stride, y.stride, w, pos, sorted, total,
+                                      narrow(M, "tokens"), narrow(k, "topk"), narrow(y.h, "row length"), y.n, dy.p,
+                                      dy.stride, dw, stream(a[8]));
 }
 
 int quantize(PyObject* const* a) {
@@ -189,15 +205,6 @@ int moe_gemm(PyObject* const* a) {
   return chord_mxfp4_moe_gemm(rows, numel(a[0]), packed, E, N, K, ints(a[5], E, "expert_counts"),
                               ints(a[6], E + 1LL, "expert_offsets"), capacity, epilogue,
                               static_cast<chord_bf16*>(C.data_ptr()), ws, numel(a[10]), status, stream(a[12]));
-}
-
-// Tensors that a kernel launched now may use: on the current device.
-template <typename... O>
-void here(O... objects) {
-  const int device = c10::cuda::current_device();
-  for (PyObject* o : {objects...})
-    if (o != Py_None && THPVariable_Check(o) && THPVariable_Unpack(o).get_device() != device)
-      raise(PyExc_ValueError, "all tensors must be on the current device (cuda:%d)", device);
 }
 
 int expert_gemm(PyObject* const* a) {
