@@ -108,12 +108,14 @@ constexpr int kOutPitch = 80;
 template <Mode kMode>
 constexpr int kOutBytes = is_gradient(kMode) ? 32 * 128 : 32 * kOutPitch;
 constexpr int kStageBudget = 6 * stage_bytes(kMaxTok);
-// The tensor cores cut their sums off toward zero, once for each 16 of the
-// contraction: over n rows a gradient's FP32 sums come out about 1e-9 n too
-// small (measured: 4e-6 at 4096 rows, 2e-5 at 16384, where FP32 sums in another
-// order have 3e-7).  An FP32 gradient is therefore added up, rounding to
-// nearest, from parts of at most this many boxes (768 rows: 8e-7); in 16 bits
-// the result's own rounding is 25 times 2e-5.
+// The tensor cores cut products off toward zero where they enter a sum, about two
+// bits below FP32's last place: n products of one sign come out up to n 2^-26 too
+// small (FP16 6.4e-9 n, at worst 9.3e-9 n; BF16, whose products have fewer bits,
+// 1e-9 n at 16384 and 6e-9 n at 2^20), products of both signs far less.  An FP32
+// gradient is therefore added up, rounding to nearest, from parts of at most this
+// many boxes (768 rows: 4.2e-6 in FP16 and 3.5e-7 in BF16 for one sign, where one
+// sum of 16384 rows is 1e-4 and 1.9e-5 off).  In 16 bits the result's own rounding is
+// larger up to n = 2^15 (FP16, 2^-11) and 2^18 (BF16, 2^-8) at the least.
 constexpr int kExactBoxes = 12;
 template <Mode kMode>
 constexpr int kSmemBytes = kStageBudget + kEpiWarps * kOutBytes<kMode> + 1024;
