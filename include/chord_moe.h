@@ -556,7 +556,8 @@ int chord_expert_wgrad(const void* dout, const void* x, int dtype, int64_t dout_
  *               that nothing saturates; code = x / scale rounded to the
  *               nearest E4M3 value, ties to even (at s = 247, whose 256 is
  *               past FP32, to at most 240).  A block that holds an infinity or
- *               a NaN gets s = 255 and codes 0, and reads as NaN.
+ *               a NaN gets s = 255 and codes 0, and reads as NaN.  A value v
+ *               is off by up to 2^-4 |v|, or 2^-10 of its scale where that is more.
  *               x [rows, K] of `dtype`, codes [rows, K], scales [rows, K/32]
  *   dequantize  the inverse: out [rows, K] of `dtype`, rounded once (FP16: to
  *               at most 65504)

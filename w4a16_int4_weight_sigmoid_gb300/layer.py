@@ -336,9 +336,11 @@ def expert_mlp(x, weights, w13, w2, order: ExpertOrder, held_in_8_bits: bool = T
     assignment (t, j) where it is local.  w13 [E_local, 2I, H] (rows 0..I-1 gate) and w2 [E_local, H, I]; x, w13 and
     w2 BF16 or FP16, H and I multiples of 8.  Differentiable once in x, weights, w13 and w2.
 
-    The backward pass keeps the rows of gate and up, and x where w13 needs a gradient: in 8 bits (MXFP8; H and I multiples of 32), which costs
-    the gradients of the weights and of the activation a relative rounding of up to 2^-4 per kept value, or as they
-    are.  The output is the same either way."""
+    The backward pass keeps the rows of gate and up, and x where w13 needs a gradient.  By default it keeps them in 8
+    bits (MXFP8; H and I multiples of 32): the gradients of the weights and of the activation then see each kept value
+    v rounded by up to 2^-4 |v|, or 2^-10 of its block's scale where that is more.  A block is 32 neighbours in a row,
+    its scale at most 1/224 of the largest of them, so that values below about 2^-18 of that are kept as 0.
+    held_in_8_bits=False keeps them as they are.  The output is the same either way."""
     if x.shape[0] != order.M or w13.shape[0] != order.E_local or w2.shape[0] != order.E_local:
         raise ValueError(f"x must hold the order's {order.M} tokens and w13 and w2 its {order.E_local} experts, got "
                          f"{x.shape[0]}, {w13.shape[0]} and {w2.shape[0]}")
