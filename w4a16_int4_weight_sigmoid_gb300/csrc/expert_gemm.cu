@@ -723,8 +723,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         load(width * t);
         if (kF32 && w.u0 > 0 && lane == 0) bulk_wait_all();   // the item's parts before are there to be added to
         // dW passes through L2 once (left to it, the lines went to DRAM in an
-        // order that took 480 us where this takes 436: 48 experts of 4096 x 7168,
-        // 43 rows each); parts are added to where they lie
+        // order that took 452 us where this takes 431: 48 experts of 4096 x 7168,
+        // 43 rows each; 128 MB 28.8 / 25.0, 64 MB 15.7 / 14.8).  A dW that fits in
+        // L2 and is read at once comes back more slowly: the call and a sum over
+        // 64 MB 28.7 us left to L2, 30.8 here; 256 MB 126.5 / 123.9.  Parts are
+        // added to where they lie
         const uint64_t policy = kF32 && w.u1 * kStageK < w.rows ? policy_evict_normal() : policy_evict_first();
 #pragma unroll 1
         for (int c0 = width * t; c0 < w.cols; c0 += 2 * width) {

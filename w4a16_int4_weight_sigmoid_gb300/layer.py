@@ -265,7 +265,10 @@ class _ExpertProduct(torch.autograd.Function):
 
 def expert_product(rows, w, order: ExpertOrder):
     """rows [order.capacity, K] times each expert's w [E_local, N, K] -> [order.capacity, N], zeros in rows that
-    are no expert's; BF16 or FP16, differentiable once in rows and w."""
+    are no expert's; BF16 or FP16, differentiable once in rows and w.
+
+    What the products find wrong on the device (counts that are no order of the rows, a wait that ran out) is recorded
+    in order.dev_status; rows and gradients are then not computed, and hold zeros or anything."""
     if rows.shape[0] != order.capacity or w.shape[0] != order.E_local:
         raise ValueError(f"rows must hold the {order.capacity} rows of the order and w its {order.E_local} experts, "
                          f"got {rows.shape[0]} and {w.shape[0]}")
@@ -340,7 +343,10 @@ def expert_mlp(x, weights, w13, w2, order: ExpertOrder, held_in_8_bits: bool = T
     bits (MXFP8; H and I multiples of 32): the gradients of the weights and of the activation then see each kept value
     v rounded by up to 2^-4 |v|, or 2^-10 of its block's scale where that is more.  A block is 32 neighbours in a row,
     its scale at most 1/224 of the largest of them, so that values below about 2^-18 of that are kept as 0.
-    held_in_8_bits=False keeps them as they are.  The output is the same either way."""
+    held_in_8_bits=False keeps them as they are.  The output is the same either way.
+
+    Errors on the device are recorded in order.dev_status, as for expert_product: a program that can wait reads it,
+    after the backward pass too, before it trusts what it got."""
     if x.shape[0] != order.M or w13.shape[0] != order.E_local or w2.shape[0] != order.E_local:
         raise ValueError(f"x must hold the order's {order.M} tokens and w13 and w2 its {order.E_local} experts, got "
                          f"{x.shape[0]}, {w13.shape[0]} and {w2.shape[0]}")
