@@ -272,8 +272,8 @@ def test_no_rows_at_all():
         check_wgrad([0, 0, 0], 64, 72, BF16, BF16, extra=extra)
 
 
-# the items of a last round that would leave half of the clusters idle are divided: few items in all, few behind
-# whole rounds, one, edges that leave a slice nothing
+# last rounds that leave most of the clusters idle: few items in all, few behind whole rounds, one, edges of a tile
+# that hold next to nothing
 @pytest.mark.parametrize("counts,K,N", [
     ([200], 136, 264), ([256] * 3, 64, 512), ([255] * 20, 72, 1024), ([90] * 77, 64, 200), ([33, 250, 100], 328, 2056),
     ([129], 1000, 8), ([70], 8, 520), ([1024], 264, 264),
